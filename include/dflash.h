@@ -59,6 +59,7 @@ typedef enum { DFLASH_F32 = 0, DFLASH_BF16 = 1, DFLASH_FP8_E4M3 = 2 } dflash_dty
 #define DFLASH_DEV_CROP      4u  /* crop to a negative length or beyond the current one */
 #define DFLASH_DEV_ROWS      8u  /* cu_rows not non-decreasing or beyond M */
 #define DFLASH_DEV_TIMEOUT  16u  /* an internal pipeline wait gave up (kernel returned early) */
+#define DFLASH_DEV_PAGE     32u  /* a page id or a slot outside the cache: not read, not written */
 
 /*
  * Model dimensions.
@@ -327,6 +328,140 @@ dflash_status dflash_accept(const int32_t* block_ids, const int32_t* posterior, 
                             int32_t* ctx_next, int32_t* next_anchor, cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The chunk step: new rows of many sequences through a cache, causally.
+ *
+ * The draft path above projects a block itself and attends without a mask. A model that
+ * runs over new tokens in order (the target verifying a drafted block, a prompt's chunk,
+ * one token per sequence) needs the same cache with its own projections and a causal
+ * mask: one map per step, then an append and an attention per layer.
+ *
+ *   map     lengths + new row counts -> pages, slots, positions, lengths after the step
+ *   append  QK-norm, RoPE, K and V rows into their slots
+ *   attn    softmax(q K^T scaling) V, row at position p over the keys at positions <= p
+ *
+ * (KV Cache + Speculative Decoding Interview Cheat Sheet, section 5: a sequence's logical
+ * rows live in fixed-size pages behind a block table; section 3: verification and chunked
+ * prefill run several rows of a sequence at once. DFlash KV Injection Walkthrough, Steps
+ * 4.1-4.4 for the norm, the rotation and the head layout, Step 6 for the verified block.)
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * The rows of one step, grouped by sequence: rows cu_rows[b] .. cu_rows[b+1]-1 are the new
+ * rows of sequence b, in order. All device memory owned by the caller, 4-byte aligned.
+ *   cu_rows    int32 [batch + 1], cu_rows[0] = 0, non-decreasing, cu_rows[batch] <= rows.
+ *              Rows cu_rows[batch] .. rows-1 are padding (a captured step of fixed size):
+ *              no call reads or writes anything of theirs but their slot and position
+ *   kv_lens    int32 [batch]: rows sequence b holds once the step's rows are in, 0 for a
+ *              refused sequence. The last new row of b is at position kv_lens[b] - 1
+ *   slots      int32 [rows]: where a row's K and V go: page * 128 + row of the page (paged)
+ *              or b * capacity + position (contiguous); -1 for padding and refused rows
+ *   positions  int32 [rows]: a row's position; -1 as for slots
+ *   batch, rows  sequences (at most 8192) and rows of the arrays
+ */
+typedef struct {
+  const int32_t* cu_rows;
+  int32_t* kv_lens;
+  int32_t* slots;
+  int32_t* positions;
+  int batch, rows;
+} dflash_chunk;
+
+/*
+ * The page allocation of a paged cache, all device memory (4-byte aligned) but n_free.
+ *   block_table     the cache's block_table, as the pointer through which new pages are
+ *                   entered
+ *   pages_held      int32 [batch]: pages sequence b holds: entries 0 .. pages_held[b]-1 of
+ *                   its row of the table (a crop keeps them)
+ *   pages_held_out  int32 [batch], may be pages_held
+ *   free_pages      int32 [n_free]: ids of free pages; entries from *taken on are free
+ *   taken           int32 [1]; taken_out int32 [1], may be taken
+ */
+typedef struct {
+  int32_t* block_table;
+  const int32_t* pages_held;
+  int32_t* pages_held_out;
+  const int32_t* free_pages;
+  int n_free;
+  const int32_t* taken;
+  int32_t* taken_out;
+} dflash_page_pool;
+
+/*
+ * Plans a step. For every sequence b with n = cu_rows[b+1] - cu_rows[b] new rows and
+ * len = cache->lens[layer][b]:
+ *   kv_lens[b] = len + n; the pages that ceil((len + n) / 128) needs beyond pages_held[b]
+ *   are taken from free_pages, in the order of the sequences, and entered in its row of
+ *   the block table; its rows get their slots and positions len .. len + n - 1.
+ * Refused, with nothing taken, kv_lens 0, slots and positions -1, its table row and pages
+ * held unchanged: a sequence that would outgrow the capacity, whose rows are not a
+ * valid range (DFLASH_DEV_ROWS), or that needs pages when the free list no longer holds
+ * those of all such sequences up to it (once it is short, every later sequence that needs
+ * a page is refused too). Capacity and pages set DFLASH_DEV_CAPACITY. A page id outside
+ * [0, n_pages) sets DFLASH_DEV_PAGE and gives its rows slot -1.
+ * A contiguous cache has no pages: pool may be NULL. The lengths of the cache are read,
+ * not changed; dflash_chunk_append sets them layer by layer. Calling again with the same
+ * inputs (separate _out arrays) writes the same results.
+ * Host errors: null or misaligned pointers, chunk->batch != cache->batch, a pool whose
+ * block_table is not the cache's, negative sizes, a cache of more than 2^31 - 1 slots.
+ */
+dflash_status dflash_chunk_map(const dflash_kv_cache* cache, int layer, const dflash_chunk* chunk,
+                               const dflash_page_pool* pool, cudaStream_t stream);
+
+/*
+ * Stores a step's rows in one layer of the cache. Row r, with slot s = slots[r] >= 0 and
+ * position p = positions[r]:
+ *   q_out[r] = RoPE_p(RMSNorm_{gamma_q}(q[r]))   per head
+ *   K at s   = RoPE_p(RMSNorm_{gamma_k}(k[r]))   per head, in the cache's element type
+ *   V at s   = v[r]
+ * then lens[layer][b] = kv_lens[b] for every sequence with kv_lens[b] > 0. Rows with slot
+ * -1 are skipped, their q_out left as it was.
+ *   q, k, v        device rows of n_h * d_h, n_kv * d_h, n_kv * d_h elements of dims->dtype,
+ *                  consecutive rows ld_q, ld_k, ld_v elements apart (at least the row;
+ *                  slices of a fused projection's rows are fine). bf16: 16-byte aligned,
+ *                  strides multiples of 8. q may be NULL (K and V only; q_out NULL)
+ *   gamma_q, gamma_k  device [d_h], or NULL: no norm
+ *   rope_table     device table of dflash_rope_table_build, table_len positions, or NULL
+ *                  (table_len 0): no rotation
+ *   q_out          device [rows][n_h * d_h]; may be q when ld_q = n_h * d_h
+ * A slot beyond the cache sets DFLASH_DEV_PAGE, a position beyond the table DFLASH_DEV_ROPE:
+ * the row is skipped; a sequence that reaches beyond the table keeps its length. Two rows
+ * with the same slot: either one is stored.
+ */
+dflash_status dflash_chunk_append(const dflash_dims* dims, const dflash_kv_cache* cache, int layer,
+                                  const dflash_chunk* chunk, const void* q, long long ld_q,
+                                  const void* k, long long ld_k, const void* v, long long ld_v,
+                                  const void* gamma_q, const void* gamma_k,
+                                  const float* rope_table, int table_len, void* q_out,
+                                  cudaStream_t stream);
+
+/*
+ * Causal attention of a step's rows over one layer of the cache. Row i (from 0) of the n new
+ * rows of sequence b is at p = kv_lens[b] - n + i and sees the cached rows j <= p, with a
+ * sliding window W > 0 those with p - j < W:
+ *   out = softmax(q K^T * scaling) V, query head h reading KV head h / G (G = n_h / n_kv)
+ * A row that sees no key (a refused sequence; p < 0) is zero. What the cache holds at rows a
+ * query does not see never reaches it, NaN and infinity included. Rows of padding are left as they were.
+ *   q      device rows of n_h * d_h elements, ld_q elements apart (at least the row; a
+ *          multiple of 8 for bf16); 16-byte aligned
+ *   sliding_window  0 = none; scaling  <= 0 selects d_h^-0.5
+ *   out    device [rows][n_h * d_h], 16-byte aligned, not overlapping q
+ *   workspace  dflash_chunk_workspace_bytes(dims) bytes, 256-byte aligned, of the calls that
+ *          run one after another: two calls that may run at the same time (other streams,
+ *          graphs replayed side by side) need one each
+ * Reads chunk->cu_rows and kv_lens, not slots or positions. kv_lens[b] outside
+ * [0, capacity] sets DFLASH_DEV_CAPACITY and the rows are zero; rows that are not a valid
+ * range set DFLASH_DEV_ROWS and are skipped; a page id outside the pool sets
+ * DFLASH_DEV_PAGE and reads as zeros.
+ */
+size_t dflash_chunk_workspace_bytes(const dflash_dims* dims);
+dflash_status dflash_chunk_attn(const dflash_dims* dims, const dflash_kv_cache* cache, int layer,
+                                const dflash_chunk* chunk, const void* q, long long ld_q,
+                                int sliding_window, float scaling, void* out, void* workspace,
+                                size_t ws_bytes, cudaStream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the current device's sticky
  * status word into *device_status (a mask of DFLASH_DEV_* bits). Returns
  * DFLASH_OK when the word was zero, DFLASH_ERR_DEVICE when not, and
@@ -351,6 +486,10 @@ const char* dflash_status_string(dflash_status s);
 #define DFLASH_KERNEL_ROPE_TABLE    8  /* RoPE table fill */
 #define DFLASH_KERNEL_SCHEDULE      9  /* attention work list */
 #define DFLASH_KERNEL_ACCEPT       10  /* acceptance bookkeeping */
+#define DFLASH_KERNEL_CHUNK_MAP    11  /* pages, slots and positions of a chunk step */
+#define DFLASH_KERNEL_CHUNK_APPEND 12  /* a step's norm, RoPE and cache rows */
+#define DFLASH_KERNEL_CHUNK_ATTN   13  /* causal attention of a step's rows */
+#define DFLASH_KERNEL_CHUNK_MERGE  14  /* merge of its split ranges */
 
 /*
  * Starts recording a CUDA event pair around every launch whose kind bit

@@ -886,6 +886,8 @@ __global__ void attn_combine_kernel(AttnTcParams p, const int* merge_list, const
   }
 }
 
+}  // namespace
+
 int sm_count() {
   static std::mutex mu;
   static int count[128] = {};
@@ -900,6 +902,8 @@ int sm_count() {
   }
   return count[dev];
 }
+
+namespace {
 
 template <bool NARROW, bool FP8>
 cudaError_t launch_attn(const AttnTcParams& p, int grid, cudaStream_t s) {

@@ -1,0 +1,326 @@
+// The chunk step (map, append, causal attention): parameters of its kernels, and the work
+// split that both attention kernels and their merge share.
+#pragma once
+
+#include "dflash_internal.cuh"
+
+namespace dflash {
+
+constexpr int kChunkMaxBatch = 8192;  // sequences of a step (prefix sums live in shared memory)
+
+struct ChunkMapParams {
+  const int32_t* cu_rows;
+  const int32_t* lens;
+  int32_t* kv_lens;
+  int32_t* slots;
+  int32_t* positions;
+  // paged: the pool (null otherwise)
+  int32_t* table;
+  const int32_t* held;
+  int32_t* held_out;
+  const int32_t* free_pages;
+  const int32_t* taken;
+  int32_t* taken_out;
+  unsigned* status;
+  int batch, rows, capacity, pages_per_seq, n_pages, n_free;
+  bool paged;
+};
+cudaError_t chunk_map(const ChunkMapParams& p, cudaStream_t s);
+
+struct ChunkAppendParams {
+  const int32_t* slots;
+  const int32_t* positions;
+  const int32_t* kv_lens;
+  int32_t* lens;          // this layer's
+  const void* q;          // or null
+  const void* k;
+  const void* v;
+  long long ld_q, ld_k, ld_v;
+  const void* gamma_q;    // or null: no norm
+  const void* gamma_k;
+  const float2* rope;     // or null: no rotation
+  void* q_out;
+  void* cache_k;          // layer base: units of [n_kv][unit_rows][d_h] (a page, or a sequence)
+  void* cache_v;
+  unsigned* status;
+  long long n_slots;      // units * unit_rows
+  int unit_rows;
+  int batch, rows, capacity, n_h, n_kv, d_h, table_len;
+  float eps, k_scale, v_scale;
+  bool fp8;
+};
+cudaError_t chunk_append(int dtype, const ChunkAppendParams& p, cudaStream_t s);
+
+struct ChunkAttnParams {
+  const int32_t* cu_rows;
+  const int32_t* kv_lens;
+  const void* q;
+  long long ld_q;
+  const void* cache_k;        // layer base
+  const void* cache_v;
+  const int32_t* block_table; // paged, or null
+  void* out;                  // [rows][n_h * d_h]
+  float* part;                // [2 * CTAs][kItemRows][d_h]: partial outputs, not normalised
+  float2* part_ml;            // [2 * CTAs][kItemRows]: (maximum, sum) of each partial row
+  int4* merge;                // [CTAs]: {sequence, KV head, item, pieces} of the range cut in CTA c
+  unsigned* status;
+  int batch, rows, n_h, n_kv, d_h, G, capacity, pages_per_seq, n_pages, window;
+  float scaling, k_scale, v_scale;
+  bool fp8;
+};
+
+size_t chunk_attn_workspace(int dtype, int d_h);
+// Carves part, part_ml and merge out of the workspace; false when it is too small.
+bool chunk_attn_carve(int dtype, int d_h, ChunkAttnParams& p, void* workspace, size_t bytes);
+cudaError_t chunk_attn(int dtype, const ChunkAttnParams& p, cudaStream_t s);
+cudaError_t chunk_attn_simt(int dtype, const ChunkAttnParams& p, cudaStream_t s);
+cudaError_t chunk_attn_tc(const ChunkAttnParams& p, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// The work split. The query rows of (sequence b, KV head) are its n new rows times the G
+// query heads that share the KV head, stacked row-major (row = token * G + head). An item
+// is `rows` consecutive stacked rows with all their key tiles; all items lie end to end as
+// one line of costs (a fixed cost each, plus their key tiles) and CTA c works on
+// [total * c / n, total * (c + 1) / n) of it, cutting items where its share begins or ends.
+// A piece of a cut item leaves an fp32 partial in the workspace (at most two per CTA: the
+// end of an item begun before, and the start of one continued after), so the workspace
+// depends on the number of CTAs alone. Every CTA derives its share from the lengths by
+// itself: no list, no launch of its own, nothing read back to the host.
+// ---------------------------------------------------------------------------
+namespace chunk {
+
+struct Split {
+  const int32_t* cu_rows;
+  const int32_t* kv_lens;
+  int batch, rows, n_kv, G, capacity, window;
+  int item_rows;   // stacked rows of an item
+  int tile_keys;   // keys of a tile
+  int item_cost;   // fixed cost of an item, in tiles
+};
+
+struct Seq {
+  int row0, n, kv;  // first row, new rows, rows held (0: refused)
+};
+
+__device__ __forceinline__ Seq load_seq(const Split& p, int b, unsigned* bad) {
+  Seq s;
+  s.row0 = p.cu_rows[b];
+  s.n = p.cu_rows[b + 1] - s.row0;
+  s.kv = p.kv_lens[b];
+  if (s.row0 < 0 || s.n < 0 || s.n > p.rows - s.row0) {
+    *bad |= DFLASH_DEV_ROWS;
+    s.n = 0;
+  }
+  if (s.kv < 0 || s.kv > p.capacity) {
+    *bad |= DFLASH_DEV_CAPACITY;
+    s.kv = 0;
+  }
+  return s;
+}
+
+__device__ __forceinline__ int n_items(const Split& p, const Seq& s) {
+  return (int)(((long long)s.n * p.G + p.item_rows - 1) / p.item_rows);
+}
+
+// First key (a multiple of the tile) and key tiles of item t.
+__device__ __forceinline__ int2 item_keys(const Split& p, const Seq& s, int t) {
+  const long long r0 = (long long)t * p.item_rows;
+  const long long r1 = min(r0 + p.item_rows, (long long)s.n * p.G);
+  const int first = s.kv - s.n + (int)(r0 / p.G), last = s.kv - s.n + (int)((r1 - 1) / p.G);
+  if (last < 0) return make_int2(0, 0);
+  int k0 = 0;
+  if (p.window > 0 && first >= p.window) k0 = (first - p.window + 1) / p.tile_keys * p.tile_keys;
+  return make_int2(k0, (last - k0) / p.tile_keys + 1);
+}
+
+__device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+// A CTA's share and where it starts.
+struct Start {
+  long long begin, end;  // on the cost line
+  long long total;
+  int ctas;              // CTAs with a share
+  int b, kvh, t;         // the item that holds `begin`
+  int off;               // cost units of it before `begin`
+};
+
+// CTAs that get a share: at least one unit each.
+__device__ __forceinline__ int active_ctas(long long total, int ctas) {
+  return total < ctas ? (int)total : ctas;
+}
+__device__ __forceinline__ long long bound(long long total, int active, int c) {
+  return total * c / active;
+}
+
+// Run by all threads of the CTA; `cost` is shared scratch of p.batch long longs (free again
+// after the call and a __syncthreads), `st` shared.
+__device__ __forceinline__ void locate(const Split& p, long long* cost, Start* st, unsigned* status) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  unsigned bad = 0;
+  for (int b = warp; b < p.batch; b += nw) {
+    const Seq s = load_seq(p, b, &bad);
+    const int items = n_items(p, s);
+    long long sum = 0;
+    for (int t = lane; t < items; t += 32) sum += p.item_cost + item_keys(p, s, t).y;
+    if (items > 1) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    if (lane == 0) cost[b] = sum * p.n_kv;
+  }
+  if (bad && lane == 0 && blockIdx.x == 0) atomicOr(status, bad);
+  __syncthreads();
+  if (warp == 0) {  // prefix sums, in place
+    long long carry = 0;
+    for (int base = 0; base < p.batch; base += 32) {
+      long long v = base + lane < p.batch ? cost[base + lane] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      v += carry;
+      if (base + lane < p.batch) cost[base + lane] = v;
+      carry = __shfl_sync(0xffffffffu, v, 31);
+    }
+    __syncwarp();
+    const int active = active_ctas(carry, (int)gridDim.x);
+    const int c = (int)blockIdx.x;
+    const long long begin = c < active ? bound(carry, active, c) : carry;
+    const long long end = c < active ? bound(carry, active, c + 1) : carry;
+    int b = 0;
+    if (begin < end) {  // the first sequence whose prefix exceeds begin
+      int lo = 0, hi = p.batch - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (cost[mid] > begin) hi = mid; else lo = mid + 1;
+      }
+      b = lo;
+      unsigned ignored = 0;
+      const Seq s = load_seq(p, b, &ignored);
+      const long long before = b > 0 ? cost[b - 1] : 0;
+      const long long per_head = (cost[b] - before) / p.n_kv;
+      const int kvh = (int)((begin - before) / per_head);
+      long long rest = begin - before - per_head * kvh;
+      // the item: scan their costs 32 at a time
+      const int items = n_items(p, s);
+      int t = 0;
+      for (int base = 0; base < items; base += 32) {
+        const int u = base + lane;
+        const int w = u < items ? p.item_cost + item_keys(p, s, u).y : 0;
+        long long v = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, v > rest);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          t = base + l;
+          rest -= __shfl_sync(0xffffffffu, v - w, l);
+          break;
+        }
+        rest -= __shfl_sync(0xffffffffu, v, 31);
+      }
+      if (lane == 0) {
+        st->kvh = kvh;
+        st->t = t;
+        st->off = (int)rest;
+      }
+    }
+    if (lane == 0) {
+      st->begin = begin;
+      st->end = end;
+      st->total = carry;
+      st->ctas = active;
+      st->b = b;
+    }
+  }
+  __syncthreads();
+}
+
+// One piece of work: key tiles [tile0, tile1) of item t of (b, kvh).
+struct Piece {
+  int b, kvh, t;
+  int row0, n, kv;   // of the sequence
+  int k0;            // first key of the item
+  int tile0, tile1;
+  int slot;          // -1: the whole item; else partial slot 0 or 1 of this CTA
+};
+
+// Walks a CTA's share piece by piece (one thread, or all threads of a warp alike).
+struct Walker {
+  Split p;
+  Seq s;
+  long long at, end, total;
+  int ctas, b, kvh, t, off;
+  int4 merge;  // what to merge: {b, kvh, t, pieces}, pieces 0 when nothing was cut here
+
+  __device__ void init(const Split& split, const Start& st) {
+    p = split;
+    at = st.begin;
+    end = st.end;
+    total = st.total;
+    ctas = st.ctas;
+    b = st.b;
+    kvh = st.kvh;
+    t = st.t;
+    off = st.off;
+    merge = make_int4(0, 0, 0, 0);
+    unsigned ignored = 0;
+    if (at < end) s = load_seq(p, b, &ignored);
+  }
+
+  __device__ bool next(Piece* w) {
+    while (at < end) {
+      const int items = n_items(p, s);
+      if (t >= items) {  // next KV head, next sequence
+        t = 0;
+        if (items == 0 || ++kvh >= p.n_kv) {
+          kvh = 0;
+          if (++b >= p.batch) return false;
+          unsigned ignored = 0;
+          s = load_seq(p, b, &ignored);
+        }
+        continue;
+      }
+      const int2 keys = item_keys(p, s, t);
+      const int whole = p.item_cost + keys.y;
+      const int take = (int)min((long long)(whole - off), end - at);
+      const int tile0 = max(0, off - p.item_cost), tile1 = max(0, off + take - p.item_cost);
+      const bool starts = off == 0;
+      w->b = b;
+      w->kvh = kvh;
+      w->t = t;
+      w->row0 = s.row0;
+      w->n = s.n;
+      w->kv = s.kv;
+      w->k0 = keys.x;
+      w->tile0 = tile0;
+      w->tile1 = tile1;
+      w->slot = tile0 == 0 && tile1 == keys.y ? -1 : (tile0 == 0 ? 1 : 0);
+      at += take;
+      off += take;
+      if (w->slot == 1 && tile1 > 0) {
+        // the start of an item that goes on: how many CTAs finish it
+        const long long item_end = at + (whole - off);
+        int c = (int)blockIdx.x + 1, n = 1;
+        while (bound(total, ctas, c) < item_end) {
+          ++c;
+          ++n;
+        }
+        merge = make_int4(b, kvh, t, n);
+      }
+      if (off == whole) {
+        ++t;
+        off = 0;
+      }
+      if (tile1 > tile0 || (keys.y == 0 && starts)) return true;
+    }
+    return false;
+  }
+};
+
+}  // namespace chunk
+}  // namespace dflash

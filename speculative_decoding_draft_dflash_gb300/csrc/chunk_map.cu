@@ -1,0 +1,156 @@
+// Plan of a chunk step: pages from the free list, slots and positions of the new rows, and
+// the lengths after the step (KV Cache + Speculative Decoding Interview Cheat Sheet, section
+// 5: logical rows in fixed-size pages behind a block table).
+//
+//   total_b = len_b + n_b,  need_b = max(0, ceil(total_b / 128) - held_b),
+//   end_b = need_0 + .. + need_b (sequences that fit the capacity),
+//   page i of need_b = free[taken + end_b - need_b + i],
+//   slot of a row at position p = table[b][p / 128] * 128 + p % 128.
+//
+// A few KB of integers: the launch and its chain of dependent loads are the cost. One
+// launch does both halves. The first CTA scans the sequences; then every CTA of the cluster
+// expands rows, a cluster barrier in between.
+#include "chunk.cuh"
+#include "sm100_ptx.cuh"
+
+namespace dflash {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kPage = 128;
+
+__global__ void __launch_bounds__(kThreads) chunk_map_kernel(const ChunkMapParams p) {
+  extern __shared__ int cu_s[];  // [batch + 1]
+  __shared__ long long warp_tot[kThreads / 32];
+  __shared__ long long carry;
+  __shared__ int taken_sum;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned rank = ptx::cluster_ctarank();
+  for (int i = threadIdx.x; i <= p.batch; i += kThreads) cu_s[i] = p.cu_rows[i];
+  if (threadIdx.x == 0) {
+    carry = 0;
+    taken_sum = 0;
+  }
+  __syncthreads();
+  if (rank == 0) {
+    const int head = p.paged ? *p.taken : 0;
+    const long long avail = (long long)p.n_free - head;
+    unsigned bad = p.paged && head < 0 ? DFLASH_DEV_CAPACITY : 0u;
+    for (int base = 0; base < p.batch; base += kThreads) {
+      const int b = base + threadIdx.x;
+      bool fits = false;
+      int held = 0, need = 0;
+      long long total = 0;
+      if (b < p.batch) {
+        const int lo = cu_s[b], hi = cu_s[b + 1], len = p.lens[b];
+        held = p.paged ? p.held[b] : 0;
+        total = (long long)len + hi - lo;
+        if (lo < 0 || hi < lo || hi > p.rows) {
+          bad |= DFLASH_DEV_ROWS;
+        } else if (len < 0 || total > p.capacity || held < 0 || held > p.pages_per_seq || head < 0) {
+          bad |= DFLASH_DEV_CAPACITY;
+        } else {
+          fits = true;
+          if (p.paged) need = max(0, (int)((total + kPage - 1) / kPage) - held);
+        }
+      }
+      // inclusive prefix sum of the pages asked for
+      long long v = need;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (lane == 31) warp_tot[warp] = v;
+      __syncthreads();
+      if (warp == 0) {
+        long long t = warp_tot[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long u = __shfl_up_sync(0xffffffffu, t, o);
+          if (lane >= o) t += u;
+        }
+        warp_tot[lane] = t;
+      }
+      __syncthreads();
+      const long long end = carry + (warp > 0 ? warp_tot[warp - 1] : 0) + v;
+      const bool ok = fits && (need == 0 || end <= avail);
+      if (fits && !ok) bad |= DFLASH_DEV_CAPACITY;
+      const int got = ok ? need : 0;
+      if (b < p.batch) {
+        p.kv_lens[b] = ok ? (int)total : 0;
+        if (p.paged) p.held_out[b] = held + got;
+      }
+      // the new pages of this warp's sequences, 32 at a time
+      unsigned with = __ballot_sync(0xffffffffu, got > 0);
+      while (with) {
+        const int l = __ffs(with) - 1;
+        with &= with - 1;
+        const int n = __shfl_sync(0xffffffffu, got, l), h = __shfl_sync(0xffffffffu, held, l);
+        const long long at = head + __shfl_sync(0xffffffffu, end, l) - n;
+        int32_t* row = p.table + (size_t)(base + warp * 32 + l) * p.pages_per_seq + h;
+        for (int i = lane; i < n; i += 32) {
+          const int id = p.free_pages[at + i];
+          row[i] = id;
+          if (id < 0 || id >= p.n_pages) bad |= DFLASH_DEV_PAGE;
+        }
+      }
+      const int warp_got = __reduce_add_sync(0xffffffffu, got);
+      if (lane == 0 && warp_got) atomicAdd(&taken_sum, warp_got);
+      __syncthreads();
+      if (threadIdx.x == 0) carry += warp_tot[kThreads / 32 - 1];
+      __syncthreads();
+    }
+    if (p.paged && threadIdx.x == 0) *p.taken_out = head + taken_sum;
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    if (lane == 0 && bad) atomicOr(p.status, bad);
+  }
+  ptx::cluster_sync();  // the table, the lengths: visible to every CTA of the cluster
+  // rows: the sequence by binary search (the last b with cu[b] <= r)
+  const int n_cta = (int)gridDim.x;
+  for (int r = (int)rank * kThreads + threadIdx.x; r < p.rows; r += n_cta * kThreads) {
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cu_s[mid] <= r) lo = mid; else hi = mid;
+    }
+    int slot = -1, pos = -1;
+    if (r >= cu_s[lo] && r < cu_s[lo + 1] && __ldcg(p.kv_lens + lo) > 0) {
+      pos = p.lens[lo] + (r - cu_s[lo]);
+      if (p.paged) {
+        const int page = __ldcg(p.table + (size_t)lo * p.pages_per_seq + pos / kPage);
+        slot = page >= 0 && page < p.n_pages ? page * kPage + pos % kPage : -1;
+        if (slot < 0) {
+          pos = -1;
+          atomicOr(p.status, DFLASH_DEV_PAGE);
+        }
+      } else {
+        slot = lo * p.capacity + pos;
+      }
+    }
+    p.slots[r] = slot;
+    p.positions[r] = pos;
+  }
+}
+
+}  // namespace
+
+cudaError_t chunk_map(const ChunkMapParams& p, cudaStream_t s) {
+  LaunchScope ls_(DFLASH_KERNEL_CHUNK_MAP, s);
+  cudaLaunchConfig_t cfg = {};
+  // few rows: one CTA expands them as fast as eight would start
+  const int ctas = p.rows > 4 * kThreads ? 8 : 1;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)(p.batch + 1) * sizeof(int);  // at most 32 KB
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_map_kernel, p);
+}
+
+}  // namespace dflash

@@ -36,8 +36,6 @@ unsigned* status_word() {
   return ptr[dev];
 }
 
-namespace {
-
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 dflash_status check_dims(const dflash_dims* d) {
@@ -95,6 +93,10 @@ float kv_scale(const dflash_kv_cache* c, int layer, int which) {
   return kv_fp8(c) && c->kv_scales ? c->kv_scales[2 * layer + which] : 1.f;
 }
 
+dflash_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA; }
+
+namespace {
+
 // Fills the fp8 fields of a per-head epilogue: quantisation by the inverse scales, and
 // Q as codes + remainder codes (the remainder array follows the codes in q_out).
 void fp8_epilogue(HeadEpilogue& ep, const dflash_dims* d, const dflash_kv_cache* c, int layer) {
@@ -105,8 +107,6 @@ void fp8_epilogue(HeadEpilogue& ep, const dflash_dims* d, const dflash_kv_cache*
   if (ep.q_out)
     ep.q_lo = (char*)ep.q_out + (size_t)c->batch * d->n_h * d->block_size * d->d_h;
 }
-
-dflash_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA; }
 
 // Attention chunking for a cache of `capacity` rows and an optional window.
 void attn_chunks(const dflash_dims* d, int capacity, int window, int* chunk, int* n_chunks) {

@@ -57,8 +57,22 @@ struct Carver {
 // test lowered it with dflash_test_wait_limit; dflash_api.cu).
 unsigned long long wait_limit_ns();
 
+// SMs of the current device (attn_tc.cu)
+int sm_count();
+
 // per-device sticky status word (defined in dflash_api.cu)
 unsigned* status_word();
+
+// Host argument checks shared by the entry points (dflash_api.cu).
+bool aligned16(const void* p);
+dflash_status check_dims(const dflash_dims* d);
+dflash_status check_cache(const dflash_kv_cache* c, int layer);
+dflash_status check_layout(const dflash_dims* d, const dflash_kv_cache* c);
+bool kv_fp8(const dflash_kv_cache* c);
+size_t esize(const dflash_dims* d);
+size_t kv_esize(const dflash_dims* d, const dflash_kv_cache* c);  // bytes of one cache element
+float kv_scale(const dflash_kv_cache* c, int layer, int which);
+dflash_status cuda_status(cudaError_t e);
 
 // Brackets one kernel launch: counts it and, while tracing selects its kind,
 // records CUDA events around it on its stream (trace.cu).

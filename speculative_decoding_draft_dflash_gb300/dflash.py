@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_double, c_float, c_int, c_size_t, c_uint, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int, c_longlong, c_size_t, c_uint, c_void_p
 
 import numpy as np
 import torch
@@ -22,10 +22,11 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdflash.so")
 
 DFLASH_F32, DFLASH_BF16 = 0, 1
-DEV_CAPACITY, DEV_ROPE, DEV_CROP, DEV_ROWS, DEV_TIMEOUT = 1, 2, 4, 8, 16
+DEV_CAPACITY, DEV_ROPE, DEV_CROP, DEV_ROWS, DEV_TIMEOUT, DEV_PAGE = 1, 2, 4, 8, 16, 32
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE = range(6)
 KERNEL_NAMES = {1: "gemm", 2: "rmsnorm", 3: "head_epilogue", 4: "attention", 5: "combine",
-                6: "lens", 7: "crop", 8: "rope_table", 9: "schedule", 10: "accept"}
+                6: "lens", 7: "crop", 8: "rope_table", 9: "schedule", 10: "accept",
+                11: "chunk_map", 12: "chunk_append", 13: "chunk_attn", 14: "chunk_merge"}
 KERNEL_IDS = {v: k for k, v in KERNEL_NAMES.items()}
 
 
@@ -50,6 +51,17 @@ class dflash_kv_cache(ctypes.Structure):
 DFLASH_FP8_E4M3 = 2
 
 
+class dflash_chunk(ctypes.Structure):
+    _fields_ = [("cu_rows", c_void_p), ("kv_lens", c_void_p), ("slots", c_void_p),
+                ("positions", c_void_p), ("batch", c_int), ("rows", c_int)]
+
+
+class dflash_page_pool(ctypes.Structure):
+    _fields_ = [("block_table", c_void_p), ("pages_held", c_void_p), ("pages_held_out", c_void_p),
+                ("free_pages", c_void_p), ("n_free", c_int), ("taken", c_void_p),
+                ("taken_out", c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libdflash.so is not built ({LIB_PATH}); run "
@@ -71,6 +83,12 @@ def _load():
         "dflash_layer_out": (c_int, [P, c_int, P, P, P, P, c_int, P, P, P, P, P, c_size_t, P]),
         "dflash_rms_norm": (c_int, [P, c_int, P, P, P, P]),
         "dflash_accept": (c_int, [P, P, c_int, c_int, P, P, P, P, P, P]),
+        "dflash_chunk_map": (c_int, [P, c_int, P, P, P]),
+        "dflash_chunk_append": (c_int, [P, P, c_int, P, P, c_longlong, P, c_longlong, P, c_longlong,
+                                        P, P, P, c_int, P, P]),
+        "dflash_chunk_workspace_bytes": (c_size_t, [P]),
+        "dflash_chunk_attn": (c_int, [P, P, c_int, P, P, c_longlong, c_int, c_float, P, P, c_size_t,
+                                      P]),
         "dflash_status_get": (c_int, [POINTER(c_uint), P]),
         "dflash_status_string": (ctypes.c_char_p, [c_int]),
         "dflash_trace_start": (c_int, [c_uint, c_int]),
@@ -273,6 +291,50 @@ class KVCache:
         self.v[layer, pages, :, r] = V.permute(1, 0, 2).to(self.v.dtype)
 
 
+class ChunkPlan:
+    """The rows of one step (dflash_chunk): cu_rows int32 [batch + 1] groups `rows` rows by
+    sequence; kv_lens [batch], slots [rows] and positions [rows] are what dflash_chunk_map
+    fills and the other calls read. Arrays that are not given are allocated next to cu_rows
+    (kv_lens 0, slots and positions -1). The tensors are kept, so the plan stays valid as
+    long as it lives; one plan serves every layer of a step."""
+
+    def __init__(self, cu_rows, rows, kv_lens=None, slots=None, positions=None):
+        i32 = torch.int32
+        self.batch, self.rows = int(cu_rows.numel()) - 1, int(rows)
+        if self.batch < 1 or self.rows < 0:
+            raise ValueError(f"chunk plan: {self.batch} sequences, {self.rows} rows")
+        new = lambda n, v: torch.full((n,), v, dtype=i32, device=cu_rows.device)  # noqa: E731
+        self.cu_rows = cu_rows
+        self.kv_lens = new(self.batch, 0) if kv_lens is None else kv_lens
+        self.slots = new(self.rows, -1) if slots is None else slots
+        self.positions = new(self.rows, -1) if positions is None else positions
+        self.desc = dflash_chunk(_ptr(cu_rows, "cu_rows", i32, self.batch + 1),
+                                 _ptr(self.kv_lens, "kv_lens", i32, self.batch),
+                                 _ptr(self.slots, "slots", i32, self.rows),
+                                 _ptr(self.positions, "positions", i32, self.rows),
+                                 self.batch, self.rows)
+        self.ref = ctypes.byref(self.desc)
+
+
+class PagePool:
+    """The page allocation of a paged cache (dflash_page_pool): pages held per sequence, the
+    list of free pages and how many of them are taken. The _out arrays default to the inputs
+    (updated in place)."""
+
+    def __init__(self, pages_held, free_pages, taken, pages_held_out=None, taken_out=None):
+        i32, batch = torch.int32, int(pages_held.numel())
+        self.batch = batch
+        self.pages_held, self.free_pages, self.taken = pages_held, free_pages, taken
+        self.pages_held_out = pages_held if pages_held_out is None else pages_held_out
+        self.taken_out = taken if taken_out is None else taken_out
+        self.desc = dflash_page_pool(None, _ptr(pages_held, "pages_held", i32, batch),
+                                     _ptr(self.pages_held_out, "pages_held_out", i32, batch),
+                                     _ptr(free_pages, "free_pages", i32), int(free_pages.numel()),
+                                     _ptr(taken, "taken", i32, 1),
+                                     _ptr(self.taken_out, "taken_out", i32, 1))
+        self.ref = ctypes.byref(self.desc)
+
+
 # ---------------------------------------------------------------------------
 # the C calls
 # ---------------------------------------------------------------------------
@@ -388,6 +450,76 @@ def dflash_accept(block_ids, posterior, ctx_len, accept_len, next_cu_rows, ctx_n
                               _ptr(ctx_next, "ctx_next", i32, batch),
                               _ptr(next_anchor, "next_anchor", i32, batch), _stream(stream)),
            "dflash_accept")
+
+
+def _rows(t, what, dtype, rows, width):
+    """(address, elements between rows) of `rows` rows of `width` elements: a CUDA tensor
+    [>= rows][width] (or [>= rows][heads][d_h]) whose rows are dense; the rows themselves may
+    lie apart (a slice of a fused projection's output)."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: element type {t.dtype}, the call needs {dtype}")
+    shape, st = t.shape, t.stride()
+    dense = (len(shape) == 2 and shape[1] == width and st[1] == 1) or (
+        len(shape) == 3 and shape[1] * shape[2] == width and st[2] == 1 and
+        (st[1] == shape[2] or shape[1] == 1))
+    if not dense or shape[0] < rows:
+        raise ValueError(f"{what}: shape {tuple(shape)}, strides {st}; the call needs {rows} rows "
+                         f"of {width} dense elements")
+    return t.data_ptr(), st[0] if shape[0] > 1 else width
+
+
+def _chunk(plan, cache):
+    """C descriptor of a plan, checked against the cache's batch."""
+    if plan.batch != cache.batch:
+        raise ValueError(f"chunk plan: {plan.batch} sequences, the cache has {cache.batch}")
+    return plan.ref
+
+
+def dflash_chunk_map(cache, layer, plan, pool=None, stream=None):
+    """Pages, slots, positions and lengths of a step, from the lengths of `layer`."""
+    desc = cache.desc if isinstance(cache, KVCache) else cache
+    if pool is not None:
+        if pool.batch < desc.batch:
+            raise ValueError(f"page pool: {pool.batch} sequences, the cache has {desc.batch}")
+        pool.desc.block_table = desc.block_table
+    _check(_lib.dflash_chunk_map(ctypes.byref(desc), int(layer), _chunk(plan, desc),
+                                 None if pool is None else pool.ref, _stream(stream)),
+           "dflash_chunk_map")
+
+
+def dflash_chunk_append(dims, cache, layer, plan, q, k, v, gamma_q, gamma_k, rope_table, table_len,
+                        q_out, stream=None):
+    """Norm, RoPE and store of a step's rows in one layer; q and q_out may be None."""
+    desc, et, d_h, rows = _desc(dims, cache), _et(dims), dims.d_h, plan.rows
+    qw, kw = dims.n_h * d_h, dims.n_kv * d_h
+    qp, ldq = (None, 0) if q is None else _rows(q, "q", et, rows, qw)
+    kp, ldk = _rows(k, "k", et, rows, kw)
+    vp, ldv = _rows(v, "v", et, rows, kw)
+    _check(_lib.dflash_chunk_append(ctypes.byref(dims), ctypes.byref(desc), int(layer),
+                                    _chunk(plan, desc), qp, ldq, kp, ldk, vp, ldv,
+                                    _ptr(gamma_q, "gamma_q", et, d_h),
+                                    _ptr(gamma_k, "gamma_k", et, d_h),
+                                    None if rope_table is None else _rope(dims, rope_table, table_len),
+                                    int(table_len), _ptr(q_out, "q_out", et, rows * qw),
+                                    _stream(stream)), "dflash_chunk_append")
+
+
+def dflash_chunk_workspace_bytes(dims):
+    return int(_lib.dflash_chunk_workspace_bytes(ctypes.byref(dims)))
+
+
+def dflash_chunk_attn(dims, cache, layer, plan, q, sliding_window, scaling, out, workspace,
+                      stream=None):
+    """Causal attention of a step's rows over one layer of the cache."""
+    desc, et = _desc(dims, cache), _et(dims)
+    qw = dims.n_h * dims.d_h
+    qp, ldq = _rows(q, "q", et, plan.rows, qw)
+    _check(_lib.dflash_chunk_attn(ctypes.byref(dims), ctypes.byref(desc), int(layer),
+                                  _chunk(plan, desc), qp, ldq, int(sliding_window), float(scaling),
+                                  _ptr(out, "out", et, plan.rows * qw), *_ws(workspace),
+                                  _stream(stream)), "dflash_chunk_attn")
 
 
 def dflash_layer_out_workspace_bytes(dims, M, d_ff):
