@@ -5,7 +5,7 @@ namespace dflash {
 namespace {
 
 constexpr int kSimtRows = 64;   // stacked query rows of an item (chunk_attn_simt.cu)
-constexpr int kTcRows = 256;    // (chunk_attn_tc.cu)
+constexpr int kTcRows = 256;    // at most (chunk_attn_tc.cu)
 
 int item_rows(int dtype) { return dtype == DFLASH_F32 ? kSimtRows : kTcRows; }
 
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkAttnParams 
     float L = 0.f;
     for (int i = lane; i < m.w; i += 32) {
       const float2 ml = p.part_ml[at(i)];
-      L += weight(ml.x) * ml.y;
+      L += ml.y == 0.f ? 0.f : weight(ml.x) * ml.y;
     }
     L = warp_sum(L);
     float2 acc[4] = {};
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkAttnParams 
         }
       }
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     const long long q = r0 + r;
     const int token = (int)(q / p.G), g = (int)(q - (long long)token * p.G);
     T* dst = (T*)p.out + ((size_t)(row0 + token) * p.n_h + m.y * p.G + g) * p.d_h;
@@ -104,14 +104,14 @@ bool chunk_attn_carve(int dtype, int d_h, ChunkAttnParams& p, void* workspace, s
 }
 
 cudaError_t chunk_attn(int dtype, const ChunkAttnParams& p, cudaStream_t s) {
-  cudaError_t e = chunk_attn_simt(dtype, p, s);
+  cudaError_t e = dtype == DFLASH_F32 ? chunk_attn_simt(p, s) : chunk_attn_tc(p, s);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_MERGE, s);
   const dim3 grid(sm_count(), 4);
   if (dtype == DFLASH_F32)
     chunk_merge_kernel<float><<<grid, 256, 0, s>>>(p, kSimtRows);
   else
-    chunk_merge_kernel<bf16><<<grid, 256, 0, s>>>(p, kSimtRows);
+    chunk_merge_kernel<bf16><<<grid, 256, 0, s>>>(p, chunk_attn_tc_item_rows(p.G));
   return cudaGetLastError();
 }
 

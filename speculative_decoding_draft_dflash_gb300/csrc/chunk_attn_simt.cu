@@ -15,11 +15,7 @@ constexpr int RI = 64;   // stacked query rows of an item
 constexpr int TK = 64;   // keys per tile
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float elem(const float* p, size_t i) { return p[i]; }
-__device__ __forceinline__ float elem(const bf16* p, size_t i) { return __bfloat162float(p[i]); }
-__device__ __forceinline__ float elem(const uint8_t* p, size_t i) { return e4m3x2_value(p[i]).x; }
-
-template <typename T, typename C, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) chunk_attn_simt_kernel(const ChunkAttnParams p) {
   constexpr int LD = DP + 4, LP = TK + 4;
   extern __shared__ float4 smem4[];
@@ -35,9 +31,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_simt_kernel(const Chun
   walk.init(split, start);
   __syncthreads();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, d = p.d_h;
-  const T* q = (const T*)p.q;
-  const C* ck = (const C*)p.cache_k;
-  const C* cvv = (const C*)p.cache_v;
+  const float* q = (const float*)p.q;
+  const float* ck = (const float*)p.cache_k;
+  const float* cv = (const float*)p.cache_v;
   chunk::Piece w;
   while (walk.next(&w)) {
     const long long r0 = (long long)w.t * RI;
@@ -48,7 +44,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_simt_kernel(const Chun
       float x = 0.f;
       if (r < rows && c < d) {
         const int token = (int)((r0 + r) / p.G), g = (int)(r0 + r - (long long)token * p.G);
-        x = elem(q, (size_t)(w.row0 + token) * p.ld_q + (size_t)(w.kvh * p.G + g) * d + c);
+        x = q[(size_t)(w.row0 + token) * p.ld_q + (size_t)(w.kvh * p.G + g) * d + c];
       }
       Qs[r * LD + c] = x;
     }
@@ -66,21 +62,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_simt_kernel(const Chun
     for (int j = w.tile0; j < w.tile1; ++j) {
       const int k0 = w.k0 + j * TK;
       __syncthreads();
-      // rows of the tile: inside one page, or of the sequence's slab; keys past the length
-      // are zero (what their slots hold is never read)
-      long long row = -1;
-      if (p.block_table) {
-        const int page = p.block_table[(size_t)w.b * p.pages_per_seq + (k0 >> 7)];
-        if (page >= 0 && page < p.n_pages) row = ((long long)page * p.n_kv + w.kvh) * 128 + (k0 & 127);
-        else if (threadIdx.x == 0) atomicOr(p.status, DFLASH_DEV_PAGE);
-      } else {
-        row = ((long long)w.b * p.n_kv + w.kvh) * p.capacity + k0;
-      }
+      // keys past the length are zero (what their slots hold is never read)
+      const size_t row = ((size_t)w.b * p.n_kv + w.kvh) * p.capacity + k0;
       for (int i = threadIdx.x; i < TK * DP; i += kThreads) {
         const int r = i / DP, c = i - r * DP;
-        const bool in = row >= 0 && k0 + r < w.kv && c < d;
-        Ks[r * LD + c] = in ? elem(ck, (size_t)(row + r) * d + c) * p.k_scale : 0.f;
-        Vs[r * LD + c] = in ? elem(cvv, (size_t)(row + r) * d + c) * p.v_scale : 0.f;
+        const bool in = k0 + r < w.kv && c < d;
+        Ks[r * LD + c] = in ? ck[(row + r) * d + c] : 0.f;
+        Vs[r * LD + c] = in ? cv[(row + r) * d + c] : 0.f;
       }
       __syncthreads();
       float s[4][4] = {};
@@ -157,13 +145,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_simt_kernel(const Chun
       if (r >= rows) continue;
       const size_t at = (size_t)(2 * blockIdx.x + (w.slot > 0)) * RI + r;
       if (w.slot < 0) {
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int token = (int)((r0 + r) / p.G), g = (int)(r0 + r - (long long)token * p.G);
-        T* dst = (T*)p.out + ((size_t)(w.row0 + token) * p.n_h + w.kvh * p.G + g) * d;
+        float* dst = (float*)p.out + ((size_t)(w.row0 + token) * p.n_h + w.kvh * p.G + g) * d;
 #pragma unroll
         for (int e = 0; e < DP / 16; ++e) {
           const int c = tx * 4 + 64 * (e >> 2) + (e & 3);
-          if (c < d) dst[c] = from_f<T>(o[i][e] * inv);
+          if (c < d) dst[c] = o[i][e] * inv;
         }
       } else {
 #pragma unroll
@@ -171,34 +159,31 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_simt_kernel(const Chun
           const int c = tx * 4 + 64 * (e >> 2) + (e & 3);
           if (c < d) p.part[at * d + c] = o[i][e];
         }
-        if (tx == 0)
-          p.part_ml[at] = make_float2(sizeof(T) == 4 ? m[i] : m[i] * 1.4426950408889634f, sum);
+        if (tx == 0) p.part_ml[at] = make_float2(m[i], sum);
       }
     }
   }
   if (threadIdx.x == 0) p.merge[blockIdx.x] = walk.merge;
 }
 
-template <typename T, typename C, int DP>
+template <int DP>
 cudaError_t launch(const ChunkAttnParams& p, cudaStream_t s) {
   const int smem = (int)sizeof(float) * ((RI + 2 * TK) * (DP + 4) + RI * (TK + 4));
   static_assert((64 + 128) * (DP + 4) * 4 + 64 * 68 * 4 >= 8 * kChunkMaxBatch, "prefix sums");
-  cudaError_t e = cudaFuncSetAttribute(chunk_attn_simt_kernel<T, C, DP>,
+  cudaError_t e = cudaFuncSetAttribute(chunk_attn_simt_kernel<DP>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_ATTN, s);
-  chunk_attn_simt_kernel<T, C, DP><<<sm_count(), kThreads, smem, s>>>(p);
+  chunk_attn_simt_kernel<DP><<<sm_count(), kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t chunk_attn_simt(int dtype, const ChunkAttnParams& p, cudaStream_t s) {
-  if (dtype == DFLASH_BF16)
-    return p.fp8 ? launch<bf16, uint8_t, 128>(p, s) : launch<bf16, bf16, 128>(p, s);
-  if (p.d_h <= 64) return launch<float, float, 64>(p, s);
-  if (p.d_h <= 128) return launch<float, float, 128>(p, s);
-  return launch<float, float, 256>(p, s);
+cudaError_t chunk_attn_simt(const ChunkAttnParams& p, cudaStream_t s) {
+  if (p.d_h <= 64) return launch<64>(p, s);
+  if (p.d_h <= 128) return launch<128>(p, s);
+  return launch<256>(p, s);
 }
 
 }  // namespace dflash

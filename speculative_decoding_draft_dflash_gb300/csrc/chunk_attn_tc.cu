@@ -1,0 +1,895 @@
+// Causal chunk attention on tcgen05 tensor cores (bf16; bf16 or E4M3 cache, d_h = 128).
+//
+//   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(s_ij - m_i),  s_ij = q_i k_j scaling log2(e)
+// over the keys j that row i sees, in one pass over 128-key tiles with the running reference
+// m_i. m_i only moves when a tile's maximum exceeds it by more than 8 (p stays below 2^8), so
+// the rescaling of the accumulator in tensor memory is rare.
+//
+// Query rows: the rows that share a KV head, stacked token by token (row = token * G + head),
+// fill M = 128 tiles of TQ = 128 / G whole tokens. An item (chunk.cuh) is two such tiles, A and
+// B. With more than one tile of rows each K / V tile serves A and B in turn, and the tensor
+// cores work on one while the other's softmax runs. An item of one tile (a decoded token, a
+// verified block) takes the keys of even tiles through A and odd ones through B, with the same
+// queries, and merges the two halves at the end.
+//
+// One persistent CTA per SM. Warps: 0-3 softmax of A, 4-7 softmax of B (a thread per row, all
+// 128 columns: no exchange between threads), 8 work list and TMA loads, 9 MMA issue, 10-11
+// (bf16) check of the V tiles that the mask cuts, 12-15 (E4M3) conversion of K tiles to bf16
+// and V tiles to f16. Tensor memory: S_A, S_B, O_A, O_B of 128 columns each; P (16 bits)
+// overwrites the first half of its S and is the A operand of the PV product from there.
+//
+// A masked key has weight exactly 0, and its V row must not enter even as 0 * NaN. In tiles
+// that are not visible to every row of the item, the checking warps replace what is not finite
+// by 0 and flag the item; the epilogue of a flagged item then adds the replaced values of the
+// keys that its row does see.
+#include <float.h>
+#include <string.h>
+
+#include "chunk.cuh"
+#include "sm100_ptx.cuh"
+
+namespace dflash {
+
+// 3-D view [rows][heads][128] of bf16 rows ld elements apart, box {64, box_heads, box_rows},
+// 128-byte swizzle (gemm_tc.cu); and the 2-D maps of the cache.
+bool encode_3d_bf16(CUtensorMap* m, const void* base, long long rows, int heads, long long ld,
+                    int box_heads, int box_rows);
+bool encode_2d_bf16(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows);
+bool encode_2d_u8(CUtensorMap* m, const void* base, long long rows, int box_rows);
+
+namespace {
+
+constexpr int TK = 128;
+constexpr uint32_t TILE = 128 * 128 * 2;  // a 16-bit tile
+constexpr uint32_t HALF = TILE / 2;       // its 64-column box
+constexpr int kRing = 4;                  // items in flight between the roles
+
+constexpr uint32_t TM_S = 0, TM_O = 256;  // tensor-memory columns of S_A; O_A (B: + 128)
+
+template <bool FP8>
+struct Plan {
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr int CHECK_WARPS = FP8 ? 4 : 2, W_CHECK = FP8 ? 12 : 10;
+  static constexpr int STAGES = FP8 ? 4 : 5;             // loaded K / V tiles
+  static constexpr uint32_t LOAD = FP8 ? TK * 128 : TILE;
+  static constexpr int C_STAGES = FP8 ? 3 : 0;           // converted tiles
+  static constexpr uint32_t OFF_KV = 2 * TILE;           // after Q_A, Q_B
+  static constexpr uint32_t OFF_C = OFF_KV + STAGES * LOAD;
+  static constexpr uint32_t OFF_END = OFF_C + C_STAGES * TILE;
+  // operand ring the MMA thread reads: the loaded tiles, or the converted ones
+  static constexpr int M_STAGES = FP8 ? C_STAGES : STAGES;
+  static constexpr uint32_t OFF_M = FP8 ? OFF_C : OFF_KV;
+  // registers: the softmax warpgroups take what the others give back (setmaxnreg draws on the
+  // launch's own registers: 384 x 168 = 256 x 200 + 128 x 104, 512 x 128 = 256 x 168 + 256 x 88)
+  static constexpr int REG_SOFT = FP8 ? 168 : 200, REG_REST = FP8 ? 88 : 104;
+};
+
+struct Params {
+  CUtensorMap q, k, v;
+  chunk::Split split;
+  const int32_t* table;  // paged: [batch][pps] page ids, or null
+  int pps, n_pages;
+  int oob_row;           // a row beyond the K / V maps: reads as zeros
+  const void* cache_v;   // this layer's V (the rare repair reads it)
+  bf16* out;
+  float* part;
+  float2* part_ml;
+  int4* merge;
+  unsigned* status;
+  int n_h, TQ, RT;       // tokens and rows of a tile
+  float sl2, v_scale;    // scaling * log2(e) (fp8: * k_scale); scale of the V codes
+  unsigned long long wait_ns;
+};
+
+struct Item {
+  chunk::Piece w;
+  int bad;  // a V tile held something not finite under the mask
+};
+
+// What follows the tiles in shared memory (nothing is declared statically, so that the tiles
+// start at the 1024-byte boundary their swizzle needs and fill the CTA's 227 KB).
+struct Tail {
+  uint64_t qf[2], qe[2];          // Q tile landed / read by its last S
+  uint64_t kf[5], ke[5];          // K / V tile landed / stage free again
+  uint64_t vq[5];                 // bf16: a V tile to check is on its way to the stage
+  uint64_t vc[5];                 // bf16: V tile checked; E4M3: tile converted
+  uint64_t ce[5];                 // E4M3: converted stage free again
+  uint64_t s[2], p[2];            // S complete; P stored
+  uint64_t o[2], oe;              // O complete: of one row tile; of both halves of the keys
+  uint64_t of;                    // O read by all softmax warps
+  uint64_t x[2];                  // (reference, sum) exchanged
+  uint64_t itf[kRing], ite[kRing], chk[kRing];  // item listed / released / V checks done
+  uint64_t fin;
+  Item ring[kRing];
+  chunk::Start start;
+  uint32_t tmem_slot;
+  int abort_flag;
+  float2 xml[2][128];             // (reference, sum) of the even / odd half
+};
+
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, unsigned* status) {
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (ptx::globaltimer() - t0 > ptx::kWaitLimitNs) {
+      atomicOr(status, DFLASH_DEV_TIMEOUT);
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));  // a -> low half
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+// Two E4M3 codes -> bf16x2 (exact: E4M3's range and mantissa lie inside bf16's).
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
+  const float2 f = e4m3x2_value((uint16_t)two);
+  return pack_bf16(f.x, f.y);
+}
+
+// A from tensor memory, B from shared memory.
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+constexpr uint32_t idesc_f16_f32(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+template <int N> __device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Facts of an item that every role derives alike.
+struct Geometry {
+  int T;          // key tiles of the piece
+  int key0;       // first key of its first tile
+  int first, last;  // positions of the item's first and last row
+  bool dual;      // two tiles of query rows (else even / odd key tiles)
+  __device__ __forceinline__ Geometry(const Params& p, const chunk::Piece& w) {
+    const int tok0 = w.t * 2 * p.TQ, tok1 = min(tok0 + 2 * p.TQ, w.n);
+    T = w.tile1 - w.tile0;
+    key0 = w.k0 + w.tile0 * TK;
+    first = w.kv - w.n + tok0;
+    last = w.kv - w.n + tok1 - 1;
+    dual = tok1 - tok0 > p.TQ;
+  }
+  // whether some row of the item does not see some key of tile j
+  __device__ __forceinline__ bool cut(const Params& p, int j) const {
+    const int k = key0 + j * TK;
+    return k + TK - 1 > first || (p.split.window > 0 && last - k >= p.split.window);
+  }
+  // keys of tile j that some row may see, counted from its start
+  __device__ __forceinline__ int valid(int j) const { return min(TK, last + 1 - (key0 + j * TK)); }
+  // Where K_j and V_j stand among the item's 2 T operand tiles. Two row tiles: K0 V0 K1 V1 ..;
+  // even / odd: K0 K1 V0 K2 V1 K3 .. V(T-2) V(T-1), each S two tiles ahead of its PV.
+  __device__ __forceinline__ int k_at(int j) const { return dual ? 2 * j : j < 2 ? j : 2 * j - 1; }
+  __device__ __forceinline__ int v_at(int j) const {
+    return dual ? 2 * j + 1 : j == T - 1 ? 2 * T - 1 : 2 * j + 2;
+  }
+};
+
+// Adds to 32 columns of an output row what the checking warps took out of the V tiles: the
+// values that are not finite, of keys the row sees.
+template <bool FP8>
+__device__ __noinline__ void repair(const Params& p, const Item& it, int pos, int col, float* o) {
+  const Geometry g(p, it.w);
+  for (int j = 0; j < g.T; ++j) {
+    if (!g.cut(p, j)) continue;
+    const int k = g.key0 + j * TK;
+    long long row;
+    if (p.table) {
+      const int page = p.table[(size_t)it.w.b * p.pps + (k >> 7)];
+      if (page < 0 || page >= p.n_pages) continue;
+      row = ((long long)page * p.split.n_kv + it.w.kvh) * TK;
+    } else {
+      row = ((long long)it.w.b * p.split.n_kv + it.w.kvh) * p.split.capacity + k;
+    }
+    for (int e = 0; e < TK; ++e) {
+      if (k + e > pos || (p.split.window > 0 && pos - (k + e) >= p.split.window)) continue;
+      for (int c = 0; c < 32; ++c) {
+        const size_t at = (size_t)(row + e) * 128 + col + c;
+        const float x = FP8 ? e4m3x2_value(((const uint8_t*)p.cache_v)[at]).x
+                            : __bfloat162float(((const bf16*)p.cache_v)[at]);
+        if (!isfinite(x)) o[c] += x;
+      }
+    }
+  }
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(const __grid_constant__ Params p) {
+  using PL = Plan<FP8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Tail& sh = *reinterpret_cast<Tail*>(smem + PL::OFF_END);
+  Item(&ring)[kRing] = sh.ring;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sbase = ptx::smem_u32(smem);
+  if (sbase & 1023) {  // the swizzled tiles would be misplaced
+    if (threadIdx.x == 0) atomicOr(p.status, DFLASH_DEV_TIMEOUT);
+    return;
+  }
+  auto bar = [](uint64_t* b) { return ptx::smem_u32(b); };
+  auto wait = [&](uint64_t& b, int parity) {
+    return ptx::mbar_wait(ptx::smem_u32(&b), (uint32_t)(parity & 1), &sh.abort_flag, p.status, p.wait_ns);
+  };
+
+  if (threadIdx.x == 0) {
+    sh.abort_flag = 0;
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(&sh.qf[i]), 1);
+      ptx::mbar_init(bar(&sh.qe[i]), 1);
+      ptx::mbar_init(bar(&sh.s[i]), 1);
+      ptx::mbar_init(bar(&sh.p[i]), 4);
+      ptx::mbar_init(bar(&sh.o[i]), 1);
+      ptx::mbar_init(bar(&sh.x[i]), 4);
+    }
+    ptx::mbar_init(bar(&sh.oe), 1);
+    ptx::mbar_init(bar(&sh.of), 8);
+    for (int i = 0; i < 5; ++i) {
+      ptx::mbar_init(bar(&sh.kf[i]), 1);
+      ptx::mbar_init(bar(&sh.ke[i]), FP8 ? PL::CHECK_WARPS : 1);
+      ptx::mbar_init(bar(&sh.vq[i]), 1);
+      ptx::mbar_init(bar(&sh.vc[i]), PL::CHECK_WARPS);
+      ptx::mbar_init(bar(&sh.ce[i]), 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      ptx::mbar_init(bar(&sh.itf[i]), 1);
+      ptx::mbar_init(bar(&sh.ite[i]), 1 + 8 + PL::CHECK_WARPS);
+      ptx::mbar_init(bar(&sh.chk[i]), PL::CHECK_WARPS);
+    }
+    ptx::mbar_init(bar(&sh.fin), 1);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(ptx::smem_u32(&sh.tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  // prefix sums of the work split, in what becomes the K / V ring
+  static_assert(PL::OFF_END - PL::OFF_KV >= 8 * kChunkMaxBatch, "prefix sums");
+  chunk::locate(p.split, reinterpret_cast<long long*>(smem + PL::OFF_KV), &sh.start, p.status);
+  ptx::fence_proxy_async_smem();  // TMA overwrites them
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh.tmem_slot;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------------ softmax
+    reg_inc<PL::REG_SOFT>();
+    const int X = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + TM_S + X * 128, tO = tmem + lanes + TM_O;
+    const int G = p.split.G, rt = r / G, rg = r - rt * G;     // token and head of this row
+    const int wt0 = ((warp & 3) * 32) / G;                    // tokens of the warp's first and last row
+    const int wt1 = ((warp & 3) * 32 + 31) / G;
+    int ns = 0, no = 0, nd = 0, nx = 0;  // tiles, items with keys; of two row tiles, of one
+    for (int n = 0;; ++n) {
+      const int slot = n % kRing;
+      if (!__all_sync(0xffffffffu, wait(sh.itf[slot], n / kRing))) break;
+      const Item& it = ring[slot];
+      if (it.w.b < 0) break;
+      const Geometry g(p, it.w);
+      const int tok = (g.dual ? X * p.TQ : 0) + rt;           // token of the item
+      const int left = it.w.n - it.w.t * 2 * p.TQ;            // tokens from the item's start on
+      const bool valid = r < p.RT && tok < left;
+      const int pos = g.first + tok;
+      const int wfirst = g.first + tok - rt + wt0;
+      const bool any = __any_sync(0xffffffffu, valid);
+      const int wlast = min(g.first + tok - rt + wt1, g.last);
+      float m_ref = -INFINITY, l = 0.f;
+      bool alive = true;
+      const int step = g.dual ? 1 : 2;
+      int done = 0;  // tiles of this accumulator
+      for (int j = g.dual ? 0 : X; j < g.T; j += step, ++done) {
+        alive = wait(sh.s[X], ns++);
+        alive = __all_sync(0xffffffffu, alive);
+        if (!alive) break;
+        if (any) {
+          ptx::tc_fence_after();
+          uint32_t raw[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(tS + 32 * c, raw[c]);
+          ptx::tmem_ld_wait();
+          float s[TK];
+#pragma unroll
+          for (int e = 0; e < TK; ++e) s[e] = __uint_as_float(raw[e >> 5][e & 31]);
+          const int k = g.key0 + j * TK;
+          const bool open = k + TK - 1 <= wfirst && (p.split.window <= 0 || wlast - k < p.split.window);
+          if (!open) {
+            // visible columns lo .. hi
+            const int hi = valid ? pos - k : -1;
+            const int lo = p.split.window > 0 ? hi - p.split.window + 1 : -1;
+#pragma unroll
+            for (int e = 0; e < TK; ++e) s[e] = e <= hi && e >= lo ? s[e] : -INFINITY;
+          }
+          float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int e = 4; e < TK - 4; e += 8) {
+            m4[0] = fmax3(m4[0], s[e], s[e + 1]);
+            m4[1] = fmax3(m4[1], s[e + 2], s[e + 3]);
+            m4[2] = fmax3(m4[2], s[e + 4], s[e + 5]);
+            m4[3] = fmax3(m4[3], s[e + 6], s[e + 7]);
+          }
+          m4[0] = fmax3(m4[0], s[TK - 4], s[TK - 3]);
+          m4[1] = fmax3(m4[1], s[TK - 2], s[TK - 1]);
+          const float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * p.sl2;
+          float alpha = 1.f;
+          bool resc = false;
+          if (m_ref == -INFINITY) {
+            m_ref = mx;
+          } else if (mx > m_ref + 8.f) {
+            alpha = ptx::ex2(m_ref - mx);
+            m_ref = mx;
+            resc = true;
+          }
+          if (__any_sync(0xffffffffu, resc) && done > 0) {
+            // S_j is complete, so is the PV before it: O holds the tiles so far
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32];
+              ptx::tmem_ld_32x32b_x32(tO + X * 128 + 32 * c, v);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              ptx::tmem_st_32x32b_x32(tO + X * 128 + 32 * c, v);
+            }
+          }
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          const float2 sl2v = make_float2(p.sl2, p.sl2), nmu = make_float2(-mu, -mu);
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                           make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+              const float2 x = __ffma2_rn(make_float2(s[64 * h + e], s[64 * h + e + 1]), sl2v, nmu);
+              const float2 y = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+              acc[(e >> 1) & 3] = __fadd2_rn(acc[(e >> 1) & 3], y);
+              pk[e >> 1] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+            }
+            ptx::tmem_st_32x32b_x32(tS + 32 * h, pk);
+          }
+          const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+          l = l * alpha + ((a01.x + a01.y) + (a23.x + a23.y));
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(&sh.p[X]));
+      }
+      if (!alive) break;
+      // ---- epilogue
+      const int token = it.w.t * 2 * p.TQ + tok;
+      bf16* orow = p.out + ((size_t)(it.w.row0 + token) * p.n_h + it.w.kvh * G + rg) * 128;
+      if (g.T == 0) {  // no row sees a key
+        if (valid && (g.dual || X == 0)) {
+          const uint32_t z[8] = {};
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(orow + 16 * c) = make_uint4(z[0], z[1], z[2], z[3]),
+            *reinterpret_cast<uint4*>(orow + 16 * c + 8) = make_uint4(z[4], z[5], z[6], z[7]);
+        }
+      } else {
+        float wa = 1.f, wb = 0.f;  // weights of the two accumulators (one: its own)
+        if (!g.dual) {
+          // the other half has read what the last exchange left
+          if (no > 0 && !__all_sync(0xffffffffu, wait(sh.of, no - 1))) break;
+          sh.xml[X][r] = make_float2(m_ref, l);
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(&sh.x[X]));
+          if (!__all_sync(0xffffffffu, wait(sh.x[X ^ 1], nx))) break;
+          const float2 other = sh.xml[X ^ 1][r];
+          const float ma = X == 0 ? m_ref : other.x, mb = X == 0 ? other.x : m_ref;
+          const float la = X == 0 ? l : other.y, lb = X == 0 ? other.y : l;
+          m_ref = fmaxf(ma, mb);
+          wa = ma == -INFINITY ? 0.f : ptx::ex2(ma - m_ref);
+          wb = mb == -INFINITY ? 0.f : ptx::ex2(mb - m_ref);
+          l = (la == 0.f ? 0.f : la * wa) + (lb == 0.f ? 0.f : lb * wb);
+        }
+        if (!__all_sync(0xffffffffu, g.dual ? wait(sh.o[X], nd++) : wait(sh.oe, nx++))) break;
+        if (!__all_sync(0xffffffffu, wait(sh.chk[slot], n / kRing))) break;
+        ++no;
+        ptx::tc_fence_after();
+        const bool bad = *reinterpret_cast<const volatile int*>(&it.bad) != 0;
+        const float inv = it.w.slot < 0 ? (l == 0.f ? 0.f : (FP8 ? p.v_scale : 1.f) / l) : (FP8 ? p.v_scale : 1.f);
+        const size_t prow = (size_t)(2 * blockIdx.x + (it.w.slot > 0)) * (2 * p.RT) + (g.dual ? X * p.RT : 0) + r;
+        // two row tiles: all columns of this one's; else half of the columns of both
+        const int c0 = g.dual ? 0 : 2 * X, c1 = g.dual ? 4 : 2 * X + 2;
+        if (any) {
+#pragma unroll 1
+          for (int c = c0; c < c1; ++c) {
+            float o[32];
+            if (g.dual) {
+              uint32_t v[32];
+              ptx::tmem_ld_32x32b_x32(tO + X * 128 + 32 * c, v);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * inv;
+            } else {
+              uint32_t v[32], u[32];
+              ptx::tmem_ld_32x32b_x32(tO + 32 * c, v);
+              ptx::tmem_ld_32x32b_x32(tO + 128 + 32 * c, u);
+              ptx::tmem_ld_wait();
+              // an accumulator without keys (or without a tile) is not read as a number
+              const float fa = wa * inv, fb = wb * inv;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                o[e] = (wa == 0.f ? 0.f : __uint_as_float(v[e]) * fa) + (wb == 0.f ? 0.f : __uint_as_float(u[e]) * fb);
+            }
+            if (!(l > 0.f)) {  // no key, or a score that is not a number
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = l;
+            }
+            if (bad && valid) {
+              float fix[32];
+              for (int e = 0; e < 32; ++e) fix[e] = 0.f;
+              repair<FP8>(p, it, pos, 32 * c, fix);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] += fix[e];
+            }
+            if (valid) {
+              if (it.w.slot < 0) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                  uint4 w;
+                  w.x = pack_bf16(o[e], o[e + 1]);
+                  w.y = pack_bf16(o[e + 2], o[e + 3]);
+                  w.z = pack_bf16(o[e + 4], o[e + 5]);
+                  w.w = pack_bf16(o[e + 6], o[e + 7]);
+                  *reinterpret_cast<uint4*>(orow + 32 * c + e) = w;
+                }
+              } else {
+                float* dst = p.part + prow * 128 + 32 * c;
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              }
+            }
+          }
+          if (it.w.slot >= 0 && valid && (g.dual || X == 0)) p.part_ml[prow] = make_float2(m_ref, l);
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(&sh.of));
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(&sh.ite[slot]));
+    }
+  } else {
+    reg_dec<PL::REG_REST>();
+    if (warp == 8) {
+      // ------------------------------------------------------------------ work list, TMA
+      if (lane == 0) {
+        ptx::prefetch_tmap(&p.q);
+        ptx::prefetch_tmap(&p.k);
+        ptx::prefetch_tmap(&p.v);
+        chunk::Walker walk;
+        walk.init(p.split, sh.start);
+        chunk::Piece w;
+        int at = 0, nq[2] = {0, 0};
+        bool more = walk.next(&w);
+        for (int n = 0;; ++n) {
+          const int slot = n % kRing;
+          if (n >= kRing && !wait(sh.ite[slot], n / kRing - 1)) break;
+          if (!more) w.b = -1;
+          ring[slot].w = w;
+          ring[slot].bad = 0;
+          ptx::mbar_arrive(bar(&sh.itf[slot]));
+          if (!more) break;
+          const chunk::Piece cur = w;
+          const Geometry g(p, cur);
+          more = walk.next(&w);  // its loads are in flight while this item's tiles are issued
+          if (g.T == 0) continue;
+          const int32_t* table = p.table ? p.table + (size_t)cur.b * p.pps + (g.key0 >> 7) : nullptr;
+          auto tile_row = [&](int j) -> int {
+            if (!table) return (cur.b * p.split.n_kv + cur.kvh) * p.split.capacity + g.key0 + j * TK;
+            const int page = table[j];
+            if (page < 0 || page >= p.n_pages) {
+              atomicOr(p.status, DFLASH_DEV_PAGE);
+              return p.oob_row;
+            }
+            return (page * p.split.n_kv + cur.kvh) * TK;
+          };
+          bool stop = false;
+          auto load_q = [&](int X) {
+            if (nq[X] > 0 && !wait(sh.qe[X], nq[X] - 1)) {
+              stop = true;
+              return;
+            }
+            ++nq[X];
+            ptx::mbar_arrive_expect_tx(bar(&sh.qf[X]), (uint32_t)p.RT * 256);
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(sbase + X * TILE + h * HALF, &p.q, bar(&sh.qf[X]), 64 * h, cur.kvh * p.split.G,
+                          cur.row0 + (2 * cur.t + X) * p.TQ);
+          };
+          auto load = [&](const CUtensorMap* map, int row, bool check) {
+            const int s = at % PL::STAGES, u = at / PL::STAGES;
+            if (u > 0 && !wait(sh.ke[s], u - 1)) {
+              stop = true;
+              return;
+            }
+            const uint32_t dst = sbase + PL::OFF_KV + s * PL::LOAD;
+            ptx::mbar_arrive_expect_tx(bar(&sh.kf[s]), PL::LOAD);
+            ptx::tma_load_2d(dst, map, bar(&sh.kf[s]), 0, row);
+            if (!FP8) ptx::tma_load_2d(dst + HALF, map, bar(&sh.kf[s]), 64, row);
+            // the checking warps look at some stages only, so they are told which phase of
+            // the stage's barrier is theirs: the one running now
+            if (!FP8 && check) ptx::mbar_arrive(bar(&sh.vq[s]));
+            ++at;
+          };
+          // tiles in the order of Geometry::k_at / v_at; Q after the first K is under way
+          int row_k = tile_row(0), row_v = row_k, row_k2 = 0;
+          load(&p.k, row_k, false);
+          if (!stop) load_q(0);
+          if (!stop && g.dual) load_q(1);
+          if (g.dual) {
+            for (int j = 0; j < g.T && !stop; ++j) {
+              if (j + 1 < g.T) row_k = tile_row(j + 1);
+              load(&p.v, row_v, g.cut(p, j));
+              if (!stop && j + 1 < g.T) load(&p.k, row_k, false);
+              row_v = row_k;
+            }
+          } else {
+            int row_v2 = 0;  // rows of tiles j, j + 1, j + 2
+            if (g.T > 1 && !stop) {
+              row_v2 = tile_row(1);
+              load(&p.k, row_v2, false);
+            }
+            for (int j = 0; j < g.T && !stop; ++j) {
+              if (j + 2 < g.T) row_k2 = tile_row(j + 2);
+              load(&p.v, row_v, g.cut(p, j));
+              if (!stop && j + 2 < g.T) load(&p.k, row_k2, false);
+              row_v = row_v2;
+              row_v2 = row_k2;
+            }
+          }
+          if (stop) break;
+        }
+        p.merge[blockIdx.x] = walk.merge;
+        // nothing of ours may still be landing in shared memory when the CTA exits
+        for (int X = 0; X < 2; ++X)
+          if (nq[X] > 0) drain(bar(&sh.qf[X]), (nq[X] - 1) & 1, p.status);
+        for (int i = at > PL::STAGES ? at - PL::STAGES : 0; i < at; ++i)
+          drain(bar(&sh.kf[i % PL::STAGES]), (i / PL::STAGES) & 1, p.status);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------------ MMA issue
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, TK);
+        constexpr uint32_t idesc_pv = (FP8 ? idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128)) | (1u << 16);
+        int base = 0, np[2] = {0, 0}, nq[2] = {0, 0}, items = 0;
+        uint32_t chk = 0;  // bf16: phases of the stages' check barriers
+        bool issued = false;
+        for (int n = 0;; ++n) {
+          const int slot = n % kRing;
+          if (!wait(sh.itf[slot], n / kRing)) break;
+          const chunk::Piece w = ring[slot].w;
+          ptx::mbar_arrive(bar(&sh.ite[slot]));
+          if (w.b < 0) break;
+          const Geometry g(p, w);
+          if (g.T == 0) continue;
+          auto ready = [&](int i) -> bool {  // operand tile i of the item is in shared memory
+            const int s = (base + i) % PL::M_STAGES, u = (base + i) / PL::M_STAGES;
+            return FP8 ? wait(sh.vc[s], u) : wait(sh.kf[s], u);
+          };
+          auto tile = [&](int i) { return sbase + PL::OFF_M + ((base + i) % PL::M_STAGES) * TILE; };
+          auto release = [&](int i) {
+            const int s = (base + i) % PL::M_STAGES;
+            ptx::mma_commit(FP8 ? bar(&sh.ce[s]) : bar(&sh.ke[s]));
+          };
+          auto issue_s = [&](int X, int j) {  // S_X = Q K_j^T
+            const uint32_t qa = sbase + (g.dual ? X : 0) * TILE, ka = tile(g.k_at(j));
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = (kk >> 2) * HALF + (kk & 3) * 32;
+              ptx::mma_bf16(tmem + TM_S + X * 128, ptx::smem_desc_sw128(qa + off), ptx::smem_desc_sw128(ka + off),
+                            idesc_s, kk > 0 ? 1u : 0u);
+            }
+            issued = true;
+            ptx::mma_commit(bar(&sh.s[X]));
+          };
+          auto issue_pv = [&](int X, int j, bool first) {  // O_X += P V_j
+            const uint32_t va = tile(g.v_at(j)), pa = tmem + TM_S + X * 128;
+            const int end = g.valid(j);
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              if (kk * 16 < end)
+                mma_ts(tmem + TM_O + X * 128, pa + kk * 8, ptx::smem_desc_sw128_mn(va + kk * 2048, HALF), idesc_pv,
+                       (!first || kk > 0) ? 1u : 0u);
+          };
+          auto checked = [&](int i) -> bool {  // bf16: the tile has been through the check
+            const int s = (base + i) % 5;
+            if (!wait(sh.vc[s], (chk >> s) & 1)) return false;
+            chk ^= 1u << s;
+            return true;
+          };
+          auto ready_v = [&](int j) { return ready(g.v_at(j)) && (FP8 || !g.cut(p, j) || checked(g.v_at(j))); };
+          // first S of each accumulator
+          if (!wait(sh.qf[0], nq[0]++)) break;
+          if (!ready(g.k_at(0))) break;
+          issue_s(0, 0);
+          if (g.dual) {
+            if (g.T == 1) ptx::mma_commit(bar(&sh.qe[0]));
+            if (!wait(sh.qf[1], nq[1]++)) break;
+            issue_s(1, 0);
+            if (g.T == 1) ptx::mma_commit(bar(&sh.qe[1]));
+            release(g.k_at(0));
+          } else {
+            release(g.k_at(0));
+            if (g.T > 1) {
+              if (!ready(g.k_at(1))) break;
+              issue_s(1, 1);
+              release(g.k_at(1));
+            }
+            if (g.T <= 2) ptx::mma_commit(bar(&sh.qe[0]));
+          }
+          bool ok = true;
+          for (int j = 0; j < g.T && ok; ++j) {
+            if (g.dual) {
+#pragma unroll
+              for (int X = 0; X < 2; ++X) {
+                ok = ok && wait(sh.p[X], np[X]++) && (X == 1 || ready_v(j));
+                // the last item's O has been read
+                if (ok && X == 0 && j == 0 && items > 0) ok = wait(sh.of, items - 1);
+                if (!ok) break;
+                issue_pv(X, j, j == 0);
+                if (X == 1) release(g.v_at(j));
+                if (j + 1 < g.T) {
+                  if (X == 0 && !ready(g.k_at(j + 1))) {
+                    ok = false;
+                    break;
+                  }
+                  issue_s(X, j + 1);
+                  if (j + 2 == g.T) ptx::mma_commit(bar(&sh.qe[X]));
+                  if (X == 1) release(g.k_at(j + 1));
+                } else {
+                  ptx::mma_commit(bar(&sh.o[X]));
+                }
+              }
+            } else {
+              const int X = j & 1;
+              ok = wait(sh.p[X], np[X]++) && ready_v(j);
+              if (ok && j == 0 && items > 0) ok = wait(sh.of, items - 1);
+              if (!ok) break;
+              issue_pv(X, j, j < 2);
+              release(g.v_at(j));
+              if (j + 2 < g.T) {
+                if (!ready(g.k_at(j + 2))) {
+                  ok = false;
+                  break;
+                }
+                issue_s(X, j + 2);
+                release(g.k_at(j + 2));
+                if (j + 3 == g.T) ptx::mma_commit(bar(&sh.qe[0]));
+              }
+              if (j + 1 == g.T) ptx::mma_commit(bar(&sh.oe));
+            }
+          }
+          if (!ok) break;
+          ++items;
+          base += 2 * g.T;
+        }
+        // every MMA issued by this thread has finished before tensor memory is released
+        if (issued) {
+          ptx::mma_commit(bar(&sh.fin));
+          drain(bar(&sh.fin), 0, p.status);
+        }
+      }
+    } else if (warp >= PL::W_CHECK) {
+      const int ct = (warp - PL::W_CHECK) * 32 + lane;
+      int base = 0;
+      uint32_t told = 0;  // bf16: phases of vq
+      for (int n = 0;; ++n) {
+        const int slot = n % kRing;
+        if (!__all_sync(0xffffffffu, wait(sh.itf[slot], n / kRing))) break;
+        const chunk::Piece w = ring[slot].w;
+        if (w.b < 0) break;
+        const Geometry g(p, w);
+        bool alive = true;
+        if constexpr (FP8) {
+          // -------------------------------------------------------------- conversion
+          // thread = key row: 8 chunks of 16 codes -> 16 chunks of 8 values, both in the
+          // 128-byte swizzled layout (chunk c of row k at c ^ (k & 7)). Rows no query sees
+          // are zeros; NaN under the mask is taken out of V.
+          const int sw = ct & 7;
+          for (int i = 0; i < 2 * g.T && alive; ++i) {
+            const int a = base + i, s = a % PL::STAGES, cs = a % PL::C_STAGES;
+            bool is_v;
+            int j;
+            if (g.dual) {
+              is_v = i & 1;
+              j = i >> 1;
+            } else {
+              is_v = i >= 2 ? (i & 1) == 0 : false;
+              if (i == 2 * g.T - 1) is_v = true;
+              j = is_v ? (i == 2 * g.T - 1 ? g.T - 1 : (i - 2) >> 1) : (i < 2 ? i : (i + 1) >> 1);
+            }
+            alive = wait(sh.kf[s], a / PL::STAGES) && (a < PL::C_STAGES || wait(sh.ce[cs], a / PL::C_STAGES - 1));
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) break;
+            const uint8_t* src = smem + PL::OFF_KV + s * PL::LOAD + ct * 128;
+            uint8_t* dst = smem + PL::OFF_C + cs * TILE + ct * 128;
+            const bool in = ct < g.valid(j), cut = is_v && g.cut(p, j);
+            bool nan = false;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint4 x = in ? *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
+              if (cut) {
+                uint32_t* word = &x.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  // bytes whose low seven bits are all ones: NaN
+                  const uint32_t m = __vcmpeq4(word[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                  nan |= m != 0;
+                  word[e] &= ~m;
+                }
+              }
+              const uint32_t in4[4] = {x.x, x.y, x.z, x.w};
+              uint32_t out8[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t two = in4[e >> 1] >> (16 * (e & 1));
+                out8[e] = is_v ? e4m3x2_to_f16x2(two) : e4m3x2_to_bf16x2(two);
+              }
+              const int h = c >> 2, c2 = 2 * (c & 3);
+              *reinterpret_cast<uint4*>(dst + h * HALF + ((c2 ^ sw) << 4)) = make_uint4(out8[0], out8[1], out8[2], out8[3]);
+              *reinterpret_cast<uint4*>(dst + h * HALF + (((c2 + 1) ^ sw) << 4)) = make_uint4(out8[4], out8[5], out8[6], out8[7]);
+            }
+            if (nan) *reinterpret_cast<volatile int*>(&ring[slot].bad) = 1;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              ptx::mbar_arrive(bar(&sh.vc[cs]));
+              ptx::mbar_arrive(bar(&sh.ke[s]));
+            }
+          }
+        } else {
+          // -------------------------------------------------------------- check of V
+          // 64 threads over 16-byte chunks (which chunk of its row does not matter, so the
+          // swizzle does not either): x * 0 is 0 but for infinities and NaN. Rows past the
+          // last visible key become zeros up to the end of their K-step.
+          for (int j = 0; j < g.T && alive; ++j) {
+            if (!g.cut(p, j)) continue;
+            const int a = base + g.v_at(j), s = a % PL::STAGES;
+            alive = wait(sh.vq[s], (told >> s) & 1) && wait(sh.kf[s], a / PL::STAGES);
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) break;
+            told ^= 1u << s;
+            uint4* v = reinterpret_cast<uint4*>(smem + PL::OFF_KV + s * PL::LOAD);
+            const int rows = g.valid(j), end = (rows + 15) & ~15;
+            __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
+            const __nv_bfloat162 zero = acc;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint4* vh = v + h * (HALF / 16);
+#pragma unroll 8
+              for (int i = ct; i < rows * 8; i += 64) {
+                const uint4 x = vh[i];
+                const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&x);
+                acc = __hfma2(e[0], zero, acc);
+                acc = __hfma2(e[1], zero, acc);
+                acc = __hfma2(e[2], zero, acc);
+                acc = __hfma2(e[3], zero, acc);
+              }
+              for (int i = rows * 8 + ct; i < end * 8; i += 64) vh[i] = make_uint4(0, 0, 0, 0);
+            }
+            const bool nan = __hisnan(acc.x) || __hisnan(acc.y);
+            if (nan) {  // in the chunks that this thread looked at
+              for (int h = 0; h < 2; ++h)
+                for (int i = ct; i < rows * 8; i += 64) {
+                  uint4 x = v[h * (HALF / 16) + i];
+                  uint32_t* word = &x.x;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)  // halves whose exponent is all ones
+                    word[e] &= ~__vcmpeq2(word[e] & 0x7F807F80u, 0x7F807F80u);
+                  v[h * (HALF / 16) + i] = x;
+                }
+            }
+            if (nan) *reinterpret_cast<volatile int*>(&ring[slot].bad) = 1;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(&sh.vc[s]));
+          }
+        }
+        if (!alive) break;
+        base += 2 * g.T;
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(&sh.chk[slot]));
+          ptx::mbar_arrive(bar(&sh.ite[slot]));
+        }
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool FP8>
+cudaError_t launch(const Params& p, cudaStream_t s) {
+  constexpr size_t smem = Plan<FP8>::OFF_END + sizeof(Tail);
+  static_assert(smem <= 227 * 1024, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(chunk_attn_tc_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  LaunchScope ls_(DFLASH_KERNEL_CHUNK_ATTN, s);
+  chunk_attn_tc_kernel<FP8><<<sm_count(), Plan<FP8>::THREADS, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int chunk_attn_tc_item_rows(int G) { return 2 * (128 / G) * G; }
+
+cudaError_t chunk_attn_tc(const ChunkAttnParams& a, cudaStream_t s) {
+  if (a.d_h != 128 || a.G > 128) return cudaErrorInvalidValue;
+  Params p;
+  memset(&p, 0, sizeof(p));
+  p.TQ = 128 / a.G;
+  p.RT = p.TQ * a.G;
+  p.split = {a.cu_rows, a.kv_lens, a.batch, a.rows, a.n_kv, a.G, a.capacity, a.window, 2 * p.RT, TK, 2};
+  const long long kv_rows = a.block_table ? (long long)a.n_pages * a.n_kv * TK
+                                          : (long long)a.batch * a.n_kv * a.capacity;
+  p.oob_row = (int)kv_rows;
+  if (!encode_3d_bf16(&p.q, a.q, a.rows, a.n_h, a.ld_q, a.G, p.TQ)) return cudaErrorInvalidValue;
+  const bool ok = a.fp8 ? encode_2d_u8(&p.k, a.cache_k, kv_rows, TK) && encode_2d_u8(&p.v, a.cache_v, kv_rows, TK)
+                        : encode_2d_bf16(&p.k, a.cache_k, kv_rows, 128, TK) &&
+                              encode_2d_bf16(&p.v, a.cache_v, kv_rows, 128, TK);
+  if (!ok) return cudaErrorInvalidValue;
+  p.table = a.block_table;
+  p.pps = a.pages_per_seq;
+  p.n_pages = a.n_pages;
+  p.cache_v = a.cache_v;
+  p.out = (bf16*)a.out;
+  p.part = a.part;
+  p.part_ml = a.part_ml;
+  p.merge = a.merge;
+  p.status = a.status;
+  p.n_h = a.n_h;
+  p.sl2 = a.scaling * 1.4426950408889634f * (a.fp8 ? a.k_scale : 1.f);
+  p.v_scale = a.v_scale;
+  p.wait_ns = wait_limit_ns();
+  return a.fp8 ? launch<true>(p, s) : launch<false>(p, s);
+}
+
+}  // namespace dflash
