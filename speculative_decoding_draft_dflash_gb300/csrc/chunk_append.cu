@@ -77,9 +77,7 @@ __global__ void __launch_bounds__(256) chunk_append_bf16_kernel(const ChunkAppen
   const int r = (int)(unit / groups);
   if (r >= p.rows) return;
   const int h0 = (int)(unit - (long long)r * groups) * kHeadsPerUnit + half;
-  int slot, pos;
-  if (!row_live(p, r, &slot, &pos)) return;
-  // the heads' rows
+  // the heads' rows, requested before the slot is known (a skipped row is read in vain)
   uint4 w[kUnroll];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
@@ -88,8 +86,10 @@ __global__ void __launch_bounds__(256) chunk_append_bf16_kernel(const ChunkAppen
     const bf16* src = h < n_q ? (const bf16*)p.q + (size_t)r * p.ld_q + h * 128
                     : h < n_q + p.n_kv ? (const bf16*)p.k + (size_t)r * p.ld_k + (h - n_q) * 128
                                        : (const bf16*)p.v + (size_t)r * p.ld_v + (h - n_q - p.n_kv) * 128;
-    w[i] = reinterpret_cast<const uint4*>(src)[l];
+    w[i] = __ldcs(reinterpret_cast<const uint4*>(src) + l);
   }
+  int slot, pos;
+  if (!row_live(p, r, &slot, &pos)) return;
   // (cos, sin) of this lane's 8 pairs; the upper half-head adds where the lower subtracts
   float c[8], s[8];
   if (p.rope) {

@@ -78,6 +78,7 @@ struct Params {
   unsigned* status;
   int n_h, TQ, RT;       // tokens and rows of a tile
   float sl2, v_scale;    // scaling * log2(e) (fp8: * k_scale); scale of the V codes
+  int out32;             // out is 32-byte aligned
   unsigned long long wait_ns;
 };
 
@@ -162,6 +163,19 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// One lane of the (converged) warp, as the compiler can see: code under it keeps descriptors
+// and addresses in uniform registers. Under `lane == 0` each MMA cost its thread about 110
+// cycles of issue (the tile itself takes 64), and that bound the kernel.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
 }
 
 template <int N> __device__ __forceinline__ void reg_inc() {
@@ -463,20 +477,29 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
             }
             if (valid) {
               if (it.w.slot < 0) {
+                // whole 32-byte sectors where `out` allows
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint4 w;
-                  w.x = pack_bf16(o[e], o[e + 1]);
-                  w.y = pack_bf16(o[e + 2], o[e + 3]);
-                  w.z = pack_bf16(o[e + 4], o[e + 5]);
-                  w.w = pack_bf16(o[e + 6], o[e + 7]);
-                  *reinterpret_cast<uint4*>(orow + 32 * c + e) = w;
+                for (int e = 0; e < 32; e += 16) {
+                  uint32_t w[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[e + 2 * i], o[e + 2 * i + 1]);
+                  bf16* dst = orow + 32 * c + e;
+                  if (p.out32) {
+                    ptx::st_global_v8(dst, w);
+                  } else {
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                  }
                 }
               } else {
                 float* dst = p.part + prow * 128 + 32 * c;
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                for (int e = 0; e < 32; e += 8) {
+                  uint32_t w[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(o[e + i]);
+                  ptx::st_global_v8(dst + e, w);  // the workspace is 256-byte aligned
+                }
               }
             }
           }
@@ -588,67 +611,87 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
       }
     } else if (warp == 9) {
       // ------------------------------------------------------------------ MMA issue
-      if (lane == 0) {
+      {
         constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, TK);
         constexpr uint32_t idesc_pv = (FP8 ? idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128)) | (1u << 16);
         int base = 0, np[2] = {0, 0}, nq[2] = {0, 0}, items = 0;
         uint32_t chk = 0;  // bf16: phases of the stages' check barriers
         bool issued = false;
+        // every lane takes the same way; one issues
+        auto waitw = [&](uint64_t& b, int parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+        auto commit = [&](uint64_t& b) {
+          if (elect_one()) ptx::mma_commit(bar(&b));
+          __syncwarp();
+        };
         for (int n = 0;; ++n) {
           const int slot = n % kRing;
-          if (!wait(sh.itf[slot], n / kRing)) break;
+          if (!waitw(sh.itf[slot], n / kRing)) break;
           const chunk::Piece w = ring[slot].w;
-          ptx::mbar_arrive(bar(&sh.ite[slot]));
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(&sh.ite[slot]));
           if (w.b < 0) break;
           const Geometry g(p, w);
           if (g.T == 0) continue;
           auto ready = [&](int i) -> bool {  // operand tile i of the item is in shared memory
             const int s = (base + i) % PL::M_STAGES, u = (base + i) / PL::M_STAGES;
-            return FP8 ? wait(sh.vc[s], u) : wait(sh.kf[s], u);
+            return FP8 ? waitw(sh.vc[s], u) : waitw(sh.kf[s], u);
           };
           auto tile = [&](int i) { return sbase + PL::OFF_M + ((base + i) % PL::M_STAGES) * TILE; };
           auto release = [&](int i) {
             const int s = (base + i) % PL::M_STAGES;
-            ptx::mma_commit(FP8 ? bar(&sh.ce[s]) : bar(&sh.ke[s]));
+            commit(FP8 ? sh.ce[s] : sh.ke[s]);
           };
           auto issue_s = [&](int X, int j) {  // S_X = Q K_j^T
             const uint32_t qa = sbase + (g.dual ? X : 0) * TILE, ka = tile(g.k_at(j));
             ptx::tc_fence_after();
+            const uint64_t da = ptx::smem_desc_sw128(qa), db = ptx::smem_desc_sw128(ka);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t off = (kk >> 2) * HALF + (kk & 3) * 32;
-              ptx::mma_bf16(tmem + TM_S + X * 128, ptx::smem_desc_sw128(qa + off), ptx::smem_desc_sw128(ka + off),
-                            idesc_s, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                ptx::mma_bf16(tmem + TM_S + X * 128, da + off, db + off, idesc_s, kk > 0 ? 1u : 0u);
+              }
+              ptx::mma_commit(bar(&sh.s[X]));
             }
+            __syncwarp();
             issued = true;
-            ptx::mma_commit(bar(&sh.s[X]));
           };
           auto issue_pv = [&](int X, int j, bool first) {  // O_X += P V_j
             const uint32_t va = tile(g.v_at(j)), pa = tmem + TM_S + X * 128;
             const int end = g.valid(j);
             ptx::tc_fence_after();
+            const uint64_t db = ptx::smem_desc_sw128_mn(va, HALF);
+            if (elect_one()) {
+              if (end > TK - 16) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              if (kk * 16 < end)
-                mma_ts(tmem + TM_O + X * 128, pa + kk * 8, ptx::smem_desc_sw128_mn(va + kk * 2048, HALF), idesc_pv,
-                       (!first || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < 8; ++kk)
+                  mma_ts(tmem + TM_O + X * 128, pa + kk * 8, db + kk * (2048 >> 4), idesc_pv,
+                         (!first || kk > 0) ? 1u : 0u);
+              } else {
+#pragma unroll 1
+                for (int kk = 0; kk * 16 < end; ++kk)
+                  mma_ts(tmem + TM_O + X * 128, pa + kk * 8, db + kk * (2048 >> 4), idesc_pv,
+                         (!first || kk > 0) ? 1u : 0u);
+              }
+            }
+            __syncwarp();
           };
           auto checked = [&](int i) -> bool {  // bf16: the tile has been through the check
             const int s = (base + i) % 5;
-            if (!wait(sh.vc[s], (chk >> s) & 1)) return false;
+            if (!waitw(sh.vc[s], (chk >> s) & 1)) return false;
             chk ^= 1u << s;
             return true;
           };
           auto ready_v = [&](int j) { return ready(g.v_at(j)) && (FP8 || !g.cut(p, j) || checked(g.v_at(j))); };
           // first S of each accumulator
-          if (!wait(sh.qf[0], nq[0]++)) break;
+          if (!waitw(sh.qf[0], nq[0]++)) break;
           if (!ready(g.k_at(0))) break;
           issue_s(0, 0);
           if (g.dual) {
-            if (g.T == 1) ptx::mma_commit(bar(&sh.qe[0]));
-            if (!wait(sh.qf[1], nq[1]++)) break;
+            if (g.T == 1) commit(sh.qe[0]);
+            if (!waitw(sh.qf[1], nq[1]++)) break;
             issue_s(1, 0);
-            if (g.T == 1) ptx::mma_commit(bar(&sh.qe[1]));
+            if (g.T == 1) commit(sh.qe[1]);
             release(g.k_at(0));
           } else {
             release(g.k_at(0));
@@ -657,16 +700,16 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
               issue_s(1, 1);
               release(g.k_at(1));
             }
-            if (g.T <= 2) ptx::mma_commit(bar(&sh.qe[0]));
+            if (g.T <= 2) commit(sh.qe[0]);
           }
           bool ok = true;
           for (int j = 0; j < g.T && ok; ++j) {
             if (g.dual) {
 #pragma unroll
               for (int X = 0; X < 2; ++X) {
-                ok = ok && wait(sh.p[X], np[X]++) && (X == 1 || ready_v(j));
+                ok = ok && waitw(sh.p[X], np[X]++) && (X == 1 || ready_v(j));
                 // the last item's O has been read
-                if (ok && X == 0 && j == 0 && items > 0) ok = wait(sh.of, items - 1);
+                if (ok && X == 0 && j == 0 && items > 0) ok = waitw(sh.of, items - 1);
                 if (!ok) break;
                 issue_pv(X, j, j == 0);
                 if (X == 1) release(g.v_at(j));
@@ -676,16 +719,16 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
                     break;
                   }
                   issue_s(X, j + 1);
-                  if (j + 2 == g.T) ptx::mma_commit(bar(&sh.qe[X]));
+                  if (j + 2 == g.T) commit(sh.qe[X]);
                   if (X == 1) release(g.k_at(j + 1));
                 } else {
-                  ptx::mma_commit(bar(&sh.o[X]));
+                  commit(sh.o[X]);
                 }
               }
             } else {
               const int X = j & 1;
-              ok = wait(sh.p[X], np[X]++) && ready_v(j);
-              if (ok && j == 0 && items > 0) ok = wait(sh.of, items - 1);
+              ok = waitw(sh.p[X], np[X]++) && ready_v(j);
+              if (ok && j == 0 && items > 0) ok = waitw(sh.of, items - 1);
               if (!ok) break;
               issue_pv(X, j, j < 2);
               release(g.v_at(j));
@@ -696,9 +739,9 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
                 }
                 issue_s(X, j + 2);
                 release(g.k_at(j + 2));
-                if (j + 3 == g.T) ptx::mma_commit(bar(&sh.qe[0]));
+                if (j + 3 == g.T) commit(sh.qe[0]);
               }
-              if (j + 1 == g.T) ptx::mma_commit(bar(&sh.oe));
+              if (j + 1 == g.T) commit(sh.oe);
             }
           }
           if (!ok) break;
@@ -707,7 +750,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         }
         // every MMA issued by this thread has finished before tensor memory is released
         if (issued) {
-          ptx::mma_commit(bar(&sh.fin));
+          commit(sh.fin);
           drain(bar(&sh.fin), 0, p.status);
         }
       }
@@ -888,6 +931,7 @@ cudaError_t chunk_attn_tc(const ChunkAttnParams& a, cudaStream_t s) {
   p.n_h = a.n_h;
   p.sl2 = a.scaling * 1.4426950408889634f * (a.fp8 ? a.k_scale : 1.f);
   p.v_scale = a.v_scale;
+  p.out32 = ((uintptr_t)a.out & 31) == 0;
   p.wait_ns = wait_limit_ns();
   return a.fp8 ? launch<true>(p, s) : launch<false>(p, s);
 }

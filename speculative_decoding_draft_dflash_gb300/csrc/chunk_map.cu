@@ -18,9 +18,12 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kPage = 128;
+constexpr int kRows = 4;               // rows of a thread whose lookups overlap
+constexpr int kRefused = -2147483647;  // no shift is that small: lengths and row numbers are >= 0
 
 __global__ void __launch_bounds__(kThreads) chunk_map_kernel(const ChunkMapParams p) {
   extern __shared__ int cu_s[];  // [batch + 1]
+  int* shift_s = cu_s + p.batch + 1;  // [batch]
   __shared__ long long warp_tot[kThreads / 32];
   __shared__ long long carry;
   __shared__ int taken_sum;
@@ -106,43 +109,64 @@ __global__ void __launch_bounds__(kThreads) chunk_map_kernel(const ChunkMapParam
     if (lane == 0 && bad) atomicOr(p.status, bad);
   }
   ptx::cluster_sync();  // the table, the lengths: visible to every CTA of the cluster
-  // rows: the sequence by binary search (the last b with cu[b] <= r)
-  const int n_cta = (int)gridDim.x;
-  for (int r = (int)rank * kThreads + threadIdx.x; r < p.rows; r += n_cta * kThreads) {
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cu_s[mid] <= r) lo = mid; else hi = mid;
-    }
-    int slot = -1, pos = -1;
-    if (r >= cu_s[lo] && r < cu_s[lo + 1] && __ldcg(p.kv_lens + lo) > 0) {
-      pos = p.lens[lo] + (r - cu_s[lo]);
-      if (p.paged) {
-        const int page = __ldcg(p.table + (size_t)lo * p.pages_per_seq + pos / kPage);
-        slot = page >= 0 && page < p.n_pages ? page * kPage + pos % kPage : -1;
-        if (slot < 0) {
-          pos = -1;
-          atomicOr(p.status, DFLASH_DEV_PAGE);
-        }
-      } else {
-        slot = lo * p.capacity + pos;
+  // what a row needs of its sequence: position = row + shift, or refused
+  for (int b = threadIdx.x; b < p.batch; b += kThreads)
+    shift_s[b] = __ldcg(p.kv_lens + b) > 0 ? p.lens[b] - cu_s[b] : kRefused;
+  __syncthreads();
+  // rows, kRows of a thread in flight: the sequence by binary search (the last b with cu[b] <= r)
+  const int n_cta = (int)gridDim.x, stride = n_cta * kThreads;
+  for (int r0 = (int)rank * kThreads + threadIdx.x; r0 < p.rows; r0 += kRows * stride) {
+    int pos[kRows], page[kRows], seq[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const long long r = r0 + (long long)i * stride;
+      pos[i] = page[i] = -1;
+      if (r >= p.rows) continue;
+      int lo = 0, hi = p.batch;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu_s[mid] <= r) lo = mid; else hi = mid;
+      }
+      seq[i] = lo;
+      if (r >= cu_s[lo] && r < cu_s[lo + 1] && shift_s[lo] != kRefused) {
+        pos[i] = (int)r + shift_s[lo];
+        if (p.paged) page[i] = __ldcg(p.table + (size_t)lo * p.pages_per_seq + pos[i] / kPage);
       }
     }
-    p.slots[r] = slot;
-    p.positions[r] = pos;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const long long r = r0 + (long long)i * stride;
+      if (r >= p.rows) continue;
+      int slot = -1;
+      if (pos[i] >= 0) {
+        if (!p.paged) {
+          slot = seq[i] * p.capacity + pos[i];
+        } else if (page[i] >= 0 && page[i] < p.n_pages) {
+          slot = page[i] * kPage + pos[i] % kPage;
+        } else {
+          pos[i] = -1;
+          atomicOr(p.status, DFLASH_DEV_PAGE);
+        }
+      }
+      p.slots[r] = slot;
+      p.positions[r] = pos[i];
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t chunk_map(const ChunkMapParams& p, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(chunk_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (2 * kChunkMaxBatch + 1) * (int)sizeof(int));
+  if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_MAP, s);
   cudaLaunchConfig_t cfg = {};
   // few rows: one CTA expands them as fast as eight would start
   const int ctas = p.rows > 4 * kThreads ? 8 : 1;
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)(p.batch + 1) * sizeof(int);  // at most 32 KB
+  cfg.dynamicSmemBytes = (size_t)(2 * p.batch + 1) * sizeof(int);  // at most 64 KB
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
