@@ -46,7 +46,7 @@ struct ChunkAppendParams {
   long long n_slots;      // units * unit_rows
   int unit_rows;
   int batch, rows, capacity, n_h, n_kv, d_h, table_len;
-  float eps, k_scale, v_scale;
+  float eps, k_inv, v_inv;  // E4M3: codes of x * inv, inv = 1 / scale
   bool fp8;
 };
 cudaError_t chunk_append(int dtype, const ChunkAppendParams& p, cudaStream_t s);

@@ -136,8 +136,8 @@ DFLASH_API dflash_status dflash_chunk_append(const dflash_dims* d, const dflash_
   p.table_len = table_len;
   p.eps = d->eps;
   p.fp8 = kv_fp8(c);
-  p.k_scale = kv_scale(c, layer, 0);
-  p.v_scale = kv_scale(c, layer, 1);
+  p.k_inv = 1.f / kv_scale(c, layer, 0);
+  p.v_inv = 1.f / kv_scale(c, layer, 1);
   return cuda_status(chunk_append(d->dtype, p, stream));
 }
 

@@ -68,26 +68,30 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return w;
 }
 
-__global__ void __launch_bounds__(256) chunk_append_bf16_kernel(const ChunkAppendParams p) {
+// A unit is `span` groups of 8 heads of one row: the slot, the position and the (cos, sin) pairs
+// are fetched once per unit, and the next group's rows are in flight while one is worked on.
+__global__ void __launch_bounds__(256) chunk_append_bf16_kernel(const ChunkAppendParams p, int span) {
   publish_lens(p);
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
   const int n_q = p.q ? p.n_h : 0, heads = n_q + 2 * p.n_kv;
-  const int groups = (heads + kHeadsPerUnit - 1) / kHeadsPerUnit;
+  const int groups = (heads + kHeadsPerUnit - 1) / kHeadsPerUnit, units = (groups + span - 1) / span;
   const long long unit = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int r = (int)(unit / groups);
+  const int r = (int)(unit / units);
   if (r >= p.rows) return;
-  const int h0 = (int)(unit - (long long)r * groups) * kHeadsPerUnit + half;
-  // the heads' rows, requested before the slot is known (a skipped row is read in vain)
-  uint4 w[kUnroll];
+  const int g0 = (int)(unit - (long long)r * units) * span, g1 = min(g0 + span, groups);
+  auto fetch = [&](int g, uint4 (&w)[kUnroll]) {
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    const int h = h0 + 2 * i;
-    if (h >= heads) continue;
-    const bf16* src = h < n_q ? (const bf16*)p.q + (size_t)r * p.ld_q + h * 128
-                    : h < n_q + p.n_kv ? (const bf16*)p.k + (size_t)r * p.ld_k + (h - n_q) * 128
-                                       : (const bf16*)p.v + (size_t)r * p.ld_v + (h - n_q - p.n_kv) * 128;
-    w[i] = __ldcs(reinterpret_cast<const uint4*>(src) + l);
-  }
+    for (int i = 0; i < kUnroll; ++i) {
+      const int h = g * kHeadsPerUnit + half + 2 * i;
+      if (g >= g1 || h >= heads) continue;
+      const bf16* src = h < n_q ? (const bf16*)p.q + (size_t)r * p.ld_q + h * 128
+                      : h < n_q + p.n_kv ? (const bf16*)p.k + (size_t)r * p.ld_k + (h - n_q) * 128
+                                         : (const bf16*)p.v + (size_t)r * p.ld_v + (h - n_q - p.n_kv) * 128;
+      w[i] = __ldcs(reinterpret_cast<const uint4*>(src) + l);
+    }
+  };
+  uint4 next[kUnroll];
+  fetch(g0, next);  // before the slot is known: a skipped row is read in vain
   int slot, pos;
   if (!row_live(p, r, &slot, &pos)) return;
   // (cos, sin) of this lane's 8 pairs; the upper half-head adds where the lower subtracts
@@ -104,46 +108,55 @@ __global__ void __launch_bounds__(256) chunk_append_bf16_kernel(const ChunkAppen
       s[2 * i + 1] = sign * f.w;
     }
   }
+  const int u = slot / p.unit_rows;
+  const size_t cache0 = (size_t)u * p.n_kv * p.unit_rows + (slot - u * p.unit_rows);  // head 0's row
+#pragma unroll 1
+  for (int g = g0; g < g1; ++g) {
+    uint4 w[kUnroll];
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    const int h = h0 + 2 * i;
-    const bool live = h < heads, is_q = h < n_q, is_v = h >= n_q + p.n_kv;
-    float x[8];
-    if (live) unpack8(w[i], x);
-    const void* gamma = is_q ? p.gamma_q : p.gamma_k;
-    if (!is_v && live && gamma) {
-      float ss = 0.f;
+    for (int i = 0; i < kUnroll; ++i) w[i] = next[i];
+    fetch(g + 1, next);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+    for (int i = 0; i < kUnroll; ++i) {
+      const int h = g * kHeadsPerUnit + half + 2 * i;
+      const bool is_q = h < n_q, is_v = h >= n_q + p.n_kv;
+      if (h >= heads) continue;
+      float x[8];
+      unpack8(w[i], x);
+      const void* gamma = is_q ? p.gamma_q : p.gamma_k;
+      if (!is_v && gamma) {
+        float ss = 0.f;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffu << (half * 16), ss, o);
-      const float inv = rsqrtf(ss * (1.f / 128.f) + p.eps);
-      float g[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(gamma) + l), g);
+        for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * g[e];
-    }
-    if (!is_v && live && p.rope) {
+        for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffu << (half * 16), ss, o);
+        const float inv = rsqrtf(ss * (1.f / 128.f) + p.eps);
+        float gm[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(gamma) + l), gm);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = __shfl_xor_sync(0xffffu << (half * 16), x[e], 8);
-        x[e] = x[e] * c[e] + y * s[e];
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * gm[e];
       }
-    }
-    if (!live) continue;
-    if (is_q) {
-      reinterpret_cast<uint4*>((bf16*)p.q_out + (size_t)r * p.n_h * 128 + h * 128)[l] = pack8(x);
-    } else {
-      const size_t at = slot_elem(p, slot, is_v ? h - n_q - p.n_kv : h - n_q) + 8 * l;
-      void* cache = is_v ? p.cache_v : p.cache_k;
-      if (p.fp8) {
-        const float sc = is_v ? p.v_scale : p.k_scale;
-        uint2 code;
-        code.x = e4m3x4(x[0] / sc, x[1] / sc, x[2] / sc, x[3] / sc);
-        code.y = e4m3x4(x[4] / sc, x[5] / sc, x[6] / sc, x[7] / sc);
-        *reinterpret_cast<uint2*>((uint8_t*)cache + at) = code;
+      if (!is_v && p.rope) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float y = __shfl_xor_sync(0xffffu << (half * 16), x[e], 8);
+          x[e] = x[e] * c[e] + y * s[e];
+        }
+      }
+      if (is_q) {
+        reinterpret_cast<uint4*>((bf16*)p.q_out + (size_t)r * p.n_h * 128 + h * 128)[l] = pack8(x);
       } else {
-        *reinterpret_cast<uint4*>((bf16*)cache + at) = pack8(x);
+        const size_t at = (cache0 + (size_t)(is_v ? h - n_q - p.n_kv : h - n_q) * p.unit_rows) * 128 + 8 * l;
+        void* cache = is_v ? p.cache_v : p.cache_k;
+        if (p.fp8) {
+          const float inv = is_v ? p.v_inv : p.k_inv;
+          uint2 code;
+          code.x = e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+          code.y = e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+          *reinterpret_cast<uint2*>((uint8_t*)cache + at) = code;
+        } else {
+          *reinterpret_cast<uint4*>((bf16*)cache + at) = pack8(x);
+        }
       }
     }
   }
@@ -207,14 +220,17 @@ __global__ void __launch_bounds__(256) chunk_append_f32_kernel(const ChunkAppend
 
 cudaError_t chunk_append(int dtype, const ChunkAppendParams& p, cudaStream_t s) {
   const int heads = (p.q ? p.n_h : 0) + 2 * p.n_kv;
-  const int groups = dtype == DFLASH_F32 ? heads : (heads + kHeadsPerUnit - 1) / kHeadsPerUnit;
-  const long long grid = ((long long)p.rows * groups + 7) / 8;
+  // bf16: a warp per 8 heads while the rows alone do not fill the GPU, else up to 24 heads
+  const int groups = (heads + kHeadsPerUnit - 1) / kHeadsPerUnit;
+  const int span = (long long)p.rows * groups > 96ll * sm_count() ? 3 : 1;
+  const int units = dtype == DFLASH_F32 ? heads : (groups + span - 1) / span;
+  const long long grid = ((long long)p.rows * units + 7) / 8;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_APPEND, s);
   if (dtype == DFLASH_F32)
     chunk_append_f32_kernel<<<(unsigned)grid, 256, 0, s>>>(p);
   else
-    chunk_append_bf16_kernel<<<(unsigned)grid, 256, 0, s>>>(p);
+    chunk_append_bf16_kernel<<<(unsigned)grid, 256, 0, s>>>(p, span);
   return cudaGetLastError();
 }
 

@@ -107,7 +107,7 @@ cudaError_t chunk_attn(int dtype, const ChunkAttnParams& p, cudaStream_t s) {
   cudaError_t e = dtype == DFLASH_F32 ? chunk_attn_simt(p, s) : chunk_attn_tc(p, s);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_MERGE, s);
-  const dim3 grid(sm_count(), 4);
+  const dim3 grid(sm_count(), dtype == DFLASH_F32 ? 8 : 16);  // one or two rows per warp
   if (dtype == DFLASH_F32)
     chunk_merge_kernel<float><<<grid, 256, 0, s>>>(p, kSimtRows);
   else

@@ -84,17 +84,28 @@ __global__ void __launch_bounds__(kThreads) chunk_map_kernel(const ChunkMapParam
         p.kv_lens[b] = ok ? (int)total : 0;
         if (p.paged) p.held_out[b] = held + got;
       }
-      // the new pages of this warp's sequences, 32 at a time
-      unsigned with = __ballot_sync(0xffffffffu, got > 0);
-      while (with) {
-        const int l = __ffs(with) - 1;
-        with &= with - 1;
+      // the new pages of this warp's sequences, one per lane: the sequence of the k-th page is
+      // the first whose running count exceeds k
+      int upto = got;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      const int pages = __shfl_sync(0xffffffffu, upto, 31);
+      for (int k0 = 0; k0 < pages; k0 += 32) {
+        const int k = k0 + lane;
+        int l = 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          if (__shfl_sync(0xffffffffu, upto, l + o - 1) <= k) l += o;
+        l = min(l, 31);
         const int n = __shfl_sync(0xffffffffu, got, l), h = __shfl_sync(0xffffffffu, held, l);
-        const long long at = head + __shfl_sync(0xffffffffu, end, l) - n;
-        int32_t* row = p.table + (size_t)(base + warp * 32 + l) * p.pages_per_seq + h;
-        for (int i = lane; i < n; i += 32) {
-          const int id = p.free_pages[at + i];
-          row[i] = id;
+        const int i = k - (__shfl_sync(0xffffffffu, upto, l) - n);
+        const long long at = head + __shfl_sync(0xffffffffu, end, l) - n + i;
+        if (k < pages) {
+          const int id = p.free_pages[at];
+          p.table[(size_t)(base + warp * 32 + l) * p.pages_per_seq + h + i] = id;
           if (id < 0 || id >= p.n_pages) bad |= DFLASH_DEV_PAGE;
         }
       }
