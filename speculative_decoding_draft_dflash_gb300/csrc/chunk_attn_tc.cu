@@ -13,9 +13,8 @@
 // queries, and merges the two halves at the end.
 //
 // One persistent CTA per SM. Warps: 0-3 softmax of A, 4-7 softmax of B (a thread per row, all
-// 128 columns: no exchange between threads), 8 work list and TMA loads, 9 MMA issue, 10-11
-// (bf16) check of the V tiles that the mask cuts, 12-15 (E4M3) conversion of K tiles to bf16
-// and V tiles to f16. Tensor memory: S_A, S_B, O_A, O_B of 128 columns each; P (16 bits)
+// 128 columns: no exchange between threads), 8 work list and TMA loads, 9 and 10 MMA issue for
+// A and B, 11 (bf16) check of the V tiles that the mask cuts, (E4M3) Q to codes and V to f16. Tensor memory: S_A, S_B, O_A, O_B of 128 columns each; P (16 bits)
 // overwrites the first half of its S and is the A operand of the PV product from there.
 //
 // A masked key has weight exactly 0, and its V row must not enter even as 0 * NaN. In tiles
@@ -46,22 +45,23 @@ constexpr int kRing = 4;                  // items in flight between the roles
 
 constexpr uint32_t TM_S = 0, TM_O = 256;  // tensor-memory columns of S_A; O_A (B: + 128)
 
+// Shared memory: Q_A, Q_B, then 160 KB of K / V. bf16: one ring of five 32 KB stages, filled in
+// the order the MMAs take the tiles. E4M3: three 16 KB stages for K (an operand as it is),
+// three for V, and two of V converted to f16.
 template <bool FP8>
 struct Plan {
-  static constexpr int THREADS = FP8 ? 512 : 384;
-  static constexpr int CHECK_WARPS = FP8 ? 4 : 2, W_CHECK = FP8 ? 12 : 10;
-  static constexpr int STAGES = FP8 ? 4 : 5;             // loaded K / V tiles
-  static constexpr uint32_t LOAD = FP8 ? TK * 128 : TILE;
-  static constexpr int C_STAGES = FP8 ? 3 : 0;           // converted tiles
-  static constexpr uint32_t OFF_KV = 2 * TILE;           // after Q_A, Q_B
-  static constexpr uint32_t OFF_C = OFF_KV + STAGES * LOAD;
-  static constexpr uint32_t OFF_END = OFF_C + C_STAGES * TILE;
-  // operand ring the MMA thread reads: the loaded tiles, or the converted ones
-  static constexpr int M_STAGES = FP8 ? C_STAGES : STAGES;
-  static constexpr uint32_t OFF_M = FP8 ? OFF_C : OFF_KV;
+  static constexpr int THREADS = 384, W_CHECK = 11;
+  static constexpr uint32_t LOAD = FP8 ? TK * 128 : TILE;  // a tile as loaded
+  static constexpr int STAGES = FP8 ? 3 : 5;
+  static constexpr int C_STAGES = 2;
+  static constexpr uint32_t OFF_KV = 2 * TILE;
+  static constexpr uint32_t OFF_C = OFF_KV + 6 * (TK * 128);  // E4M3: after K and V
+  static constexpr uint32_t OFF_END = OFF_KV + 5 * TILE;
   // registers: the softmax warpgroups take what the others give back (setmaxnreg draws on the
-  // launch's own registers: 384 x 168 = 256 x 200 + 128 x 104, 512 x 128 = 256 x 168 + 256 x 88)
-  static constexpr int REG_SOFT = FP8 ? 168 : 200, REG_REST = FP8 ? 88 : 104;
+  // launch's own: 384 x 168 = 256 x 200 + 128 x 104)
+  static constexpr int REG_SOFT = 200, REG_REST = 104;
+  // barriers of the stages (Tail::kf, ke): E4M3 V stages follow the K stages
+  static constexpr int V_BAR = FP8 ? 3 : 0;
 };
 
 struct Params {
@@ -89,23 +89,26 @@ struct Item {
 
 // What follows the tiles in shared memory (nothing is declared statically, so that the tiles
 // start at the 1024-byte boundary their swizzle needs and fill the CTA's 227 KB).
+// Barriers that an MMA commit arrives on twice count the two MMA warps: where one warp is the
+// only reader it commits twice.
 struct Tail {
   uint64_t qf[2], qe[2];          // Q tile landed / read by its last S
-  uint64_t kf[5], ke[5];          // K / V tile landed / stage free again
-  uint64_t vq[5];                 // bf16: a V tile to check is on its way to the stage
-  uint64_t vc[5];                 // bf16: V tile checked; E4M3: tile converted
-  uint64_t ce[5];                 // E4M3: converted stage free again
+  uint64_t kf[6], ke[6];          // K / V tile landed / stage free again
+  uint64_t vc[5];                 // bf16: V tile checked; E4M3: V tile converted
+  uint64_t aux[5];                // bf16: a V tile to check is on its way to the stage;
+                                  // E4M3: 0-1 converted stage free again, 2-3 Q codes ready
   uint64_t s[2], p[2];            // S complete; P stored
   uint64_t o[2], oe;              // O complete: of one row tile; of both halves of the keys
   uint64_t of;                    // O read by all softmax warps
   uint64_t x[2];                  // (reference, sum) exchanged
   uint64_t itf[kRing], ite[kRing], chk[kRing];  // item listed / released / V checks done
-  uint64_t fin;
+  uint64_t fin[2];                // all MMAs of a warp complete
   Item ring[kRing];
   chunk::Start start;
   uint32_t tmem_slot;
   int abort_flag;
   float2 xml[2][128];             // (reference, sum) of the even / odd half
+  signed char qexp[2][128];       // E4M3: Q rows are codes of q 2^-qexp
 };
 
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, unsigned* status) {
@@ -137,10 +140,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
   return r;
 }
-// Two E4M3 codes -> bf16x2 (exact: E4M3's range and mantissa lie inside bf16's).
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
-  const float2 f = e4m3x2_value((uint16_t)two);
-  return pack_bf16(f.x, f.y);
+// kind::f8f6f4, both operands E4M3 in shared memory, K = 32.
+__device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 // A from tensor memory, B from shared memory.
@@ -153,9 +161,11 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_
       "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// kind::f16 with f16 operands, and kind::f8f6f4 with E4M3 ones: type fields 0, f32 accumulator.
 constexpr uint32_t idesc_f16_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+constexpr uint32_t idesc_e4m3_f32(int M, int N) { return idesc_f16_f32(M, N); }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z) {
   asm volatile(
@@ -214,6 +224,23 @@ struct Geometry {
   }
 };
 
+// A place in a ring of N stages that are used in order.
+template <int N>
+struct Cursor {
+  int stage = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == N) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ void skip(int n) {
+    stage += n;
+    phase ^= (stage / N) & 1;
+    stage %= N;
+  }
+};
+
 // Adds to 32 columns of an output row what the checking warps took out of the V tiles: the
 // values that are not finite, of keys the row sees.
 template <bool FP8>
@@ -264,27 +291,29 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     sh.abort_flag = 0;
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar(&sh.qf[i]), 1);
-      ptx::mbar_init(bar(&sh.qe[i]), 1);
+      ptx::mbar_init(bar(&sh.qe[i]), i == 0 ? 2 : 1);
       ptx::mbar_init(bar(&sh.s[i]), 1);
       ptx::mbar_init(bar(&sh.p[i]), 4);
       ptx::mbar_init(bar(&sh.o[i]), 1);
       ptx::mbar_init(bar(&sh.x[i]), 4);
     }
-    ptx::mbar_init(bar(&sh.oe), 1);
+    ptx::mbar_init(bar(&sh.oe), 2);
     ptx::mbar_init(bar(&sh.of), 8);
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 6; ++i) {
       ptx::mbar_init(bar(&sh.kf[i]), 1);
-      ptx::mbar_init(bar(&sh.ke[i]), FP8 ? PL::CHECK_WARPS : 1);
-      ptx::mbar_init(bar(&sh.vq[i]), 1);
-      ptx::mbar_init(bar(&sh.vc[i]), PL::CHECK_WARPS);
-      ptx::mbar_init(bar(&sh.ce[i]), 1);
+      ptx::mbar_init(bar(&sh.ke[i]), FP8 && i >= PL::V_BAR ? 1 : 2);
+    }
+    for (int i = 0; i < 5; ++i) {
+      ptx::mbar_init(bar(&sh.vc[i]), 1);
+      ptx::mbar_init(bar(&sh.aux[i]), FP8 && i < 2 ? 2 : 1);
     }
     for (int i = 0; i < kRing; ++i) {
       ptx::mbar_init(bar(&sh.itf[i]), 1);
-      ptx::mbar_init(bar(&sh.ite[i]), 1 + 8 + PL::CHECK_WARPS);
-      ptx::mbar_init(bar(&sh.chk[i]), PL::CHECK_WARPS);
+      ptx::mbar_init(bar(&sh.ite[i]), 2 + 8 + 1);
+      ptx::mbar_init(bar(&sh.chk[i]), 1);
     }
-    ptx::mbar_init(bar(&sh.fin), 1);
+    ptx::mbar_init(bar(&sh.fin[0]), 1);
+    ptx::mbar_init(bar(&sh.fin[1]), 1);
     ptx::fence_mbar_init();
   }
   if (warp == 9) {
@@ -292,7 +321,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     ptx::tmem_relinquish();
   }
   // prefix sums of the work split, in what becomes the K / V ring
-  static_assert(PL::OFF_END - PL::OFF_KV >= 8 * kChunkMaxBatch, "prefix sums");
+  static_assert(5 * TILE >= 8 * kChunkMaxBatch, "prefix sums");
   chunk::locate(p.split, reinterpret_cast<long long*>(smem + PL::OFF_KV), &sh.start, p.status);
   ptx::fence_proxy_async_smem();  // TMA overwrites them
   ptx::tc_fence_before();
@@ -323,7 +352,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
       const int wfirst = g.first + tok - rt + wt0;
       const bool any = __any_sync(0xffffffffu, valid);
       const int wlast = min(g.first + tok - rt + wt1, g.last);
-      float m_ref = -INFINITY, l = 0.f;
+      float m_ref = -INFINITY, l = 0.f, sl2 = p.sl2;
       bool alive = true;
       const int step = g.dual ? 1 : 2;
       int done = 0;  // tiles of this accumulator
@@ -332,6 +361,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         alive = __all_sync(0xffffffffu, alive);
         if (!alive) break;
         if (any) {
+          if (FP8 && done == 0) sl2 = ldexpf(p.sl2, sh.qexp[g.dual ? X : 0][r]);
           ptx::tc_fence_after();
           uint32_t raw[4][32];
 #pragma unroll
@@ -359,7 +389,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
           }
           m4[0] = fmax3(m4[0], s[TK - 4], s[TK - 3]);
           m4[1] = fmax3(m4[1], s[TK - 2], s[TK - 1]);
-          const float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * p.sl2;
+          const float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
           float alpha = 1.f;
           bool resc = false;
           if (m_ref == -INFINITY) {
@@ -382,7 +412,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
             }
           }
           const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-          const float2 sl2v = make_float2(p.sl2, p.sl2), nmu = make_float2(-mu, -mu);
+          const float2 sl2v = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                            make_float2(0.f, 0.f)};
 #pragma unroll
@@ -523,7 +553,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         chunk::Walker walk;
         walk.init(p.split, sh.start);
         chunk::Piece w;
-        int at = 0, nq[2] = {0, 0};
+        int count[2] = {0, 0}, nq[2] = {0, 0};  // tiles (bf16: of both kinds), Q tiles
         bool more = walk.next(&w);
         for (int n = 0;; ++n) {
           const int slot = n % kRing;
@@ -559,43 +589,45 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
               tma_load_3d(sbase + X * TILE + h * HALF, &p.q, bar(&sh.qf[X]), 64 * h, cur.kvh * p.split.G,
                           cur.row0 + (2 * cur.t + X) * p.TQ);
           };
-          auto load = [&](const CUtensorMap* map, int row, bool check) {
-            const int s = at % PL::STAGES, u = at / PL::STAGES;
-            if (u > 0 && !wait(sh.ke[s], u - 1)) {
+          auto load = [&](int which, int row, bool check) {  // 0: a K tile, 1: a V tile
+            int& at = FP8 ? count[which] : count[0];
+            const int s = at % PL::STAGES, u = at / PL::STAGES, bi = s + which * PL::V_BAR;
+            if (u > 0 && !wait(sh.ke[bi], u - 1)) {
               stop = true;
               return;
             }
-            const uint32_t dst = sbase + PL::OFF_KV + s * PL::LOAD;
-            ptx::mbar_arrive_expect_tx(bar(&sh.kf[s]), PL::LOAD);
-            ptx::tma_load_2d(dst, map, bar(&sh.kf[s]), 0, row);
-            if (!FP8) ptx::tma_load_2d(dst + HALF, map, bar(&sh.kf[s]), 64, row);
+            const CUtensorMap* map = which ? &p.v : &p.k;
+            const uint32_t dst = sbase + PL::OFF_KV + bi * PL::LOAD;
+            ptx::mbar_arrive_expect_tx(bar(&sh.kf[bi]), PL::LOAD);
+            ptx::tma_load_2d(dst, map, bar(&sh.kf[bi]), 0, row);
+            if (!FP8) ptx::tma_load_2d(dst + HALF, map, bar(&sh.kf[bi]), 64, row);
             // the checking warps look at some stages only, so they are told which phase of
             // the stage's barrier is theirs: the one running now
-            if (!FP8 && check) ptx::mbar_arrive(bar(&sh.vq[s]));
+            if (!FP8 && check) ptx::mbar_arrive(bar(&sh.aux[s]));
             ++at;
           };
           // tiles in the order of Geometry::k_at / v_at; Q after the first K is under way
           int row_k = tile_row(0), row_v = row_k, row_k2 = 0;
-          load(&p.k, row_k, false);
+          load(0, row_k, false);
           if (!stop) load_q(0);
           if (!stop && g.dual) load_q(1);
           if (g.dual) {
             for (int j = 0; j < g.T && !stop; ++j) {
               if (j + 1 < g.T) row_k = tile_row(j + 1);
-              load(&p.v, row_v, g.cut(p, j));
-              if (!stop && j + 1 < g.T) load(&p.k, row_k, false);
+              load(1, row_v, g.cut(p, j));
+              if (!stop && j + 1 < g.T) load(0, row_k, false);
               row_v = row_k;
             }
           } else {
             int row_v2 = 0;  // rows of tiles j, j + 1, j + 2
             if (g.T > 1 && !stop) {
               row_v2 = tile_row(1);
-              load(&p.k, row_v2, false);
+              load(0, row_v2, false);
             }
             for (int j = 0; j < g.T && !stop; ++j) {
               if (j + 2 < g.T) row_k2 = tile_row(j + 2);
-              load(&p.v, row_v, g.cut(p, j));
-              if (!stop && j + 2 < g.T) load(&p.k, row_k2, false);
+              load(1, row_v, g.cut(p, j));
+              if (!stop && j + 2 < g.T) load(0, row_k2, false);
               row_v = row_v2;
               row_v2 = row_k2;
             }
@@ -606,158 +638,219 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         // nothing of ours may still be landing in shared memory when the CTA exits
         for (int X = 0; X < 2; ++X)
           if (nq[X] > 0) drain(bar(&sh.qf[X]), (nq[X] - 1) & 1, p.status);
-        for (int i = at > PL::STAGES ? at - PL::STAGES : 0; i < at; ++i)
-          drain(bar(&sh.kf[i % PL::STAGES]), (i / PL::STAGES) & 1, p.status);
+        for (int k = 0; k < (FP8 ? 2 : 1); ++k)
+          for (int i = count[k] > PL::STAGES ? count[k] - PL::STAGES : 0; i < count[k]; ++i)
+            drain(bar(&sh.kf[i % PL::STAGES + k * PL::V_BAR]), (i / PL::STAGES) & 1, p.status);
       }
-    } else if (warp == 9) {
+    } else if (warp < PL::W_CHECK) {
       // ------------------------------------------------------------------ MMA issue
-      {
-        constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, TK);
-        constexpr uint32_t idesc_pv = (FP8 ? idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128)) | (1u << 16);
-        int base = 0, np[2] = {0, 0}, nq[2] = {0, 0}, items = 0;
-        uint32_t chk = 0;  // bf16: phases of the stages' check barriers
-        bool issued = false;
-        // every lane takes the same way; one issues
-        auto waitw = [&](uint64_t& b, int parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
-        auto commit = [&](uint64_t& b) {
-          if (elect_one()) ptx::mma_commit(bar(&b));
-          __syncwarp();
-        };
-        for (int n = 0;; ++n) {
-          const int slot = n % kRing;
-          if (!waitw(sh.itf[slot], n / kRing)) break;
-          const chunk::Piece w = ring[slot].w;
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(&sh.ite[slot]));
-          if (w.b < 0) break;
-          const Geometry g(p, w);
-          if (g.T == 0) continue;
-          auto ready = [&](int i) -> bool {  // operand tile i of the item is in shared memory
-            const int s = (base + i) % PL::M_STAGES, u = (base + i) / PL::M_STAGES;
-            return FP8 ? waitw(sh.vc[s], u) : waitw(sh.kf[s], u);
-          };
-          auto tile = [&](int i) { return sbase + PL::OFF_M + ((base + i) % PL::M_STAGES) * TILE; };
-          auto release = [&](int i) {
-            const int s = (base + i) % PL::M_STAGES;
-            commit(FP8 ? sh.ce[s] : sh.ke[s]);
-          };
-          auto issue_s = [&](int X, int j) {  // S_X = Q K_j^T
-            const uint32_t qa = sbase + (g.dual ? X : 0) * TILE, ka = tile(g.k_at(j));
-            ptx::tc_fence_after();
-            const uint64_t da = ptx::smem_desc_sw128(qa), db = ptx::smem_desc_sw128(ka);
-            if (elect_one()) {
+      // Warp 9 issues for A and warp 10 for B, so that what one does between its MMAs (waits,
+      // descriptors) hides behind the other's; in items of one row tile warp 9 issues both
+      // halves and warp 10 only keeps count. Every lane takes the same way, one issues.
+      // Between the two warps nothing orders the tensor core: where an accumulator changes
+      // hands, the new owner waits until the softmax has read the old item's O (sh.of).
+      constexpr uint32_t idesc_s = FP8 ? idesc_e4m3_f32(128, TK) : ptx::idesc_bf16_f32(128, TK);
+      constexpr uint32_t idesc_pv = (FP8 ? idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128)) | (1u << 16);
+      const int me = warp - 9;
+      int np[2] = {0, 0}, nq = 0, nof = 0, items = 0;  // P tiles, Q tiles, waits for sh.of, items
+      Cursor<PL::STAGES> cur;                          // next operand tile (E4M3: K tile)
+      Cursor<PL::C_STAGES> cv;                         // E4M3: next V tile
+      uint32_t chk = 0;                                // bf16: phases of the stages' check barriers
+      bool issued = false, was_pair = true;            // the last item was of two row tiles
+      auto waitw = [&](uint64_t& b, int parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+      const uint64_t dq[2] = {ptx::smem_desc_sw128(sbase), ptx::smem_desc_sw128(sbase + TILE)};
+      const uint64_t dk0 = ptx::smem_desc_sw128(sbase + PL::OFF_KV);
+      const uint64_t dv0 = ptx::smem_desc_sw128_mn(sbase + (FP8 ? PL::OFF_C : PL::OFF_KV), HALF);
+      // the softmax has read O of every item before this one
+      auto wait_of = [&]() -> bool {
+        while (nof < items)
+          if (!waitw(sh.of, nof++)) return false;
+        return true;
+      };
+      // by the elected lane
+      auto mma_s = [&](int X, uint64_t da, uint64_t db) {  // S_X = Q K^T
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                ptx::mma_bf16(tmem + TM_S + X * 128, da + off, db + off, idesc_s, kk > 0 ? 1u : 0u);
-              }
-              ptx::mma_commit(bar(&sh.s[X]));
-            }
-            __syncwarp();
-            issued = true;
-          };
-          auto issue_pv = [&](int X, int j, bool first) {  // O_X += P V_j
-            const uint32_t va = tile(g.v_at(j)), pa = tmem + TM_S + X * 128;
-            const int end = g.valid(j);
-            ptx::tc_fence_after();
-            const uint64_t db = ptx::smem_desc_sw128_mn(va, HALF);
-            if (elect_one()) {
-              if (end > TK - 16) {
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+          if (FP8)  // the codes of Q, then those of their remainders, 32 dims per step
+            mma_f8(tmem + TM_S + X * 128, da + off, db + (((kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+          else
+            ptx::mma_bf16(tmem + TM_S + X * 128, da + off, db + off, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(bar(&sh.s[X]));
+      };
+      auto mma_pv = [&](int X, uint64_t db, int steps, bool first) {  // O_X += P V, 16 keys a step
+        const uint32_t pa = tmem + TM_S + X * 128, o = tmem + TM_O + X * 128;
+        if (steps == 8) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                  mma_ts(tmem + TM_O + X * 128, pa + kk * 8, db + kk * (2048 >> 4), idesc_pv,
-                         (!first || kk > 0) ? 1u : 0u);
-              } else {
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(o, pa + kk * 8, db + kk * (2048 >> 4), idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        } else {
 #pragma unroll 1
-                for (int kk = 0; kk * 16 < end; ++kk)
-                  mma_ts(tmem + TM_O + X * 128, pa + kk * 8, db + kk * (2048 >> 4), idesc_pv,
-                         (!first || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < steps; ++kk)
+            mma_ts(o, pa + kk * 8, db + kk * (2048 >> 4), idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        }
+      };
+      for (int n = 0;; ++n) {
+        const int slot = n % kRing;
+        if (!waitw(sh.itf[slot], n / kRing)) break;
+        const chunk::Piece w = ring[slot].w;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(&sh.ite[slot]));
+        if (w.b < 0) break;
+        const Geometry g(p, w);
+        if (g.T == 0) continue;
+        // a tile of the operand rings, in order: its stage, once it has landed
+        auto take_k = [&](int& st) -> bool {
+          st = cur.stage;
+          const bool ok = waitw(sh.kf[st], cur.phase);
+          cur.next();
+          return ok;
+        };
+        auto take_v = [&](int& st, int j) -> bool {
+          if (FP8) {
+            st = cv.stage;
+            const bool ok = waitw(sh.vc[st], cv.phase);
+            cv.next();
+            return ok;
+          }
+          if (!take_k(st)) return false;
+          if (!g.cut(p, j)) return true;
+          const bool ok = waitw(sh.vc[st], (chk >> st) & 1);  // it has been through the check
+          chk ^= 1u << st;
+          return ok;
+        };
+        auto free_v = [&](int st) { return FP8 ? bar(&sh.aux[st]) : bar(&sh.ke[st]); };
+        if (g.dual) {
+          // ---- this warp's row tile
+          // after an item of one row tile warp 10 joins when that item is settled
+          if (me == 1 && !was_pair && !wait_of()) break;
+          was_pair = true;
+          int ks, vs;
+          if (!(FP8 ? waitw(sh.aux[2 + me], nq) : waitw(sh.qf[me], nq)) || !take_k(ks)) break;
+          ++nq;
+          issued = true;
+          ptx::tc_fence_after();
+          if (elect_one()) {
+            mma_s(me, dq[me], dk0 + ks * (PL::LOAD >> 4));
+            ptx::mma_commit(bar(&sh.ke[ks]));
+          }
+          __syncwarp();
+          bool ok = true;
+          for (int j = 0; j < g.T; ++j) {
+            // what the next PV and S read is waited for first, so that the MMAs follow P at once
+            const bool more = j + 1 < g.T;
+            const int steps = (g.valid(j) + 15) >> 4;
+            ks = 0;
+            ok = take_v(vs, j) && (!more || take_k(ks)) && (j > 0 || wait_of()) && waitw(sh.p[me], np[me]++);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (elect_one()) {
+              mma_pv(me, dv0 + vs * (TILE >> 4), steps, j == 0);
+              if (more) mma_s(me, dq[me], dk0 + ks * (PL::LOAD >> 4));
+              else ptx::mma_commit(bar(&sh.o[me]));
+              ptx::mma_commit(free_v(vs));
+              if (more) ptx::mma_commit(bar(&sh.ke[ks]));
+              // Q (and its exponents) is free with the last S, but not before the softmax has
+              // handed in a tile
+              if (j == max(g.T - 2, 0)) {
+                ptx::mma_commit(bar(&sh.qe[me]));
+                if (me == 0) ptx::mma_commit(bar(&sh.qe[0]));
               }
             }
             __syncwarp();
-          };
-          auto checked = [&](int i) -> bool {  // bf16: the tile has been through the check
-            const int s = (base + i) % 5;
-            if (!waitw(sh.vc[s], (chk >> s) & 1)) return false;
-            chk ^= 1u << s;
-            return true;
-          };
-          auto ready_v = [&](int j) { return ready(g.v_at(j)) && (FP8 || !g.cut(p, j) || checked(g.v_at(j))); };
-          // first S of each accumulator
-          if (!waitw(sh.qf[0], nq[0]++)) break;
-          if (!ready(g.k_at(0))) break;
-          issue_s(0, 0);
-          if (g.dual) {
-            if (g.T == 1) commit(sh.qe[0]);
-            if (!waitw(sh.qf[1], nq[1]++)) break;
-            issue_s(1, 0);
-            if (g.T == 1) commit(sh.qe[1]);
-            release(g.k_at(0));
-          } else {
-            release(g.k_at(0));
-            if (g.T > 1) {
-              if (!ready(g.k_at(1))) break;
-              issue_s(1, 1);
-              release(g.k_at(1));
-            }
-            if (g.T <= 2) commit(sh.qe[0]);
           }
-          bool ok = true;
-          for (int j = 0; j < g.T && ok; ++j) {
-            if (g.dual) {
-#pragma unroll
-              for (int X = 0; X < 2; ++X) {
-                ok = ok && waitw(sh.p[X], np[X]++) && (X == 1 || ready_v(j));
-                // the last item's O has been read
-                if (ok && X == 0 && j == 0 && items > 0) ok = waitw(sh.of, items - 1);
-                if (!ok) break;
-                issue_pv(X, j, j == 0);
-                if (X == 1) release(g.v_at(j));
-                if (j + 1 < g.T) {
-                  if (X == 0 && !ready(g.k_at(j + 1))) {
-                    ok = false;
-                    break;
-                  }
-                  issue_s(X, j + 1);
-                  if (j + 2 == g.T) commit(sh.qe[X]);
-                  if (X == 1) release(g.k_at(j + 1));
-                } else {
-                  commit(sh.o[X]);
-                }
-              }
+          if (!ok) break;
+          np[me ^ 1] += g.T;
+          ++items;
+        } else {
+          // ---- one row tile: even key tiles through A, odd ones through B
+          const bool hand_over = was_pair;
+          was_pair = false;
+          const int T = g.T;
+          if (me == 1) {  // keep count: 2 T operand tiles, the checks among them
+            if (FP8) {
+              cur.skip(T);
+              cv.skip(T);
             } else {
-              const int X = j & 1;
-              ok = waitw(sh.p[X], np[X]++) && ready_v(j);
-              if (ok && j == 0 && items > 0) ok = waitw(sh.of, items - 1);
-              if (!ok) break;
-              issue_pv(X, j, j < 2);
-              release(g.v_at(j));
-              if (j + 2 < g.T) {
-                if (!ready(g.k_at(j + 2))) {
-                  ok = false;
-                  break;
+              for (int i = 0, j = 0; i < 2 * T; ++i, cur.next())
+                if (i == g.v_at(j)) {
+                  if (g.cut(p, j)) chk ^= 1u << cur.stage;
+                  ++j;
                 }
-                issue_s(X, j + 2);
-                release(g.k_at(j + 2));
-                if (j + 3 == g.T) commit(sh.qe[0]);
-              }
-              if (j + 1 == g.T) commit(sh.oe);
             }
+            np[0] += (T + 1) >> 1;
+            np[1] += T >> 1;
+            // The item is not complete without this warp (sh.oe), so the barriers it passes by
+            // are never more than a phase ahead of it.
+            if (!wait_of()) break;
+            if (lane == 0) ptx::mbar_arrive(bar(&sh.oe));
+            ++items;
+            continue;
+          }
+          int ks, vs;
+          if (!(FP8 ? waitw(sh.aux[2], nq) : waitw(sh.qf[0], nq)) || !take_k(ks)) break;
+          ++nq;
+          issued = true;
+          ptx::tc_fence_after();
+          if (elect_one()) {
+            mma_s(0, dq[0], dk0 + ks * (PL::LOAD >> 4));
+            ptx::mma_commit(bar(&sh.ke[ks]));
+            ptx::mma_commit(bar(&sh.ke[ks]));
+          }
+          __syncwarp();
+          if (hand_over && !wait_of()) break;  // B was the other warp's
+          if (T > 1) {
+            if (!take_k(ks)) break;
+            ptx::tc_fence_after();
+            if (elect_one()) {
+              mma_s(1, dq[0], dk0 + ks * (PL::LOAD >> 4));
+              ptx::mma_commit(bar(&sh.ke[ks]));
+              ptx::mma_commit(bar(&sh.ke[ks]));
+            }
+            __syncwarp();
+          }
+          const int q_at = max(T - 3, min(T, 2) - 1);  // as above, for both halves
+          bool ok = true;
+          for (int j = 0; j < T; ++j) {
+            const int X = j & 1;
+            const bool more = j + 2 < T;
+            const int steps = (g.valid(j) + 15) >> 4;
+            ks = 0;
+            ok = take_v(vs, j) && (!more || take_k(ks)) && (j > 0 || wait_of());
+            ok = ok && (X == 0 ? waitw(sh.p[0], np[0]++) : waitw(sh.p[1], np[1]++));
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (elect_one()) {
+              mma_pv(X, dv0 + vs * (TILE >> 4), steps, j < 2);
+              if (more) mma_s(X, dq[0], dk0 + ks * (PL::LOAD >> 4));
+              if (j + 1 == T) ptx::mma_commit(bar(&sh.oe));
+              ptx::mma_commit(free_v(vs));
+              ptx::mma_commit(free_v(vs));
+              if (more) {
+                ptx::mma_commit(bar(&sh.ke[ks]));
+                ptx::mma_commit(bar(&sh.ke[ks]));
+              }
+              if (j == q_at) {
+                ptx::mma_commit(bar(&sh.qe[0]));
+                ptx::mma_commit(bar(&sh.qe[0]));
+              }
+            }
+            __syncwarp();
           }
           if (!ok) break;
           ++items;
-          base += 2 * g.T;
-        }
-        // every MMA issued by this thread has finished before tensor memory is released
-        if (issued) {
-          commit(sh.fin);
-          drain(bar(&sh.fin), 0, p.status);
         }
       }
+      // every MMA issued by this warp has finished before tensor memory is released
+      if (issued) {
+        if (elect_one()) ptx::mma_commit(bar(&sh.fin[me]));
+        __syncwarp();
+        drain(bar(&sh.fin[me]), 0, p.status);
+      }
     } else if (warp >= PL::W_CHECK) {
-      const int ct = (warp - PL::W_CHECK) * 32 + lane;
-      int base = 0;
-      uint32_t told = 0;  // bf16: phases of vq
+      int base = 0, nq[2] = {0, 0};
+      uint32_t told = 0;  // bf16: phases of aux
       for (int n = 0;; ++n) {
         const int slot = n % kRing;
         if (!__all_sync(0xffffffffu, wait(sh.itf[slot], n / kRing))) break;
@@ -766,71 +859,114 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         const Geometry g(p, w);
         bool alive = true;
         if constexpr (FP8) {
-          // -------------------------------------------------------------- conversion
-          // thread = key row: 8 chunks of 16 codes -> 16 chunks of 8 values, both in the
-          // 128-byte swizzled layout (chunk c of row k at c ^ (k & 7)). Rows no query sees
-          // are zeros; NaN under the mask is taken out of V.
-          const int sw = ct & 7;
-          for (int i = 0; i < 2 * g.T && alive; ++i) {
-            const int a = base + i, s = a % PL::STAGES, cs = a % PL::C_STAGES;
-            bool is_v;
-            int j;
-            if (g.dual) {
-              is_v = i & 1;
-              j = i >> 1;
-            } else {
-              is_v = i >= 2 ? (i & 1) == 0 : false;
-              if (i == 2 * g.T - 1) is_v = true;
-              j = is_v ? (i == 2 * g.T - 1 ? g.T - 1 : (i - 2) >> 1) : (i < 2 ? i : (i + 1) >> 1);
-            }
-            alive = wait(sh.kf[s], a / PL::STAGES) && (a < PL::C_STAGES || wait(sh.ce[cs], a / PL::C_STAGES - 1));
-            alive = __all_sync(0xffffffffu, alive);
+          // -------------------------------------------------------------- Q codes
+          // Two E4M3 terms of q 2^-e (e: the row's largest exponent - 7, so that nothing
+          // overflows): the code and the code of its remainder, in place of the bf16 row, each
+          // 128 bytes. q is then kept to about 2^-8 of itself, as a bf16 product would.
+          for (int X = 0; X < (g.T == 0 ? 0 : g.dual ? 2 : 1) && alive; ++X) {
+            alive = __all_sync(0xffffffffu, wait(sh.qf[X], nq[X]++));
             if (!alive) break;
-            const uint8_t* src = smem + PL::OFF_KV + s * PL::LOAD + ct * 128;
-            uint8_t* dst = smem + PL::OFF_C + cs * TILE + ct * 128;
-            const bool in = ct < g.valid(j), cut = is_v && g.cut(p, j);
-            bool nan = false;
+            for (int row = lane; row < p.RT; row += 32) {
+              uint8_t* at = smem + X * TILE + row * 128;
+              const int sw = row & 7;
+              uint4 w[16];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint4 x = in ? *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
-              if (cut) {
-                uint32_t* word = &x.x;
+              for (int c = 0; c < 16; ++c)
+                w[c] = *reinterpret_cast<const uint4*>(at + (c >> 3) * HALF + (((c & 7) ^ sw) << 4));
+              uint32_t top = 0;  // largest magnitude, as the bits of a bf16
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const uint32_t in[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, max(in[e] & 0x7FFFu, (in[e] >> 16) & 0x7FFFu));
+              }
+              // exponent (tiny rows keep 2^-107); a row with infinity or NaN becomes NaN, as
+              // its scores would
+              const int ex = min(max((int)(top >> 7), 20), 254) - 127 - 7;
+              const float mul = top >= 0x7F80u ? NAN : __uint_as_float((uint32_t)(127 - ex) << 23);
+              sh.qexp[X][row] = (signed char)ex;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {  // 16 values per chunk of codes
+                uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  // bytes whose low seven bits are all ones: NaN
-                  const uint32_t m = __vcmpeq4(word[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                  nan |= m != 0;
-                  word[e] &= ~m;
+                  const uint4 v = w[2 * c + (e >> 1)];
+                  const uint32_t p0 = e & 1 ? v.z : v.x, p1 = e & 1 ? v.w : v.y;
+                  e4m3x4_split(__uint_as_float(p0 << 16) * mul, __uint_as_float(p0 & 0xFFFF0000u) * mul,
+                               __uint_as_float(p1 << 16) * mul, __uint_as_float(p1 & 0xFFFF0000u) * mul, hi[e], lo[e]);
+                }
+                *reinterpret_cast<uint4*>(at + ((c ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(at + HALF + ((c ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              }
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(&sh.aux[2 + X]));
+          }
+          // -------------------------------------------------------------- V to f16
+          // A row of codes at a time: 8 chunks of 16 codes -> 16 chunks of 8 values, both in the
+          // 128-byte swizzled layout (chunk c of row k at c ^ (k & 7)). Rows no query sees
+          // are zeros; NaN under the mask is taken out.
+          for (int j = 0; j < g.T && alive; ++j) {
+            const int a = base + j, s = a % PL::STAGES, cs = a % PL::C_STAGES;
+            alive = wait(sh.kf[PL::V_BAR + s], a / PL::STAGES) &&
+                    (a < PL::C_STAGES || wait(sh.aux[cs], a / PL::C_STAGES - 1));
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) break;
+            const bool cut = g.cut(p, j);
+            bool nan = false;
+            for (int row = lane; row < TK; row += 32) {
+              const uint8_t* src = smem + PL::OFF_KV + (PL::V_BAR + s) * PL::LOAD + row * 128;
+              uint8_t* dst = smem + PL::OFF_C + cs * TILE + row * 128;
+              const int sw = row & 7;
+              const bool in = row < g.valid(j);
+              uint4 x[8];
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                x[c] = in ? *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
+              if (cut) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  uint32_t word[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    // bytes whose low seven bits are all ones: NaN
+                    const uint32_t m = __vcmpeq4(word[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                    nan |= m != 0;
+                    word[e] &= ~m;
+                  }
+                  x[c] = make_uint4(word[0], word[1], word[2], word[3]);
                 }
               }
-              const uint32_t in4[4] = {x.x, x.y, x.z, x.w};
-              uint32_t out8[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const uint32_t two = in4[e >> 1] >> (16 * (e & 1));
-                out8[e] = is_v ? e4m3x2_to_f16x2(two) : e4m3x2_to_bf16x2(two);
+              for (int c = 0; c < 8; ++c) {
+                uint8_t* d = dst + (c >> 2) * HALF;
+                const int c2 = 2 * (c & 3);
+                *reinterpret_cast<uint4*>(d + ((c2 ^ sw) << 4)) =
+                    make_uint4(e4m3x2_to_f16x2(x[c].x), e4m3x2_to_f16x2(x[c].x >> 16), e4m3x2_to_f16x2(x[c].y),
+                               e4m3x2_to_f16x2(x[c].y >> 16));
+                *reinterpret_cast<uint4*>(d + (((c2 + 1) ^ sw) << 4)) =
+                    make_uint4(e4m3x2_to_f16x2(x[c].z), e4m3x2_to_f16x2(x[c].z >> 16), e4m3x2_to_f16x2(x[c].w),
+                               e4m3x2_to_f16x2(x[c].w >> 16));
               }
-              const int h = c >> 2, c2 = 2 * (c & 3);
-              *reinterpret_cast<uint4*>(dst + h * HALF + ((c2 ^ sw) << 4)) = make_uint4(out8[0], out8[1], out8[2], out8[3]);
-              *reinterpret_cast<uint4*>(dst + h * HALF + (((c2 + 1) ^ sw) << 4)) = make_uint4(out8[4], out8[5], out8[6], out8[7]);
             }
             if (nan) *reinterpret_cast<volatile int*>(&ring[slot].bad) = 1;
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
               ptx::mbar_arrive(bar(&sh.vc[cs]));
-              ptx::mbar_arrive(bar(&sh.ke[s]));
+              ptx::mbar_arrive(bar(&sh.ke[PL::V_BAR + s]));
             }
           }
         } else {
           // -------------------------------------------------------------- check of V
-          // 64 threads over 16-byte chunks (which chunk of its row does not matter, so the
+          // Lanes over 16-byte chunks (which chunk of its row does not matter, so the
           // swizzle does not either): x * 0 is 0 but for infinities and NaN. Rows past the
           // last visible key become zeros up to the end of their K-step.
           for (int j = 0; j < g.T && alive; ++j) {
             if (!g.cut(p, j)) continue;
-            const int a = base + g.v_at(j), s = a % PL::STAGES;
-            alive = wait(sh.vq[s], (told >> s) & 1) && wait(sh.kf[s], a / PL::STAGES);
+            const int a = 2 * base + g.v_at(j), s = a % PL::STAGES;
+            alive = wait(sh.aux[s], (told >> s) & 1) && wait(sh.kf[s], a / PL::STAGES);
             alive = __all_sync(0xffffffffu, alive);
             if (!alive) break;
             told ^= 1u << s;
@@ -842,7 +978,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
             for (int h = 0; h < 2; ++h) {
               uint4* vh = v + h * (HALF / 16);
 #pragma unroll 8
-              for (int i = ct; i < rows * 8; i += 64) {
+              for (int i = lane; i < rows * 8; i += 32) {
                 const uint4 x = vh[i];
                 const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&x);
                 acc = __hfma2(e[0], zero, acc);
@@ -850,12 +986,12 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
                 acc = __hfma2(e[2], zero, acc);
                 acc = __hfma2(e[3], zero, acc);
               }
-              for (int i = rows * 8 + ct; i < end * 8; i += 64) vh[i] = make_uint4(0, 0, 0, 0);
+              for (int i = rows * 8 + lane; i < end * 8; i += 32) vh[i] = make_uint4(0, 0, 0, 0);
             }
             const bool nan = __hisnan(acc.x) || __hisnan(acc.y);
             if (nan) {  // in the chunks that this thread looked at
               for (int h = 0; h < 2; ++h)
-                for (int i = ct; i < rows * 8; i += 64) {
+                for (int i = lane; i < rows * 8; i += 32) {
                   uint4 x = v[h * (HALF / 16) + i];
                   uint32_t* word = &x.x;
 #pragma unroll
@@ -871,7 +1007,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
           }
         }
         if (!alive) break;
-        base += 2 * g.T;
+        base += g.T;
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive(bar(&sh.chk[slot]));
