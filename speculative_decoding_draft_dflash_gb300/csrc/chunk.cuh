@@ -80,8 +80,8 @@ int chunk_attn_tc_item_rows(int G);
 // ---------------------------------------------------------------------------
 // The work split. The query rows of (sequence b, KV head) are its n new rows times the G
 // query heads that share the KV head, stacked row-major (row = token * G + head). An item
-// is `rows` consecutive stacked rows with all their key tiles; all items lie end to end as
-// one line of costs (a fixed cost each, plus their key tiles) and CTA c works on
+// is `item_rows` consecutive stacked rows with all their key tiles; all items lie end to end as
+// one line of costs (a fixed cost each, plus one per key tile) and CTA c works on
 // [total * c / n, total * (c + 1) / n) of it, cutting items where its share begins or ends.
 // A piece of a cut item leaves an fp32 partial in the workspace (at most two per CTA: the
 // end of an item begun before, and the start of one continued after), so the workspace
@@ -95,8 +95,10 @@ struct Split {
   const int32_t* kv_lens;
   int batch, rows, n_kv, G, capacity, window;
   int item_rows;   // stacked rows of an item
+  int half_rows;   // an item of at most so many rows has the smaller tile cost
   int tile_keys;   // keys of a tile
-  int item_cost;   // fixed cost of an item, in tiles
+  // Cost units: an item, a key tile of an item, and of one of at most half_rows rows.
+  int item_cost, tile_cost, half_cost;
 };
 
 struct Seq {
@@ -134,7 +136,13 @@ __device__ __forceinline__ int2 item_keys(const Split& p, const Seq& s, int t) {
   return make_int2(k0, (last - k0) / p.tile_keys + 1);
 }
 
-__device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
+// Cost units of a key tile of item t, and of the whole item.
+__device__ __forceinline__ int tile_units(const Split& p, const Seq& s, int t) {
+  return (long long)s.n * p.G - (long long)t * p.item_rows > p.half_rows ? p.tile_cost : p.half_cost;
+}
+__device__ __forceinline__ int item_units(const Split& p, const Seq& s, int t) {
+  return p.item_cost + tile_units(p, s, t) * item_keys(p, s, t).y;
+}
 
 // A CTA's share and where it starts.
 struct Start {
@@ -143,34 +151,59 @@ struct Start {
   int ctas;              // CTAs with a share
   int b, kvh, t;         // the item that holds `begin`
   int off;               // cost units of it before `begin`
+  Seq s;                 // its sequence
 };
 
-// CTAs that get a share: at least one unit each.
-__device__ __forceinline__ int active_ctas(long long total, int ctas) {
-  return total < ctas ? (int)total : ctas;
+// CTAs that get a share: large enough for a key tile, so that every CTA inside a cut item has
+// at least one.
+__device__ __forceinline__ int active_ctas(const Split& p, long long total, int ctas) {
+  const int least = max(p.tile_cost, p.half_cost);
+  return total >= (long long)ctas * least ? ctas : max(1, (int)(total / least));
 }
 __device__ __forceinline__ long long bound(long long total, int active, int c) {
   return total * c / active;
 }
 
-// Run by all threads of the CTA; `cost` is shared scratch of p.batch long longs (free again
-// after the call and a __syncthreads), `st` shared.
-__device__ __forceinline__ void locate(const Split& p, long long* cost, Start* st, unsigned* status) {
+// Shared scratch of locate: every sequence and its cost.
+constexpr size_t kLocateBytes = sizeof(Seq) + sizeof(long long);  // per sequence
+
+// Run by all threads of the CTA; `scratch` is 16-byte aligned shared memory of kLocateBytes per
+// sequence (free again after the call and a __syncthreads), `st` shared. A thread per sequence
+// reads the lengths and adds up its items; sequences of many items get a warp.
+__device__ __forceinline__ void locate(const Split& p, void* scratch, Start* st, unsigned* status) {
+  long long* cost = reinterpret_cast<long long*>(scratch);
+  Seq* seq = reinterpret_cast<Seq*>(cost + p.batch);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  constexpr int kFew = 3;
   unsigned bad = 0;
-  for (int b = warp; b < p.batch; b += nw) {
+  bool many = false;
+  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
     const Seq s = load_seq(p, b, &bad);
+    seq[b] = s;
     const int items = n_items(p, s);
     long long sum = 0;
-    for (int t = lane; t < items; t += 32) sum += p.item_cost + item_keys(p, s, t).y;
-    if (items > 1) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    if (lane == 0) cost[b] = sum * p.n_kv;
+    for (int t = 0; t < min(items, kFew); ++t) sum += item_units(p, s, t);
+    cost[b] = items <= kFew ? sum * p.n_kv : -1;
+    many |= items > kFew;
   }
-  if (bad && lane == 0 && blockIdx.x == 0) atomicOr(status, bad);
-  __syncthreads();
+  if (bad && blockIdx.x == 0) atomicOr(status, bad);
+  if (__syncthreads_or(many)) {
+    for (int base = warp * 32; base < p.batch; base += nw * 32) {
+      unsigned left = __ballot_sync(0xffffffffu, base + lane < p.batch && cost[base + lane] < 0);
+      while (left) {
+        const int b = base + __ffs(left) - 1;
+        left &= left - 1;
+        const Seq s = seq[b];
+        const int items = n_items(p, s);
+        long long sum = 0;
+        for (int t = lane; t < items; t += 32) sum += item_units(p, s, t);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) cost[b] = sum * p.n_kv;
+      }
+    }
+    __syncthreads();
+  }
   if (warp == 0) {  // prefix sums, in place
     long long carry = 0;
     for (int base = 0; base < p.batch; base += 32) {
@@ -185,7 +218,7 @@ __device__ __forceinline__ void locate(const Split& p, long long* cost, Start* s
       carry = __shfl_sync(0xffffffffu, v, 31);
     }
     __syncwarp();
-    const int active = active_ctas(carry, (int)gridDim.x);
+    const int active = active_ctas(p, carry, (int)gridDim.x);
     const int c = (int)blockIdx.x;
     const long long begin = c < active ? bound(carry, active, c) : carry;
     const long long end = c < active ? bound(carry, active, c + 1) : carry;
@@ -197,22 +230,21 @@ __device__ __forceinline__ void locate(const Split& p, long long* cost, Start* s
         if (cost[mid] > begin) hi = mid; else lo = mid + 1;
       }
       b = lo;
-      unsigned ignored = 0;
-      const Seq s = load_seq(p, b, &ignored);
+      const Seq s = seq[b];
       const long long before = b > 0 ? cost[b - 1] : 0;
       const long long per_head = (cost[b] - before) / p.n_kv;
       const int kvh = (int)((begin - before) / per_head);
       long long rest = begin - before - per_head * kvh;
-      // the item: scan their costs 32 at a time
+      // the item: scan their costs 32 at a time (their sum fits 31 bits: the capacity does)
       const int items = n_items(p, s);
       int t = 0;
       for (int base = 0; base < items; base += 32) {
         const int u = base + lane;
-        const int w = u < items ? p.item_cost + item_keys(p, s, u).y : 0;
-        long long v = w;
+        const int w = u < items ? item_units(p, s, u) : 0;
+        int v = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long x = __shfl_up_sync(0xffffffffu, v, o);
+          const int x = __shfl_up_sync(0xffffffffu, v, o);
           if (lane >= o) v += x;
         }
         const unsigned past = __ballot_sync(0xffffffffu, v > rest);
@@ -228,6 +260,7 @@ __device__ __forceinline__ void locate(const Split& p, long long* cost, Start* s
         st->kvh = kvh;
         st->t = t;
         st->off = (int)rest;
+        st->s = s;
       }
     }
     if (lane == 0) {
@@ -269,8 +302,7 @@ struct Walker {
     t = st.t;
     off = st.off;
     merge = make_int4(0, 0, 0, 0);
-    unsigned ignored = 0;
-    if (at < end) s = load_seq(p, b, &ignored);
+    s = st.s;
   }
 
   __device__ bool next(Piece* w) {
@@ -287,9 +319,10 @@ struct Walker {
         continue;
       }
       const int2 keys = item_keys(p, s, t);
-      const int whole = p.item_cost + keys.y;
+      const int tu = tile_units(p, s, t), whole = p.item_cost + tu * keys.y;
       const int take = (int)min((long long)(whole - off), end - at);
-      const int tile0 = max(0, off - p.item_cost), tile1 = max(0, off + take - p.item_cost);
+      const int tile0 = max(0, off - p.item_cost) / tu;
+      const int tile1 = off + take == whole ? keys.y : max(0, off + take - p.item_cost) / tu;
       const bool starts = off == 0;
       w->b = b;
       w->kvh = kvh;

@@ -25,8 +25,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_simt_kernel(const Chun
   float* Ps = Vs + TK * LD;
   __shared__ chunk::Start start;
   const chunk::Split split = {p.cu_rows, p.kv_lens, p.batch, p.rows, p.n_kv, p.G, p.capacity,
-                              p.window, RI, TK, 1};
-  chunk::locate(split, reinterpret_cast<long long*>(smem4), &start, p.status);
+                              p.window, RI, RI, TK, 1, 1, 1};
+  chunk::locate(split, smem4, &start, p.status);
   chunk::Walker walk;
   walk.init(split, start);
   __syncthreads();
@@ -168,8 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_simt_kernel(const Chun
 
 template <int DP>
 cudaError_t launch(const ChunkAttnParams& p, cudaStream_t s) {
-  const int smem = (int)sizeof(float) * ((RI + 2 * TK) * (DP + 4) + RI * (TK + 4));
-  static_assert((64 + 128) * (DP + 4) * 4 + 64 * 68 * 4 >= 8 * kChunkMaxBatch, "prefix sums");
+  const int tiles = (int)sizeof(float) * ((RI + 2 * TK) * (DP + 4) + RI * (TK + 4));
+  const int scratch = (int)(chunk::kLocateBytes * p.batch);
+  const int smem = tiles > scratch ? tiles : scratch;
   cudaError_t e = cudaFuncSetAttribute(chunk_attn_simt_kernel<DP>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

@@ -320,9 +320,14 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     ptx::tmem_alloc(ptx::smem_u32(&sh.tmem_slot), 512);
     ptx::tmem_relinquish();
   }
-  // prefix sums of the work split, in what becomes the K / V ring
-  static_assert(5 * TILE >= 8 * kChunkMaxBatch, "prefix sums");
-  chunk::locate(p.split, reinterpret_cast<long long*>(smem + PL::OFF_KV), &sh.start, p.status);
+  if (warp == 8 && lane == 0) {
+    ptx::prefetch_tmap(&p.q);
+    ptx::prefetch_tmap(&p.k);
+    ptx::prefetch_tmap(&p.v);
+  }
+  // the work split, in what becomes the K / V ring
+  static_assert(5 * TILE >= chunk::kLocateBytes * kChunkMaxBatch, "scratch of the work split");
+  chunk::locate(p.split, smem + PL::OFF_KV, &sh.start, p.status);
   ptx::fence_proxy_async_smem();  // TMA overwrites them
   ptx::tc_fence_before();
   __syncthreads();
@@ -373,11 +378,18 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
           const int k = g.key0 + j * TK;
           const bool open = k + TK - 1 <= wfirst && (p.split.window <= 0 || wlast - k < p.split.window);
           if (!open) {
-            // visible columns lo .. hi
-            const int hi = valid ? pos - k : -1;
-            const int lo = p.split.window > 0 ? hi - p.split.window + 1 : -1;
+            // visible columns lo .. hi, as bits of four words
+            const int hi = valid ? min(pos - k, TK - 1) : -1;
+            const int lo = p.split.window > 0 ? max(pos - k - p.split.window + 1, 0) : 0;
 #pragma unroll
-            for (int e = 0; e < TK; ++e) s[e] = e <= hi && e >= lo ? s[e] : -INFINITY;
+            for (int c = 0; c < 4; ++c) {
+              const int h = hi - 32 * c, l0 = lo - 32 * c;
+              uint32_t m = h < 0 ? 0u : h >= 31 ? 0xffffffffu : (2u << h) - 1u;
+              m &= l0 <= 0 ? 0xffffffffu : l0 > 31 ? 0u : 0xffffffffu << l0;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                s[32 * c + e] = m & (1u << e) ? s[32 * c + e] : -INFINITY;
+            }
           }
           float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -488,11 +500,15 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
               ptx::tmem_ld_32x32b_x32(tO + 32 * c, v);
               ptx::tmem_ld_32x32b_x32(tO + 128 + 32 * c, u);
               ptx::tmem_ld_wait();
-              // an accumulator without keys (or without a tile) is not read as a number
               const float fa = wa * inv, fb = wb * inv;
+              if (__all_sync(0xffffffffu, wa != 0.f && wb != 0.f)) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                o[e] = (wa == 0.f ? 0.f : __uint_as_float(v[e]) * fa) + (wb == 0.f ? 0.f : __uint_as_float(u[e]) * fb);
+                for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * fa + __uint_as_float(u[e]) * fb;
+              } else {  // an accumulator without keys (or without a tile) is not read as a number
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  o[e] = (wa == 0.f ? 0.f : __uint_as_float(v[e]) * fa) + (wb == 0.f ? 0.f : __uint_as_float(u[e]) * fb);
+              }
             }
             if (!(l > 0.f)) {  // no key, or a score that is not a number
 #pragma unroll
@@ -547,9 +563,6 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     if (warp == 8) {
       // ------------------------------------------------------------------ work list, TMA
       if (lane == 0) {
-        ptx::prefetch_tmap(&p.q);
-        ptx::prefetch_tmap(&p.k);
-        ptx::prefetch_tmap(&p.v);
         chunk::Walker walk;
         walk.init(p.split, sh.start);
         chunk::Piece w;
@@ -1046,7 +1059,8 @@ cudaError_t chunk_attn_tc(const ChunkAttnParams& a, cudaStream_t s) {
   memset(&p, 0, sizeof(p));
   p.TQ = 128 / a.G;
   p.RT = p.TQ * a.G;
-  p.split = {a.cu_rows, a.kv_lens, a.batch, a.rows, a.n_kv, a.G, a.capacity, a.window, 2 * p.RT, TK, 2};
+  p.split = {a.cu_rows, a.kv_lens, a.batch, a.rows, a.n_kv, a.G, a.capacity, a.window, 2 * p.RT, p.RT, TK,
+             a.fp8 ? 14 : 8, a.fp8 ? 6 : 4, 3};
   const long long kv_rows = a.block_table ? (long long)a.n_pages * a.n_kv * TK
                                           : (long long)a.batch * a.n_kv * a.capacity;
   p.oob_row = (int)kv_rows;
