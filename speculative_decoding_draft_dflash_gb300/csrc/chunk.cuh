@@ -95,8 +95,9 @@ struct Split {
   const int32_t* kv_lens;
   int batch, rows, n_kv, G, capacity, window;
   int item_rows;   // stacked rows of an item
+  int item_tokens; // of whole tokens: how many, else 0
   int half_rows;   // an item of at most so many rows has the smaller tile cost
-  int tile_keys;   // keys of a tile
+  int tile_keys;   // keys of a tile (a power of two)
   // Cost units: an item, a key tile of an item, and of one of at most half_rows rows.
   int item_cost, tile_cost, half_cost;
 };
@@ -121,24 +122,31 @@ __device__ __forceinline__ Seq load_seq(const Split& p, int b, unsigned* bad) {
   return s;
 }
 
+// (rows * G fits 31 bits)
 __device__ __forceinline__ int n_items(const Split& p, const Seq& s) {
-  return (int)(((long long)s.n * p.G + p.item_rows - 1) / p.item_rows);
+  return (int)((unsigned)(s.n * p.G + p.item_rows - 1) / (unsigned)p.item_rows);
+}
+
+// Positions of the first and the last row of item t.
+__device__ __forceinline__ int2 item_span(const Split& p, const Seq& s, int t) {
+  const int p0 = s.kv - s.n;
+  if (p.item_tokens > 0) return make_int2(p0 + t * p.item_tokens, p0 + min((t + 1) * p.item_tokens, s.n) - 1);
+  const unsigned r0 = t * p.item_rows, r1 = min(r0 + p.item_rows, (unsigned)(s.n * p.G));
+  return make_int2(p0 + (int)(r0 / (unsigned)p.G), p0 + (int)((r1 - 1) / (unsigned)p.G));
 }
 
 // First key (a multiple of the tile) and key tiles of item t.
 __device__ __forceinline__ int2 item_keys(const Split& p, const Seq& s, int t) {
-  const long long r0 = (long long)t * p.item_rows;
-  const long long r1 = min(r0 + p.item_rows, (long long)s.n * p.G);
-  const int first = s.kv - s.n + (int)(r0 / p.G), last = s.kv - s.n + (int)((r1 - 1) / p.G);
-  if (last < 0) return make_int2(0, 0);
+  const int2 span = item_span(p, s, t);
+  if (span.y < 0) return make_int2(0, 0);
   int k0 = 0;
-  if (p.window > 0 && first >= p.window) k0 = (first - p.window + 1) / p.tile_keys * p.tile_keys;
-  return make_int2(k0, (last - k0) / p.tile_keys + 1);
+  if (p.window > 0 && span.x >= p.window) k0 = (span.x - p.window + 1) & ~(p.tile_keys - 1);
+  return make_int2(k0, (int)((unsigned)(span.y - k0) / (unsigned)p.tile_keys) + 1);
 }
 
 // Cost units of a key tile of item t, and of the whole item.
 __device__ __forceinline__ int tile_units(const Split& p, const Seq& s, int t) {
-  return (long long)s.n * p.G - (long long)t * p.item_rows > p.half_rows ? p.tile_cost : p.half_cost;
+  return s.n * p.G - t * p.item_rows > p.half_rows ? p.tile_cost : p.half_cost;
 }
 __device__ __forceinline__ int item_units(const Split& p, const Seq& s, int t) {
   return p.item_cost + tile_units(p, s, t) * item_keys(p, s, t).y;

@@ -160,6 +160,7 @@ DFLASH_API dflash_status dflash_chunk_attn(const dflash_dims* d, const dflash_kv
   if (st != DFLASH_OK) return st;
   // key rows of one layer are addressed with 32-bit row numbers
   if (cache_slots(c) * d->n_kv > 0x7fffffffll || c->capacity > (1 << 28)) return DFLASH_ERR_UNSUPPORTED;
+  if ((long long)ch->rows * (d->n_h / d->n_kv) > (1 << 30)) return DFLASH_ERR_UNSUPPORTED;
   if (sliding_window < 0 || !(scaling < INFINITY)) return DFLASH_ERR_INVALID_ARG;
   if (ch->rows == 0) return DFLASH_OK;
   const long long qw = (long long)d->n_h * d->d_h;

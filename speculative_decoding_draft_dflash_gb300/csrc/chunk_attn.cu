@@ -24,6 +24,7 @@ template <> __device__ __forceinline__ void store2(bf16* p, float a, float b) {
 template <typename T>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkAttnParams p, int rows_max) {
   constexpr bool kNatural = sizeof(T) == 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's partials
   const int4 m = p.merge[blockIdx.x];
   if (m.w == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -107,12 +108,18 @@ cudaError_t chunk_attn(int dtype, const ChunkAttnParams& p, cudaStream_t s) {
   cudaError_t e = dtype == DFLASH_F32 ? chunk_attn_simt(p, s) : chunk_attn_tc(p, s);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_MERGE, s);
-  const dim3 grid(sm_count(), dtype == DFLASH_F32 ? 8 : 16);  // one or two rows per warp
-  if (dtype == DFLASH_F32)
-    chunk_merge_kernel<float><<<grid, 256, 0, s>>>(p, kSimtRows);
-  else
-    chunk_merge_kernel<bf16><<<grid, 256, 0, s>>>(p, chunk_attn_tc_item_rows(p.G));
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sm_count(), dtype == DFLASH_F32 ? 8 : 16);  // one or two rows per warp
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // scheduled as SMs fall free
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return dtype == DFLASH_F32
+             ? cudaLaunchKernelEx(&cfg, chunk_merge_kernel<float>, p, kSimtRows)
+             : cudaLaunchKernelEx(&cfg, chunk_merge_kernel<bf16>, p, chunk_attn_tc_item_rows(p.G));
 }
 
 }  // namespace dflash

@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_simt_kernel(const Chun
   float* Ps = Vs + TK * LD;
   __shared__ chunk::Start start;
   const chunk::Split split = {p.cu_rows, p.kv_lens, p.batch, p.rows, p.n_kv, p.G, p.capacity,
-                              p.window, RI, RI, TK, 1, 1, 1};
+                              p.window, RI, 0, RI, TK, 1, 1, 1};
   chunk::locate(split, smem4, &start, p.status);
   chunk::Walker walk;
   walk.init(split, start);

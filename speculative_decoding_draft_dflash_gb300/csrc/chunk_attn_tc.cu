@@ -89,8 +89,7 @@ struct Item {
 
 // What follows the tiles in shared memory (nothing is declared statically, so that the tiles
 // start at the 1024-byte boundary their swizzle needs and fill the CTA's 227 KB).
-// Barriers that an MMA commit arrives on twice count the two MMA warps: where one warp is the
-// only reader it commits twice.
+// Barriers of what both MMA warps read (K and V stages, Q_A, oe) count the two.
 struct Tail {
   uint64_t qf[2], qe[2];          // Q tile landed / read by its last S
   uint64_t kf[6], ke[6];          // K / V tile landed / stage free again
@@ -241,6 +240,42 @@ struct Cursor {
   }
 };
 
+// A row of Q to E4M3: two terms of q 2^-e (e: the row's largest exponent - 7, so that nothing
+// overflows), the code and the code of its remainder, in place of the bf16 row, each 128 bytes
+// of the swizzled layout. q is then kept to about 2^-8 of itself, as a bf16 product would.
+// Returns e.
+__device__ __noinline__ int q_codes(uint8_t* tile, int row) {
+  uint8_t* at = tile + row * 128;
+  const int sw = row & 7;
+  uint4 w[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) w[c] = *reinterpret_cast<const uint4*>(at + (c >> 3) * HALF + (((c & 7) ^ sw) << 4));
+  uint32_t top = 0;  // largest magnitude, as the bits of a bf16
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const uint32_t in[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, max(in[e] & 0x7FFFu, (in[e] >> 16) & 0x7FFFu));
+  }
+  // tiny rows keep 2^-107; a row with infinity or NaN becomes NaN, as its scores would
+  const int ex = min(max((int)(top >> 7), 20), 254) - 127 - 7;
+  const float mul = top >= 0x7F80u ? NAN : __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {  // 16 values per chunk of codes
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint4 v = w[2 * c + (e >> 1)];
+      const uint32_t p0 = e & 1 ? v.z : v.x, p1 = e & 1 ? v.w : v.y;
+      e4m3x4_split(__uint_as_float(p0 << 16) * mul, __uint_as_float(p0 & 0xFFFF0000u) * mul,
+                   __uint_as_float(p1 << 16) * mul, __uint_as_float(p1 & 0xFFFF0000u) * mul, hi[e], lo[e]);
+    }
+    *reinterpret_cast<uint4*>(at + ((c ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(at + HALF + ((c ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  return ex;
+}
+
 // Adds to 32 columns of an output row what the checking warps took out of the V tiles: the
 // values that are not finite, of keys the row sees.
 template <bool FP8>
@@ -305,7 +340,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     }
     for (int i = 0; i < 5; ++i) {
       ptx::mbar_init(bar(&sh.vc[i]), 1);
-      ptx::mbar_init(bar(&sh.aux[i]), FP8 && i < 2 ? 2 : 1);
+      ptx::mbar_init(bar(&sh.aux[i]), !FP8 ? 1 : i < 2 ? 2 : 4);
     }
     for (int i = 0; i < kRing; ++i) {
       ptx::mbar_init(bar(&sh.itf[i]), 1);
@@ -325,6 +360,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     ptx::prefetch_tmap(&p.k);
     ptx::prefetch_tmap(&p.v);
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be scheduled
   // the work split, in what becomes the K / V ring
   static_assert(5 * TILE >= chunk::kLocateBytes * kChunkMaxBatch, "scratch of the work split");
   chunk::locate(p.split, smem + PL::OFF_KV, &sh.start, p.status);
@@ -343,7 +379,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     const int G = p.split.G, rt = r / G, rg = r - rt * G;     // token and head of this row
     const int wt0 = ((warp & 3) * 32) / G;                    // tokens of the warp's first and last row
     const int wt1 = ((warp & 3) * 32 + 31) / G;
-    int ns = 0, no = 0, nd = 0, nx = 0;  // tiles, items with keys; of two row tiles, of one
+    int ns = 0, no = 0, nd = 0, nx = 0, nq = 0;  // tiles, items with keys; of two row tiles, of one
     for (int n = 0;; ++n) {
       const int slot = n % kRing;
       if (!__all_sync(0xffffffffu, wait(sh.itf[slot], n / kRing))) break;
@@ -361,6 +397,16 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
       bool alive = true;
       const int step = g.dual ? 1 : 2;
       int done = 0;  // tiles of this accumulator
+      if (FP8 && g.T > 0) {
+        if (g.dual) {
+          if (!__all_sync(0xffffffffu, wait(sh.qf[X], nq))) break;
+          if (valid) sh.qexp[X][r] = (signed char)q_codes(smem + X * TILE, r);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(&sh.aux[2 + X]));
+        }
+        nq += X == 0 || g.dual;
+      }
       for (int j = g.dual ? 0 : X; j < g.T; j += step, ++done) {
         alive = wait(sh.s[X], ns++);
         alive = __all_sync(0xffffffffu, alive);
@@ -658,18 +704,17 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     } else if (warp < PL::W_CHECK) {
       // ------------------------------------------------------------------ MMA issue
       // Warp 9 issues for A and warp 10 for B, so that what one does between its MMAs (waits,
-      // descriptors) hides behind the other's; in items of one row tile warp 9 issues both
-      // halves and warp 10 only keeps count. Every lane takes the same way, one issues.
-      // Between the two warps nothing orders the tensor core: where an accumulator changes
-      // hands, the new owner waits until the softmax has read the old item's O (sh.of).
+      // descriptors) hides behind the other's. Both go through every operand tile in the order
+      // of the ring; a tile that only the other needs is freed at once. Every lane takes the
+      // same way, one issues.
       constexpr uint32_t idesc_s = FP8 ? idesc_e4m3_f32(128, TK) : ptx::idesc_bf16_f32(128, TK);
       constexpr uint32_t idesc_pv = (FP8 ? idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128)) | (1u << 16);
       const int me = warp - 9;
-      int np[2] = {0, 0}, nq = 0, nof = 0, items = 0;  // P tiles, Q tiles, waits for sh.of, items
+      int np = 0, nq[2] = {0, 0}, nof = 0, items = 0;  // P tiles, Q tiles, waits for sh.of, items
       Cursor<PL::STAGES> cur;                          // next operand tile (E4M3: K tile)
       Cursor<PL::C_STAGES> cv;                         // E4M3: next V tile
       uint32_t chk = 0;                                // bf16: phases of the stages' check barriers
-      bool issued = false, was_pair = true;            // the last item was of two row tiles
+      bool issued = false;
       auto waitw = [&](uint64_t& b, int parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
       const uint64_t dq[2] = {ptx::smem_desc_sw128(sbase), ptx::smem_desc_sw128(sbase + TILE)};
       const uint64_t dk0 = ptx::smem_desc_sw128(sbase + PL::OFF_KV);
@@ -720,7 +765,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
           cur.next();
           return ok;
         };
-        auto take_v = [&](int& st, int j) -> bool {
+        auto take_v = [&](int& st, int j, bool own) -> bool {
           if (FP8) {
             st = cv.stage;
             const bool ok = waitw(sh.vc[st], cv.phase);
@@ -729,131 +774,82 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
           }
           if (!take_k(st)) return false;
           if (!g.cut(p, j)) return true;
-          const bool ok = waitw(sh.vc[st], (chk >> st) & 1);  // it has been through the check
+          const bool ok = !own || waitw(sh.vc[st], (chk >> st) & 1);  // it has been through the check
           chk ^= 1u << st;
           return ok;
         };
         auto free_v = [&](int st) { return FP8 ? bar(&sh.aux[st]) : bar(&sh.ke[st]); };
-        if (g.dual) {
-          // ---- this warp's row tile
-          // after an item of one row tile warp 10 joins when that item is settled
-          if (me == 1 && !was_pair && !wait_of()) break;
-          was_pair = true;
-          int ks, vs;
-          if (!(FP8 ? waitw(sh.aux[2 + me], nq) : waitw(sh.qf[me], nq)) || !take_k(ks)) break;
-          ++nq;
-          issued = true;
-          ptx::tc_fence_after();
-          if (elect_one()) {
-            mma_s(me, dq[me], dk0 + ks * (PL::LOAD >> 4));
-            ptx::mma_commit(bar(&sh.ke[ks]));
-          }
-          __syncwarp();
-          bool ok = true;
-          for (int j = 0; j < g.T; ++j) {
-            // what the next PV and S read is waited for first, so that the MMAs follow P at once
-            const bool more = j + 1 < g.T;
-            const int steps = (g.valid(j) + 15) >> 4;
-            ks = 0;
-            ok = take_v(vs, j) && (!more || take_k(ks)) && (j > 0 || wait_of()) && waitw(sh.p[me], np[me]++);
-            if (!ok) break;
+        // this warp's tiles: all of them, or every other one
+        const int mine = g.dual ? g.T : (g.T + 1 - me) >> 1;
+        const int X = g.dual ? me : 0;  // its Q tile
+        const int ahead = g.dual ? 1 : 2;
+        // Q_A is waited for and released by both warps in every item, so that neither is ever
+        // more than a phase away from its barriers
+        bool ok = FP8 ? waitw(sh.aux[2], nq[0]) : waitw(sh.qf[0], nq[0]);
+        ++nq[0];
+        if (X == 1) {
+          ok = ok && (FP8 ? waitw(sh.aux[3], nq[1]) : waitw(sh.qf[1], nq[1]));
+          ++nq[1];
+        }
+        issued = issued || mine > 0;
+        int ks = 0, vs;
+        // first S of each accumulator: of K_0, and of K_1 for the odd half
+        for (int j = 0; j < min(ahead, g.T) && ok; ++j) {
+          ok = take_k(ks);
+          if (!ok) break;
+          if (g.dual || j == me) {
             ptx::tc_fence_after();
             if (elect_one()) {
-              mma_pv(me, dv0 + vs * (TILE >> 4), steps, j == 0);
-              if (more) mma_s(me, dq[me], dk0 + ks * (PL::LOAD >> 4));
-              else ptx::mma_commit(bar(&sh.o[me]));
-              ptx::mma_commit(free_v(vs));
-              if (more) ptx::mma_commit(bar(&sh.ke[ks]));
-              // Q (and its exponents) is free with the last S, but not before the softmax has
-              // handed in a tile
-              if (j == max(g.T - 2, 0)) {
-                ptx::mma_commit(bar(&sh.qe[me]));
-                if (me == 0) ptx::mma_commit(bar(&sh.qe[0]));
-              }
+              mma_s(me, dq[X], dk0 + ks * (PL::LOAD >> 4));
+              ptx::mma_commit(bar(&sh.ke[ks]));
             }
             __syncwarp();
+          } else if (lane == 0) {
+            ptx::mbar_arrive(bar(&sh.ke[ks]));
           }
-          if (!ok) break;
-          np[me ^ 1] += g.T;
-          ++items;
-        } else {
-          // ---- one row tile: even key tiles through A, odd ones through B
-          const bool hand_over = was_pair;
-          was_pair = false;
-          const int T = g.T;
-          if (me == 1) {  // keep count: 2 T operand tiles, the checks among them
-            if (FP8) {
-              cur.skip(T);
-              cv.skip(T);
-            } else {
-              for (int i = 0, j = 0; i < 2 * T; ++i, cur.next())
-                if (i == g.v_at(j)) {
-                  if (g.cut(p, j)) chk ^= 1u << cur.stage;
-                  ++j;
-                }
+        }
+        int done = 0;
+        for (int j = 0; j < g.T && ok; ++j) {
+          // what the next PV and S read is waited for first, so that the MMAs follow P at once
+          const bool own = g.dual || (j & 1) == me, more = j + ahead < g.T;
+          const int steps = (g.valid(j) + 15) >> 4;
+          ks = 0;
+          ok = take_v(vs, j, own) && (!more || take_k(ks));
+          if (!own) {
+            if (ok && lane == 0) {
+              ptx::mbar_arrive(free_v(vs));
+              if (more) ptx::mbar_arrive(bar(&sh.ke[ks]));
             }
-            np[0] += (T + 1) >> 1;
-            np[1] += T >> 1;
-            // The item is not complete without this warp (sh.oe), so the barriers it passes by
-            // are never more than a phase ahead of it.
-            if (!wait_of()) break;
-            if (lane == 0) ptx::mbar_arrive(bar(&sh.oe));
-            ++items;
             continue;
           }
-          int ks, vs;
-          if (!(FP8 ? waitw(sh.aux[2], nq) : waitw(sh.qf[0], nq)) || !take_k(ks)) break;
-          ++nq;
-          issued = true;
+          ok = ok && (done > 0 || wait_of()) && waitw(sh.p[me], np++);
+          if (!ok) break;
           ptx::tc_fence_after();
           if (elect_one()) {
-            mma_s(0, dq[0], dk0 + ks * (PL::LOAD >> 4));
-            ptx::mma_commit(bar(&sh.ke[ks]));
-            ptx::mma_commit(bar(&sh.ke[ks]));
+            mma_pv(me, dv0 + vs * (TILE >> 4), steps, done == 0);
+            if (more) mma_s(me, dq[X], dk0 + ks * (PL::LOAD >> 4));
+            if (done + 1 == mine) ptx::mma_commit(bar(g.dual ? &sh.o[me] : &sh.oe));
+            ptx::mma_commit(free_v(vs));
+            if (more) ptx::mma_commit(bar(&sh.ke[ks]));
+            // Q (and its exponents) is free with this warp's last S, but not before its softmax
+            // warps have handed in a tile
+            if (done == max(mine - 2, 0)) {
+              ptx::mma_commit(bar(&sh.qe[0]));
+              if (X == 1) ptx::mma_commit(bar(&sh.qe[1]));
+            }
           }
           __syncwarp();
-          if (hand_over && !wait_of()) break;  // B was the other warp's
-          if (T > 1) {
-            if (!take_k(ks)) break;
-            ptx::tc_fence_after();
-            if (elect_one()) {
-              mma_s(1, dq[0], dk0 + ks * (PL::LOAD >> 4));
-              ptx::mma_commit(bar(&sh.ke[ks]));
-              ptx::mma_commit(bar(&sh.ke[ks]));
-            }
-            __syncwarp();
-          }
-          const int q_at = max(T - 3, min(T, 2) - 1);  // as above, for both halves
-          bool ok = true;
-          for (int j = 0; j < T; ++j) {
-            const int X = j & 1;
-            const bool more = j + 2 < T;
-            const int steps = (g.valid(j) + 15) >> 4;
-            ks = 0;
-            ok = take_v(vs, j) && (!more || take_k(ks)) && (j > 0 || wait_of());
-            ok = ok && (X == 0 ? waitw(sh.p[0], np[0]++) : waitw(sh.p[1], np[1]++));
-            if (!ok) break;
-            ptx::tc_fence_after();
-            if (elect_one()) {
-              mma_pv(X, dv0 + vs * (TILE >> 4), steps, j < 2);
-              if (more) mma_s(X, dq[0], dk0 + ks * (PL::LOAD >> 4));
-              if (j + 1 == T) ptx::mma_commit(bar(&sh.oe));
-              ptx::mma_commit(free_v(vs));
-              ptx::mma_commit(free_v(vs));
-              if (more) {
-                ptx::mma_commit(bar(&sh.ke[ks]));
-                ptx::mma_commit(bar(&sh.ke[ks]));
-              }
-              if (j == q_at) {
-                ptx::mma_commit(bar(&sh.qe[0]));
-                ptx::mma_commit(bar(&sh.qe[0]));
-              }
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
-          ++items;
+          ++done;
         }
+        if (!ok) break;
+        if (mine == 0) {  // nothing in this item: it is still not complete without this warp
+          if (!wait_of()) break;
+          if (lane == 0) {
+            ptx::mbar_arrive(bar(&sh.oe));
+            ptx::mbar_arrive(bar(&sh.qe[0]));
+          }
+        }
+        ++items;
       }
       // every MMA issued by this warp has finished before tensor memory is released
       if (issued) {
@@ -862,7 +858,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         drain(bar(&sh.fin[me]), 0, p.status);
       }
     } else if (warp >= PL::W_CHECK) {
-      int base = 0, nq[2] = {0, 0};
+      int base = 0, nq = 0;
       uint32_t told = 0;  // bf16: phases of aux
       for (int n = 0;; ++n) {
         const int slot = n % kRing;
@@ -873,48 +869,15 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         bool alive = true;
         if constexpr (FP8) {
           // -------------------------------------------------------------- Q codes
-          // Two E4M3 terms of q 2^-e (e: the row's largest exponent - 7, so that nothing
-          // overflows): the code and the code of its remainder, in place of the bf16 row, each
-          // 128 bytes. q is then kept to about 2^-8 of itself, as a bf16 product would.
-          for (int X = 0; X < (g.T == 0 ? 0 : g.dual ? 2 : 1) && alive; ++X) {
-            alive = __all_sync(0xffffffffu, wait(sh.qf[X], nq[X]++));
-            if (!alive) break;
-            for (int row = lane; row < p.RT; row += 32) {
-              uint8_t* at = smem + X * TILE + row * 128;
-              const int sw = row & 7;
-              uint4 w[16];
-#pragma unroll
-              for (int c = 0; c < 16; ++c)
-                w[c] = *reinterpret_cast<const uint4*>(at + (c >> 3) * HALF + (((c & 7) ^ sw) << 4));
-              uint32_t top = 0;  // largest magnitude, as the bits of a bf16
-#pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const uint32_t in[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, max(in[e] & 0x7FFFu, (in[e] >> 16) & 0x7FFFu));
-              }
-              // exponent (tiny rows keep 2^-107); a row with infinity or NaN becomes NaN, as
-              // its scores would
-              const int ex = min(max((int)(top >> 7), 20), 254) - 127 - 7;
-              const float mul = top >= 0x7F80u ? NAN : __uint_as_float((uint32_t)(127 - ex) << 23);
-              sh.qexp[X][row] = (signed char)ex;
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {  // 16 values per chunk of codes
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint4 v = w[2 * c + (e >> 1)];
-                  const uint32_t p0 = e & 1 ? v.z : v.x, p1 = e & 1 ? v.w : v.y;
-                  e4m3x4_split(__uint_as_float(p0 << 16) * mul, __uint_as_float(p0 & 0xFFFF0000u) * mul,
-                               __uint_as_float(p1 << 16) * mul, __uint_as_float(p1 & 0xFFFF0000u) * mul, hi[e], lo[e]);
-                }
-                *reinterpret_cast<uint4*>(at + ((c ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(at + HALF + ((c ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              }
-            }
+          // (of two row tiles each softmax warpgroup makes its own)
+          if (g.T > 0) alive = __all_sync(0xffffffffu, wait(sh.qf[0], nq++));
+          if (!alive) break;
+          if (g.T > 0 && !g.dual) {
+            const int rows = min(p.RT, (g.last - g.first + 1) * p.split.G);
+            for (int row = lane; row < rows; row += 32) sh.qexp[0][row] = (signed char)q_codes(smem, row);
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(&sh.aux[2 + X]));
+            if (lane < 4) ptx::mbar_arrive(bar(&sh.aux[2]));
           }
           // -------------------------------------------------------------- V to f16
           // A row of codes at a time: 8 chunks of 16 codes -> 16 chunks of 8 values, both in the
@@ -1059,7 +1022,7 @@ cudaError_t chunk_attn_tc(const ChunkAttnParams& a, cudaStream_t s) {
   memset(&p, 0, sizeof(p));
   p.TQ = 128 / a.G;
   p.RT = p.TQ * a.G;
-  p.split = {a.cu_rows, a.kv_lens, a.batch, a.rows, a.n_kv, a.G, a.capacity, a.window, 2 * p.RT, p.RT, TK,
+  p.split = {a.cu_rows, a.kv_lens, a.batch, a.rows, a.n_kv, a.G, a.capacity, a.window, 2 * p.RT, 2 * p.TQ, p.RT, TK,
              a.fp8 ? 14 : 8, a.fp8 ? 6 : 4, 3};
   const long long kv_rows = a.block_table ? (long long)a.n_pages * a.n_kv * TK
                                           : (long long)a.batch * a.n_kv * a.capacity;
