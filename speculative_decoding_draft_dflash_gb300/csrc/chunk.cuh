@@ -60,8 +60,8 @@ struct ChunkAttnParams {
   const void* cache_v;
   const int32_t* block_table; // paged, or null
   void* out;                  // [rows][n_h * d_h]
-  float* part;                // [2 * CTAs][kItemRows][d_h]: partial outputs, not normalised
-  float2* part_ml;            // [2 * CTAs][kItemRows]: (maximum, sum) of each partial row
+  float* part;                // [2 * CTAs] partial items (rows x d_h), not normalised
+  float2* part_ml;            // [2 * CTAs][rows of an item]: (maximum, sum) of each partial row
   int4* merge;                // [CTAs]: {sequence, KV head, item, pieces} of the range cut in CTA c
   unsigned* status;
   int batch, rows, n_h, n_kv, d_h, G, capacity, pages_per_seq, n_pages, window;

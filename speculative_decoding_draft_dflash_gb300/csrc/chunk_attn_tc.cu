@@ -100,6 +100,7 @@ struct Tail {
   uint64_t o[2], oe;              // O complete: of one row tile; of both halves of the keys
   uint64_t of;                    // O read by all softmax warps
   uint64_t x[2];                  // (reference, sum) exchanged
+  uint64_t turn[2];               // two row tiles: the other MMA warp has issued its block
   uint64_t itf[kRing], ite[kRing], chk[kRing];  // item listed / released / V checks done
   uint64_t fin[2];                // all MMAs of a warp complete
   Item ring[kRing];
@@ -117,6 +118,27 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, unsigned* s
       atomicOr(status, DFLASH_DEV_TIMEOUT);
       return;
     }
+  }
+}
+
+// Wait of a whole warp on a barrier phase, with the same answer in every lane: false when the CTA
+// was told to stop or the limit ran out (which tells it). A phase that is already complete
+// costs one test and one vote; the clock and the abort flag are looked at every 64 tests.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
+                                          uint64_t limit_ns) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (int i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    if (i & 63) continue;
+    const uint64_t t = ptx::globaltimer();
+    if (i == 64) t0 = t;
+    const bool late = t - t0 > limit_ns;
+    if (late) {
+      *abort_flag = 1;
+      atomicOr(status, DFLASH_DEV_TIMEOUT);
+    }
+    if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
   }
 }
 
@@ -276,6 +298,34 @@ __device__ __noinline__ int q_codes(uint8_t* tile, int row) {
   return ex;
 }
 
+// A V tile of E4M3 codes to f16, by one warp: 16 codes at a time, one 16-byte chunk to two, both in the 128-byte swizzled layout (chunk c of row k at c ^ (k & 7)). Rows from `rows`
+// on (that no query sees) are zeros; where `cut`, NaN is taken out. Returns whether there was one.
+__device__ __forceinline__ bool convert_v(const uint8_t* src, uint8_t* dst, int lane, int rows, bool cut) {
+  bool nan = false;
+#pragma unroll 8
+  for (int u = lane; u < TK * 8; u += 32) {
+    const int row = u & (TK - 1), c = u / TK, sw = row & 7;
+    uint4 x = row < rows ? *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
+    if (cut) {
+      uint32_t word[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // bytes whose low seven bits are all ones
+        const uint32_t m = __vcmpeq4(word[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        nan |= m != 0;
+        word[e] &= ~m;
+      }
+      x = make_uint4(word[0], word[1], word[2], word[3]);
+    }
+    uint8_t* d = dst + row * 128 + (c >> 2) * HALF;
+    const int c2 = 2 * (c & 3);
+    *reinterpret_cast<uint4*>(d + ((c2 ^ sw) << 4)) = make_uint4(
+        e4m3x2_to_f16x2(x.x), e4m3x2_to_f16x2(x.x >> 16), e4m3x2_to_f16x2(x.y), e4m3x2_to_f16x2(x.y >> 16));
+    *reinterpret_cast<uint4*>(d + (((c2 + 1) ^ sw) << 4)) = make_uint4(
+        e4m3x2_to_f16x2(x.z), e4m3x2_to_f16x2(x.z >> 16), e4m3x2_to_f16x2(x.w), e4m3x2_to_f16x2(x.w >> 16));
+  }
+  return nan;
+}
+
 // Adds to 32 columns of an output row what the checking warps took out of the V tiles: the
 // values that are not finite, of keys the row sees.
 template <bool FP8>
@@ -318,8 +368,11 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     return;
   }
   auto bar = [](uint64_t* b) { return ptx::smem_u32(b); };
-  auto wait = [&](uint64_t& b, int parity) {
+  auto wait = [&](uint64_t& b, int parity) {  // one thread
     return ptx::mbar_wait(ptx::smem_u32(&b), (uint32_t)(parity & 1), &sh.abort_flag, p.status, p.wait_ns);
+  };
+  auto waitw = [&](uint64_t& b, int parity) {  // a whole warp
+    return wait_warp(ptx::smem_u32(&b), (uint32_t)(parity & 1), &sh.abort_flag, p.status, p.wait_ns);
   };
 
   if (threadIdx.x == 0) {
@@ -331,6 +384,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
       ptx::mbar_init(bar(&sh.p[i]), 4);
       ptx::mbar_init(bar(&sh.o[i]), 1);
       ptx::mbar_init(bar(&sh.x[i]), 4);
+      ptx::mbar_init(bar(&sh.turn[i]), 1);
     }
     ptx::mbar_init(bar(&sh.oe), 2);
     ptx::mbar_init(bar(&sh.of), 8);
@@ -382,7 +436,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     int ns = 0, no = 0, nd = 0, nx = 0, nq = 0;  // tiles, items with keys; of two row tiles, of one
     for (int n = 0;; ++n) {
       const int slot = n % kRing;
-      if (!__all_sync(0xffffffffu, wait(sh.itf[slot], n / kRing))) break;
+      if (!waitw(sh.itf[slot], n / kRing)) break;
       const Item& it = ring[slot];
       if (it.w.b < 0) break;
       const Geometry g(p, it.w);
@@ -399,7 +453,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
       int done = 0;  // tiles of this accumulator
       if (FP8 && g.T > 0) {
         if (g.dual) {
-          if (!__all_sync(0xffffffffu, wait(sh.qf[X], nq))) break;
+          if (!waitw(sh.qf[X], nq)) break;
           if (valid) sh.qexp[X][r] = (signed char)q_codes(smem + X * TILE, r);
           ptx::fence_proxy_async_smem();
           __syncwarp();
@@ -408,8 +462,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         nq += X == 0 || g.dual;
       }
       for (int j = g.dual ? 0 : X; j < g.T; j += step, ++done) {
-        alive = wait(sh.s[X], ns++);
-        alive = __all_sync(0xffffffffu, alive);
+        alive = waitw(sh.s[X], ns++);
         if (!alive) break;
         if (any) {
           if (FP8 && done == 0) sl2 = ldexpf(p.sl2, sh.qexp[g.dual ? X : 0][r]);
@@ -509,11 +562,11 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         float wa = 1.f, wb = 0.f;  // weights of the two accumulators (one: its own)
         if (!g.dual) {
           // the other half has read what the last exchange left
-          if (no > 0 && !__all_sync(0xffffffffu, wait(sh.of, no - 1))) break;
+          if (no > 0 && !waitw(sh.of, no - 1)) break;
           sh.xml[X][r] = make_float2(m_ref, l);
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar(&sh.x[X]));
-          if (!__all_sync(0xffffffffu, wait(sh.x[X ^ 1], nx))) break;
+          if (!waitw(sh.x[X ^ 1], nx)) break;
           const float2 other = sh.xml[X ^ 1][r];
           const float ma = X == 0 ? m_ref : other.x, mb = X == 0 ? other.x : m_ref;
           const float la = X == 0 ? l : other.y, lb = X == 0 ? other.y : l;
@@ -522,13 +575,14 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
           wb = mb == -INFINITY ? 0.f : ptx::ex2(mb - m_ref);
           l = (la == 0.f ? 0.f : la * wa) + (lb == 0.f ? 0.f : lb * wb);
         }
-        if (!__all_sync(0xffffffffu, g.dual ? wait(sh.o[X], nd++) : wait(sh.oe, nx++))) break;
-        if (!__all_sync(0xffffffffu, wait(sh.chk[slot], n / kRing))) break;
+        if (!(g.dual ? waitw(sh.o[X], nd++) : waitw(sh.oe, nx++))) break;
+        if (!waitw(sh.chk[slot], n / kRing)) break;
         ++no;
         ptx::tc_fence_after();
         const bool bad = *reinterpret_cast<const volatile int*>(&it.bad) != 0;
         const float inv = it.w.slot < 0 ? (l == 0.f ? 0.f : (FP8 ? p.v_scale : 1.f) / l) : (FP8 ? p.v_scale : 1.f);
-        const size_t prow = (size_t)(2 * blockIdx.x + (it.w.slot > 0)) * (2 * p.RT) + (g.dual ? X * p.RT : 0) + r;
+        const int irow = (g.dual ? X * p.RT : 0) + r;
+        const size_t pslot = (size_t)(2 * blockIdx.x + (it.w.slot > 0)) * (2 * p.RT);
         // two row tiles: all columns of this one's; else half of the columns of both
         const int c0 = g.dual ? 0 : 2 * X, c1 = g.dual ? 4 : 2 * X + 2;
         if (any) {
@@ -584,18 +638,19 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
                   }
                 }
               } else {
-                float* dst = p.part + prow * 128 + 32 * c;
+                // [column / 8][row][8]: a warp's store is one run of 1 KB
+                float* dst = p.part + pslot * 128 + ((size_t)(4 * c) * (2 * p.RT) + irow) * 8;
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
                   uint32_t w[8];
 #pragma unroll
                   for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(o[e + i]);
-                  ptx::st_global_v8(dst + e, w);  // the workspace is 256-byte aligned
+                  ptx::st_global_v8(dst + (size_t)e * (2 * p.RT), w);  // the workspace is 256-byte aligned
                 }
               }
             }
           }
-          if (it.w.slot >= 0 && valid && (g.dual || X == 0)) p.part_ml[prow] = make_float2(m_ref, l);
+          if (it.w.slot >= 0 && valid && (g.dual || X == 0)) p.part_ml[pslot + irow] = make_float2(m_ref, l);
         }
         ptx::tc_fence_before();
         __syncwarp();
@@ -711,11 +766,11 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
       constexpr uint32_t idesc_pv = (FP8 ? idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128)) | (1u << 16);
       const int me = warp - 9;
       int np = 0, nq[2] = {0, 0}, nof = 0, items = 0;  // P tiles, Q tiles, waits for sh.of, items
+      int blocks = 0;                                  // issued in items of two row tiles
       Cursor<PL::STAGES> cur;                          // next operand tile (E4M3: K tile)
       Cursor<PL::C_STAGES> cv;                         // E4M3: next V tile
       uint32_t chk = 0;                                // bf16: phases of the stages' check barriers
       bool issued = false;
-      auto waitw = [&](uint64_t& b, int parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
       const uint64_t dq[2] = {ptx::smem_desc_sw128(sbase), ptx::smem_desc_sw128(sbase + TILE)};
       const uint64_t dk0 = ptx::smem_desc_sw128(sbase + PL::OFF_KV);
       const uint64_t dv0 = ptx::smem_desc_sw128_mn(sbase + (FP8 ? PL::OFF_C : PL::OFF_KV), HALF);
@@ -822,7 +877,15 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
             }
             continue;
           }
-          ok = ok && (done > 0 || wait_of()) && waitw(sh.p[me], np++);
+          ok = ok && (done > 0 || wait_of());
+          // With two row tiles the blocks of A and B take strict turns. Without that they drift
+          // into step: both softmax at once with the tensor cores idle, then both blocks at
+          // once (3650 instead of 2800 cycles per key tile).
+          if (ok && g.dual) {
+            if (blocks >= 1 - me) ok = waitw(sh.turn[me], blocks - (1 - me));
+            ++blocks;
+          }
+          ok = ok && waitw(sh.p[me], np++);
           if (!ok) break;
           ptx::tc_fence_after();
           if (elect_one()) {
@@ -839,6 +902,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
             }
           }
           __syncwarp();
+          if (g.dual && lane == 0) ptx::mbar_arrive(bar(&sh.turn[me ^ 1]));
           ++done;
         }
         if (!ok) break;
@@ -862,7 +926,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
       uint32_t told = 0;  // bf16: phases of aux
       for (int n = 0;; ++n) {
         const int slot = n % kRing;
-        if (!__all_sync(0xffffffffu, wait(sh.itf[slot], n / kRing))) break;
+        if (!waitw(sh.itf[slot], n / kRing)) break;
         const chunk::Piece w = ring[slot].w;
         if (w.b < 0) break;
         const Geometry g(p, w);
@@ -870,7 +934,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         if constexpr (FP8) {
           // -------------------------------------------------------------- Q codes
           // (of two row tiles each softmax warpgroup makes its own)
-          if (g.T > 0) alive = __all_sync(0xffffffffu, wait(sh.qf[0], nq++));
+          if (g.T > 0) alive = waitw(sh.qf[0], nq++);
           if (!alive) break;
           if (g.T > 0 && !g.dual) {
             const int rows = min(p.RT, (g.last - g.first + 1) * p.split.G);
@@ -880,58 +944,19 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
             if (lane < 4) ptx::mbar_arrive(bar(&sh.aux[2]));
           }
           // -------------------------------------------------------------- V to f16
-          // A row of codes at a time: 8 chunks of 16 codes -> 16 chunks of 8 values, both in the
-          // 128-byte swizzled layout (chunk c of row k at c ^ (k & 7)). Rows no query sees
-          // are zeros; NaN under the mask is taken out.
           for (int j = 0; j < g.T && alive; ++j) {
-            const int a = base + j, s = a % PL::STAGES, cs = a % PL::C_STAGES;
-            alive = wait(sh.kf[PL::V_BAR + s], a / PL::STAGES) &&
-                    (a < PL::C_STAGES || wait(sh.aux[cs], a / PL::C_STAGES - 1));
-            alive = __all_sync(0xffffffffu, alive);
+            const int a = base + j, st = a % PL::STAGES, cs = a % PL::C_STAGES;
+            alive = waitw(sh.kf[PL::V_BAR + st], a / PL::STAGES) &&
+                    (a < PL::C_STAGES || waitw(sh.aux[cs], a / PL::C_STAGES - 1));
             if (!alive) break;
-            const bool cut = g.cut(p, j);
-            bool nan = false;
-            for (int row = lane; row < TK; row += 32) {
-              const uint8_t* src = smem + PL::OFF_KV + (PL::V_BAR + s) * PL::LOAD + row * 128;
-              uint8_t* dst = smem + PL::OFF_C + cs * TILE + row * 128;
-              const int sw = row & 7;
-              const bool in = row < g.valid(j);
-              uint4 x[8];
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                x[c] = in ? *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
-              if (cut) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  uint32_t word[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    // bytes whose low seven bits are all ones: NaN
-                    const uint32_t m = __vcmpeq4(word[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                    nan |= m != 0;
-                    word[e] &= ~m;
-                  }
-                  x[c] = make_uint4(word[0], word[1], word[2], word[3]);
-                }
-              }
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                uint8_t* d = dst + (c >> 2) * HALF;
-                const int c2 = 2 * (c & 3);
-                *reinterpret_cast<uint4*>(d + ((c2 ^ sw) << 4)) =
-                    make_uint4(e4m3x2_to_f16x2(x[c].x), e4m3x2_to_f16x2(x[c].x >> 16), e4m3x2_to_f16x2(x[c].y),
-                               e4m3x2_to_f16x2(x[c].y >> 16));
-                *reinterpret_cast<uint4*>(d + (((c2 + 1) ^ sw) << 4)) =
-                    make_uint4(e4m3x2_to_f16x2(x[c].z), e4m3x2_to_f16x2(x[c].z >> 16), e4m3x2_to_f16x2(x[c].w),
-                               e4m3x2_to_f16x2(x[c].w >> 16));
-              }
-            }
-            if (nan) *reinterpret_cast<volatile int*>(&ring[slot].bad) = 1;
+            if (convert_v(smem + PL::OFF_KV + (PL::V_BAR + st) * PL::LOAD, smem + PL::OFF_C + cs * TILE, lane, g.valid(j),
+                          g.cut(p, j)))
+              *reinterpret_cast<volatile int*>(&ring[slot].bad) = 1;
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
               ptx::mbar_arrive(bar(&sh.vc[cs]));
-              ptx::mbar_arrive(bar(&sh.ke[PL::V_BAR + s]));
+              ptx::mbar_arrive(bar(&sh.ke[PL::V_BAR + st]));
             }
           }
         } else {
@@ -942,8 +967,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
           for (int j = 0; j < g.T && alive; ++j) {
             if (!g.cut(p, j)) continue;
             const int a = 2 * base + g.v_at(j), s = a % PL::STAGES;
-            alive = wait(sh.aux[s], (told >> s) & 1) && wait(sh.kf[s], a / PL::STAGES);
-            alive = __all_sync(0xffffffffu, alive);
+            alive = waitw(sh.aux[s], (told >> s) & 1) && waitw(sh.kf[s], a / PL::STAGES);
             if (!alive) break;
             told ^= 1u << s;
             uint4* v = reinterpret_cast<uint4*>(smem + PL::OFF_KV + s * PL::LOAD);
