@@ -123,17 +123,16 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, unsigned* s
 
 // Wait of a whole warp on a barrier phase, with the same answer in every lane: false when the CTA
 // was told to stop or the limit ran out (which tells it). A phase that is already complete
-// costs one test and one vote; the clock and the abort flag are looked at every 64 tests.
+// costs one test and one vote; a warp that waits longer is suspended by the test (polling warps
+// take shared-memory slots from those that work).
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
                                           uint64_t limit_ns) {
-  uint64_t t0 = 0;
+  if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = ptx::globaltimer();
 #pragma unroll 1
-  for (int i = 1;; ++i) {
-    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
-    if (i & 63) continue;
-    const uint64_t t = ptx::globaltimer();
-    if (i == 64) t0 = t;
-    const bool late = t - t0 > limit_ns;
+  for (;;) {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 10000u))) return true;
+    const bool late = ptx::globaltimer() - t0 > limit_ns;
     if (late) {
       *abort_flag = 1;
       atomicOr(status, DFLASH_DEV_TIMEOUT);
@@ -301,27 +300,43 @@ __device__ __noinline__ int q_codes(uint8_t* tile, int row) {
 // A V tile of E4M3 codes to f16, by one warp: 16 codes at a time, one 16-byte chunk to two, both in the 128-byte swizzled layout (chunk c of row k at c ^ (k & 7)). Rows from `rows`
 // on (that no query sees) are zeros; where `cut`, NaN is taken out. Returns whether there was one.
 __device__ __forceinline__ bool convert_v(const uint8_t* src, uint8_t* dst, int lane, int rows, bool cut) {
+  // Shared memory answers slowly while MMAs read it at its full rate, so kFlight chunks are
+  // requested at once (with 8: 177 us for 64 tokens of 8 heads x 4600 keys; one by one 317).
+  constexpr int kFlight = 8;
   bool nan = false;
-#pragma unroll 8
-  for (int u = lane; u < TK * 8; u += 32) {
-    const int row = u & (TK - 1), c = u / TK, sw = row & 7;
-    uint4 x = row < rows ? *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
-    if (cut) {
-      uint32_t word[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+  for (int u0 = 0; u0 < TK * 8; u0 += 32 * kFlight) {
+    uint4 x[kFlight];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {  // bytes whose low seven bits are all ones
-        const uint32_t m = __vcmpeq4(word[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        nan |= m != 0;
-        word[e] &= ~m;
-      }
-      x = make_uint4(word[0], word[1], word[2], word[3]);
+    for (int i = 0; i < kFlight; ++i) {
+      const int u = u0 + 32 * i + lane, row = u & (TK - 1), c = u / TK;
+      x[i] = row < rows ? *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4)) : make_uint4(0, 0, 0, 0);
     }
-    uint8_t* d = dst + row * 128 + (c >> 2) * HALF;
-    const int c2 = 2 * (c & 3);
-    *reinterpret_cast<uint4*>(d + ((c2 ^ sw) << 4)) = make_uint4(
-        e4m3x2_to_f16x2(x.x), e4m3x2_to_f16x2(x.x >> 16), e4m3x2_to_f16x2(x.y), e4m3x2_to_f16x2(x.y >> 16));
-    *reinterpret_cast<uint4*>(d + (((c2 + 1) ^ sw) << 4)) = make_uint4(
-        e4m3x2_to_f16x2(x.z), e4m3x2_to_f16x2(x.z >> 16), e4m3x2_to_f16x2(x.w), e4m3x2_to_f16x2(x.w >> 16));
+    if (cut) {
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        uint32_t word[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // bytes whose low seven bits are all ones
+          const uint32_t m = __vcmpeq4(word[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          nan |= m != 0;
+          word[e] &= ~m;
+        }
+        x[i] = make_uint4(word[0], word[1], word[2], word[3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      const int u = u0 + 32 * i + lane, row = u & (TK - 1), c = u / TK, sw = row & 7;
+      uint8_t* d = dst + row * 128 + (c >> 2) * HALF;
+      const int c2 = 2 * (c & 3);
+      *reinterpret_cast<uint4*>(d + ((c2 ^ sw) << 4)) =
+          make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16), e4m3x2_to_f16x2(x[i].y),
+                     e4m3x2_to_f16x2(x[i].y >> 16));
+      *reinterpret_cast<uint4*>(d + (((c2 + 1) ^ sw) << 4)) =
+          make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16), e4m3x2_to_f16x2(x[i].w),
+                     e4m3x2_to_f16x2(x[i].w >> 16));
+    }
   }
   return nan;
 }
@@ -461,10 +476,14 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         }
         nq += X == 0 || g.dual;
       }
-      for (int j = g.dual ? 0 : X; j < g.T; j += step, ++done) {
+      // Warps without rows skip the tiles; the warpgroup's first warp hands in P for them.
+      const int rows = min(p.RT, (g.last - g.first + 1) * G - (g.dual ? X * p.RT : 0));
+      const int hand_in = (warp & 3) == 0 ? 5 - ((rows + 31) >> 5) : 1;
+      if (!any) ns += g.dual ? g.T : (g.T + 1 - X) >> 1;
+      for (int j = !any ? g.T : g.dual ? 0 : X; j < g.T; j += step, ++done) {
         alive = waitw(sh.s[X], ns++);
         if (!alive) break;
-        if (any) {
+        {
           if (FP8 && done == 0) sl2 = ldexpf(p.sl2, sh.qexp[g.dual ? X : 0][r]);
           ptx::tc_fence_after();
           uint32_t raw[4][32];
@@ -544,7 +563,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
           ptx::tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(&sh.p[X]));
+        if (lane < hand_in) ptx::mbar_arrive(bar(&sh.p[X]));
       }
       if (!alive) break;
       // ---- epilogue
