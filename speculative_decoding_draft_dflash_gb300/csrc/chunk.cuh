@@ -90,14 +90,18 @@ int chunk_attn_tc_item_rows(int G);
 // ---------------------------------------------------------------------------
 namespace chunk {
 
+// TOKENS: an item is item_tokens whole tokens; else item_rows stacked rows wherever they end.
+// (The functions here are compiled into a kernel whose code has to stay small: what does not
+// fit the instruction cache is fetched again and again by warps that do different things.)
+template <bool TOKENS>
 struct Split {
   const int32_t* cu_rows;
   const int32_t* kv_lens;
   int batch, rows, n_kv, G, capacity, window;
   int item_rows;   // stacked rows of an item
-  int item_tokens; // of whole tokens: how many, else 0
+  int item_tokens; // TOKENS: tokens of an item
   int half_rows;   // an item of at most so many rows has the smaller tile cost
-  int tile_keys;   // keys of a tile (a power of two)
+  int tile_shift;  // log2 of a tile's keys
   // Cost units: an item, a key tile of an item, and of one of at most half_rows rows.
   int item_cost, tile_cost, half_cost;
 };
@@ -106,7 +110,8 @@ struct Seq {
   int row0, n, kv;  // first row, new rows, rows held (0: refused)
 };
 
-__device__ __forceinline__ Seq load_seq(const Split& p, int b, unsigned* bad) {
+template <bool TOKENS>
+__device__ __forceinline__ Seq load_seq(const Split<TOKENS>& p, int b, unsigned* bad) {
   Seq s;
   s.row0 = p.cu_rows[b];
   s.n = p.cu_rows[b + 1] - s.row0;
@@ -123,32 +128,38 @@ __device__ __forceinline__ Seq load_seq(const Split& p, int b, unsigned* bad) {
 }
 
 // (rows * G fits 31 bits)
-__device__ __forceinline__ int n_items(const Split& p, const Seq& s) {
+template <bool TOKENS>
+__device__ __forceinline__ int n_items(const Split<TOKENS>& p, const Seq& s) {
+  if (TOKENS) return (int)((unsigned)(s.n + p.item_tokens - 1) / (unsigned)p.item_tokens);
   return (int)((unsigned)(s.n * p.G + p.item_rows - 1) / (unsigned)p.item_rows);
 }
 
 // Positions of the first and the last row of item t.
-__device__ __forceinline__ int2 item_span(const Split& p, const Seq& s, int t) {
+template <bool TOKENS>
+__device__ __forceinline__ int2 item_span(const Split<TOKENS>& p, const Seq& s, int t) {
   const int p0 = s.kv - s.n;
-  if (p.item_tokens > 0) return make_int2(p0 + t * p.item_tokens, p0 + min((t + 1) * p.item_tokens, s.n) - 1);
+  if (TOKENS) return make_int2(p0 + t * p.item_tokens, p0 + min((t + 1) * p.item_tokens, s.n) - 1);
   const unsigned r0 = t * p.item_rows, r1 = min(r0 + p.item_rows, (unsigned)(s.n * p.G));
   return make_int2(p0 + (int)(r0 / (unsigned)p.G), p0 + (int)((r1 - 1) / (unsigned)p.G));
 }
 
 // First key (a multiple of the tile) and key tiles of item t.
-__device__ __forceinline__ int2 item_keys(const Split& p, const Seq& s, int t) {
+template <bool TOKENS>
+__device__ __forceinline__ int2 item_keys(const Split<TOKENS>& p, const Seq& s, int t) {
   const int2 span = item_span(p, s, t);
   if (span.y < 0) return make_int2(0, 0);
   int k0 = 0;
-  if (p.window > 0 && span.x >= p.window) k0 = (span.x - p.window + 1) & ~(p.tile_keys - 1);
-  return make_int2(k0, (int)((unsigned)(span.y - k0) / (unsigned)p.tile_keys) + 1);
+  if (p.window > 0 && span.x >= p.window) k0 = (span.x - p.window + 1) >> p.tile_shift << p.tile_shift;
+  return make_int2(k0, ((span.y - k0) >> p.tile_shift) + 1);
 }
 
 // Cost units of a key tile of item t, and of the whole item.
-__device__ __forceinline__ int tile_units(const Split& p, const Seq& s, int t) {
+template <bool TOKENS>
+__device__ __forceinline__ int tile_units(const Split<TOKENS>& p, const Seq& s, int t) {
   return s.n * p.G - t * p.item_rows > p.half_rows ? p.tile_cost : p.half_cost;
 }
-__device__ __forceinline__ int item_units(const Split& p, const Seq& s, int t) {
+template <bool TOKENS>
+__device__ __forceinline__ int item_units(const Split<TOKENS>& p, const Seq& s, int t) {
   return p.item_cost + tile_units(p, s, t) * item_keys(p, s, t).y;
 }
 
@@ -164,11 +175,12 @@ struct Start {
 
 // CTAs that get a share: large enough for a key tile, so that every CTA inside a cut item has
 // at least one.
-__device__ __forceinline__ int active_ctas(const Split& p, long long total, int ctas) {
+template <bool TOKENS>
+__device__ __forceinline__ int active_ctas(const Split<TOKENS>& p, long long total, int ctas) {
   const int least = max(p.tile_cost, p.half_cost);
   return total >= (long long)ctas * least ? ctas : max(1, (int)(total / least));
 }
-__device__ __forceinline__ long long bound(long long total, int active, int c) {
+static __device__ __noinline__ long long bound(long long total, int active, int c) {
   return total * c / active;
 }
 
@@ -177,46 +189,38 @@ constexpr size_t kLocateBytes = sizeof(Seq) + sizeof(long long);  // per sequenc
 
 // Run by all threads of the CTA; `scratch` is 16-byte aligned shared memory of kLocateBytes per
 // sequence (free again after the call and a __syncthreads), `st` shared. A thread per sequence
-// reads the lengths and adds up its items; sequences of many items get a warp.
-__device__ __forceinline__ void locate(const Split& p, void* scratch, Start* st, unsigned* status) {
+// reads the lengths; then eight lanes per sequence add up its items.
+template <bool TOKENS>
+__device__ __noinline__ void locate(const Split<TOKENS>& p, void* scratch, Start* st, unsigned* status) {
   long long* cost = reinterpret_cast<long long*>(scratch);
   Seq* seq = reinterpret_cast<Seq*>(cost + p.batch);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  constexpr int kFew = 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned bad = 0;
-  bool many = false;
-  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
-    const Seq s = load_seq(p, b, &bad);
-    seq[b] = s;
-    const int items = n_items(p, s);
-    long long sum = 0;
-    for (int t = 0; t < min(items, kFew); ++t) sum += item_units(p, s, t);
-    cost[b] = items <= kFew ? sum * p.n_kv : -1;
-    many |= items > kFew;
-  }
+#pragma unroll 1
+  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) seq[b] = load_seq(p, b, &bad);
   if (bad && blockIdx.x == 0) atomicOr(status, bad);
-  if (__syncthreads_or(many)) {
-    for (int base = warp * 32; base < p.batch; base += nw * 32) {
-      unsigned left = __ballot_sync(0xffffffffu, base + lane < p.batch && cost[base + lane] < 0);
-      while (left) {
-        const int b = base + __ffs(left) - 1;
-        left &= left - 1;
-        const Seq s = seq[b];
-        const int items = n_items(p, s);
-        long long sum = 0;
-        for (int t = lane; t < items; t += 32) sum += item_units(p, s, t);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) cost[b] = sum * p.n_kv;
-      }
+  __syncthreads();
+#pragma unroll 1
+  for (int base = 0; base < p.batch; base += blockDim.x >> 3) {
+    const int b = base + (threadIdx.x >> 3);
+    long long sum = 0;
+    if (b < p.batch) {
+      const Seq s = seq[b];
+      const int items = n_items(p, s);
+#pragma unroll 1
+      for (int t = threadIdx.x & 7; t < items; t += 8) sum += item_units(p, s, t);
     }
-    __syncthreads();
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (b < p.batch && (threadIdx.x & 7) == 0) cost[b] = sum * p.n_kv;
   }
+  __syncthreads();
   if (warp == 0) {  // prefix sums, in place
     long long carry = 0;
+#pragma unroll 1
     for (int base = 0; base < p.batch; base += 32) {
       long long v = base + lane < p.batch ? cost[base + lane] : 0;
-#pragma unroll
+#pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const long long u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
@@ -240,17 +244,22 @@ __device__ __forceinline__ void locate(const Split& p, void* scratch, Start* st,
       b = lo;
       const Seq s = seq[b];
       const long long before = b > 0 ? cost[b - 1] : 0;
-      const long long per_head = (cost[b] - before) / p.n_kv;
-      const int kvh = (int)((begin - before) / per_head);
-      long long rest = begin - before - per_head * kvh;
+      const long long per_head = bound(cost[b] - before, p.n_kv, 1);
+      int kvh = 0;
+      long long rest = begin - before;
+      while (rest >= per_head) {  // (n_kv steps at most)
+        rest -= per_head;
+        ++kvh;
+      }
       // the item: scan their costs 32 at a time (their sum fits 31 bits: the capacity does)
       const int items = n_items(p, s);
       int t = 0;
+#pragma unroll 1
       for (int base = 0; base < items; base += 32) {
         const int u = base + lane;
         const int w = u < items ? item_units(p, s, u) : 0;
         int v = w;
-#pragma unroll
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
           const int x = __shfl_up_sync(0xffffffffu, v, o);
           if (lane >= o) v += x;
@@ -292,14 +301,15 @@ struct Piece {
 };
 
 // Walks a CTA's share piece by piece (one thread, or all threads of a warp alike).
+template <bool TOKENS>
 struct Walker {
-  Split p;
+  Split<TOKENS> p;
   Seq s;
   long long at, end, total;
   int ctas, b, kvh, t, off;
   int4 merge;  // what to merge: {b, kvh, t, pieces}, pieces 0 when nothing was cut here
 
-  __device__ void init(const Split& split, const Start& st) {
+  __device__ __forceinline__ void init(const Split<TOKENS>& split, const Start& st) {
     p = split;
     at = st.begin;
     end = st.end;
@@ -313,7 +323,7 @@ struct Walker {
     s = st.s;
   }
 
-  __device__ bool next(Piece* w) {
+  __device__ __forceinline__ bool next(Piece* w) {
     while (at < end) {
       const int items = n_items(p, s);
       if (t >= items) {  // next KV head, next sequence

@@ -12,7 +12,7 @@ namespace dflash {
 namespace {
 
 constexpr int RI = 64;   // stacked query rows of an item
-constexpr int TK = 64;   // keys per tile
+constexpr int TK = 64;   // keys per tile (2^6)
 constexpr int kThreads = 256;
 
 template <int DP>
@@ -24,10 +24,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_simt_kernel(const Chun
   float* Vs = Ks + TK * LD;
   float* Ps = Vs + TK * LD;
   __shared__ chunk::Start start;
-  const chunk::Split split = {p.cu_rows, p.kv_lens, p.batch, p.rows, p.n_kv, p.G, p.capacity,
-                              p.window, RI, 0, RI, TK, 1, 1, 1};
+  const chunk::Split<false> split = {p.cu_rows, p.kv_lens, p.batch, p.rows, p.n_kv, p.G, p.capacity,
+                              p.window, RI, 0, RI, 6, 1, 1, 1};
   chunk::locate(split, smem4, &start, p.status);
-  chunk::Walker walk;
+  chunk::Walker<false> walk;
   walk.init(split, start);
   __syncthreads();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, d = p.d_h;

@@ -38,7 +38,7 @@ bool encode_2d_u8(CUtensorMap* m, const void* base, long long rows, int box_rows
 
 namespace {
 
-constexpr int TK = 128;
+constexpr int TK = 128;                   // keys of a tile (2^7)
 constexpr uint32_t TILE = 128 * 128 * 2;  // a 16-bit tile
 constexpr uint32_t HALF = TILE / 2;       // its 64-column box
 constexpr int kRing = 4;                  // items in flight between the roles
@@ -66,7 +66,7 @@ struct Plan {
 
 struct Params {
   CUtensorMap q, k, v;
-  chunk::Split split;
+  chunk::Split<true> split;
   const int32_t* table;  // paged: [batch][pps] page ids, or null
   int pps, n_pages;
   int oob_row;           // a row beyond the K / V maps: reads as zeros
@@ -107,6 +107,7 @@ struct Tail {
   chunk::Start start;
   uint32_t tmem_slot;
   int abort_flag;
+  int rows[4];                    // of the last key tiles (the loading thread's)
   float2 xml[2][128];             // (reference, sum) of the even / odd half
   signed char qexp[2][128];       // E4M3: Q rows are codes of q 2^-qexp
 };
@@ -121,17 +122,15 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, unsigned* s
   }
 }
 
-// Wait of a whole warp on a barrier phase, with the same answer in every lane: false when the CTA
-// was told to stop or the limit ran out (which tells it). A phase that is already complete
+// Waits of a whole warp on a barrier phase, with the same answer in every lane: false when the
+// CTA was told to stop or the limit ran out (which tells it). A phase that is already complete
 // costs one test and one vote; a warp that waits longer is suspended by the test (polling warps
 // take shared-memory slots from those that work).
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
+__device__ __forceinline__ bool wait_more(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
                                           uint64_t limit_ns) {
-  if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = ptx::globaltimer();
 #pragma unroll 1
-  for (;;) {
-    if (__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 10000u))) return true;
+  while (!__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 10000u))) {
     const bool late = ptx::globaltimer() - t0 > limit_ns;
     if (late) {
       *abort_flag = 1;
@@ -139,6 +138,15 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
     }
     if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
   }
+  return true;
+}
+__device__ __noinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
+                                      uint64_t limit_ns) {
+  return ptx::mbar_wait_idle(bar, parity, abort_flag, status, limit_ns);
+}
+__device__ __noinline__ bool wait_more_call(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
+                                            uint64_t limit_ns) {
+  return wait_more(bar, parity, abort_flag, status, limit_ns);
 }
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
@@ -208,6 +216,30 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+// 32 lanes x 16 columns of tensor memory.
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// 32 bytes to global memory.
+__device__ __forceinline__ void st8(void* p, const uint32_t* w) {
+  const uint32_t v[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
+  ptx::st_global_v8(p, v);
+}
+
 template <int N> __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
@@ -236,9 +268,8 @@ struct Geometry {
   }
   // keys of tile j that some row may see, counted from its start
   __device__ __forceinline__ int valid(int j) const { return min(TK, last + 1 - (key0 + j * TK)); }
-  // Where K_j and V_j stand among the item's 2 T operand tiles. Two row tiles: K0 V0 K1 V1 ..;
+  // Where V_j stands among the item's 2 T operand tiles. Two row tiles: K0 V0 K1 V1 ..;
   // even / odd: K0 K1 V0 K2 V1 K3 .. V(T-2) V(T-1), each S two tiles ahead of its PV.
-  __device__ __forceinline__ int k_at(int j) const { return dual ? 2 * j : j < 2 ? j : 2 * j - 1; }
   __device__ __forceinline__ int v_at(int j) const {
     return dual ? 2 * j + 1 : j == T - 1 ? 2 * T - 1 : 2 * j + 2;
   }
@@ -297,54 +328,60 @@ __device__ __noinline__ int q_codes(uint8_t* tile, int row) {
   return ex;
 }
 
-// A V tile of E4M3 codes to f16, by one warp: 16 codes at a time, one 16-byte chunk to two, both in the 128-byte swizzled layout (chunk c of row k at c ^ (k & 7)). Rows from `rows`
-// on (that no query sees) are zeros; where `cut`, NaN is taken out. Returns whether there was one.
-__device__ __forceinline__ bool convert_v(const uint8_t* src, uint8_t* dst, int lane, int rows, bool cut) {
-  // Shared memory answers slowly while MMAs read it at its full rate, so kFlight chunks are
-  // requested at once (with 8: 177 us for 64 tokens of 8 heads x 4600 keys; one by one 317).
-  constexpr int kFlight = 8;
+// A V tile of E4M3 codes to f16, by one warp, a row per lane at a time: 16 codes (a 16-byte chunk
+// of a row) to two chunks, both in the 128-byte swizzled layout (chunk c of row k at c ^ (k & 7)).
+// Rows from `rows` on (that no query sees) are zeros. Shared memory answers slowly while MMAs
+// read it at its full rate, so a row's chunks are requested at once (64 tokens over 8 x 4600
+// keys: 168 us; chunk by chunk 317).
+__device__ __forceinline__ void convert_v(const uint8_t* src, uint8_t* dst, int lane, int rows) {
+#pragma unroll 1
+  for (int row = lane; row < TK; row += 32) {
+    const uint8_t* sr = src + row * 128;
+    uint8_t* dr = dst + row * 128;
+    const int sw = row & 7;
+    const bool in = row < rows;
+    uint4 x[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = in ? *reinterpret_cast<const uint4*>(sr + ((c ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      uint8_t* d = dr + (c >> 2) * HALF;
+      const int c2 = 2 * (c & 3);
+      *reinterpret_cast<uint4*>(d + ((c2 ^ sw) << 4)) = make_uint4(
+          e4m3x2_to_f16x2(x[c].x), e4m3x2_to_f16x2(x[c].x >> 16), e4m3x2_to_f16x2(x[c].y), e4m3x2_to_f16x2(x[c].y >> 16));
+      *reinterpret_cast<uint4*>(d + (((c2 + 1) ^ sw) << 4)) = make_uint4(
+          e4m3x2_to_f16x2(x[c].z), e4m3x2_to_f16x2(x[c].z >> 16), e4m3x2_to_f16x2(x[c].w), e4m3x2_to_f16x2(x[c].w >> 16));
+    }
+  }
+}
+// Takes NaN codes (bytes whose low seven bits are all ones) out of the rows of a tile that its
+// lane converts. Returns whether there was one.
+__device__ __noinline__ bool drop_nan(uint8_t* tile, int lane, int rows) {
   bool nan = false;
 #pragma unroll 1
-  for (int u0 = 0; u0 < TK * 8; u0 += 32 * kFlight) {
-    uint4 x[kFlight];
+  for (int row = lane; row < rows; row += 32) {
+    uint4* at = reinterpret_cast<uint4*>(tile + row * 128);
+    uint4 x[8];
+    uint32_t hit = 0;
 #pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int u = u0 + 32 * i + lane, row = u & (TK - 1), c = u / TK;
-      x[i] = row < rows ? *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4)) : make_uint4(0, 0, 0, 0);
-    }
-    if (cut) {
+    for (int c = 0; c < 8; ++c) x[c] = at[c ^ (row & 7)];  // (the order spreads lanes over banks)
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i) {
-        uint32_t word[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {  // bytes whose low seven bits are all ones
-          const uint32_t m = __vcmpeq4(word[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          nan |= m != 0;
-          word[e] &= ~m;
-        }
-        x[i] = make_uint4(word[0], word[1], word[2], word[3]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int u = u0 + 32 * i + lane, row = u & (TK - 1), c = u / TK, sw = row & 7;
-      uint8_t* d = dst + row * 128 + (c >> 2) * HALF;
-      const int c2 = 2 * (c & 3);
-      *reinterpret_cast<uint4*>(d + ((c2 ^ sw) << 4)) =
-          make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16), e4m3x2_to_f16x2(x[i].y),
-                     e4m3x2_to_f16x2(x[i].y >> 16));
-      *reinterpret_cast<uint4*>(d + (((c2 + 1) ^ sw) << 4)) =
-          make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16), e4m3x2_to_f16x2(x[i].w),
-                     e4m3x2_to_f16x2(x[i].w >> 16));
-    }
+    for (int c = 0; c < 8; ++c)  // a byte of 0x7F carries into its top bit
+      hit |= ((x[c].x & 0x7F7F7F7Fu) + 0x01010101u) | ((x[c].y & 0x7F7F7F7Fu) + 0x01010101u) |
+             ((x[c].z & 0x7F7F7F7Fu) + 0x01010101u) | ((x[c].w & 0x7F7F7F7Fu) + 0x01010101u);
+    if ((hit & 0x80808080u) == 0) continue;
+    nan = true;
+    uint32_t* w = reinterpret_cast<uint32_t*>(at);
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) w[i] &= ~__vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
   }
   return nan;
 }
 
-// Adds to 32 columns of an output row what the checking warps took out of the V tiles: the
+// Adds to 16 columns of an output row what the checking warps took out of the V tiles: the
 // values that are not finite, of keys the row sees.
 template <bool FP8>
-__device__ __noinline__ void repair(const Params& p, const Item& it, int pos, int col, float* o) {
+__device__ __noinline__ void repair(const Params& p, const Item& it, int pos, int col, float* o) {  // 16 columns
   const Geometry g(p, it.w);
   for (int j = 0; j < g.T; ++j) {
     if (!g.cut(p, j)) continue;
@@ -357,9 +394,11 @@ __device__ __noinline__ void repair(const Params& p, const Item& it, int pos, in
     } else {
       row = ((long long)it.w.b * p.split.n_kv + it.w.kvh) * p.split.capacity + k;
     }
+#pragma unroll 1
     for (int e = 0; e < TK; ++e) {
       if (k + e > pos || (p.split.window > 0 && pos - (k + e) >= p.split.window)) continue;
-      for (int c = 0; c < 32; ++c) {
+#pragma unroll 1
+      for (int c = 0; c < 16; ++c) {
         const size_t at = (size_t)(row + e) * 128 + col + c;
         const float x = FP8 ? e4m3x2_value(((const uint8_t*)p.cache_v)[at]).x
                             : __bfloat162float(((const bf16*)p.cache_v)[at]);
@@ -384,10 +423,18 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
   }
   auto bar = [](uint64_t* b) { return ptx::smem_u32(b); };
   auto wait = [&](uint64_t& b, int parity) {  // one thread
-    return ptx::mbar_wait(ptx::smem_u32(&b), (uint32_t)(parity & 1), &sh.abort_flag, p.status, p.wait_ns);
+    const uint32_t at = ptx::smem_u32(&b), ph = (uint32_t)(parity & 1);
+    return ptx::mbar_try_wait(at, ph) || wait_one(at, ph, &sh.abort_flag, p.status, p.wait_ns);
   };
-  auto waitw = [&](uint64_t& b, int parity) {  // a whole warp
-    return wait_warp(ptx::smem_u32(&b), (uint32_t)(parity & 1), &sh.abort_flag, p.status, p.wait_ns);
+  auto waits = [&](uint64_t& b, int parity) {  // softmax warps (a call would cost them registers)
+    const uint32_t at = ptx::smem_u32(&b), ph = (uint32_t)(parity & 1);
+    return __all_sync(0xffffffffu, ptx::mbar_try_wait(at, ph)) ||
+           wait_more(at, ph, &sh.abort_flag, p.status, p.wait_ns);
+  };
+  auto waitw = [&](uint64_t& b, int parity) {  // the others
+    const uint32_t at = ptx::smem_u32(&b), ph = (uint32_t)(parity & 1);
+    return __all_sync(0xffffffffu, ptx::mbar_try_wait(at, ph)) ||
+           wait_more_call(at, ph, &sh.abort_flag, p.status, p.wait_ns);
   };
 
   if (threadIdx.x == 0) {
@@ -451,7 +498,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     int ns = 0, no = 0, nd = 0, nx = 0, nq = 0;  // tiles, items with keys; of two row tiles, of one
     for (int n = 0;; ++n) {
       const int slot = n % kRing;
-      if (!waitw(sh.itf[slot], n / kRing)) break;
+      if (!waits(sh.itf[slot], n / kRing)) break;
       const Item& it = ring[slot];
       if (it.w.b < 0) break;
       const Geometry g(p, it.w);
@@ -468,7 +515,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
       int done = 0;  // tiles of this accumulator
       if (FP8 && g.T > 0) {
         if (g.dual) {
-          if (!waitw(sh.qf[X], nq)) break;
+          if (!waits(sh.qf[X], nq)) break;
           if (valid) sh.qexp[X][r] = (signed char)q_codes(smem + X * TILE, r);
           ptx::fence_proxy_async_smem();
           __syncwarp();
@@ -481,7 +528,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
       const int hand_in = (warp & 3) == 0 ? 5 - ((rows + 31) >> 5) : 1;
       if (!any) ns += g.dual ? g.T : (g.T + 1 - X) >> 1;
       for (int j = !any ? g.T : g.dual ? 0 : X; j < g.T; j += step, ++done) {
-        alive = waitw(sh.s[X], ns++);
+        alive = waits(sh.s[X], ns++);
         if (!alive) break;
         {
           if (FP8 && done == 0) sl2 = ldexpf(p.sl2, sh.qexp[g.dual ? X : 0][r]);
@@ -543,22 +590,20 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
           }
           const float mu = m_ref == -INFINITY ? 0.f : m_ref;
           const float2 sl2v = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
-          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                           make_float2(0.f, 0.f)};
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
+          for (int h = 0; h < 4; ++h) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-              const float2 x = __ffma2_rn(make_float2(s[64 * h + e], s[64 * h + e + 1]), sl2v, nmu);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = __ffma2_rn(make_float2(s[32 * h + e], s[32 * h + e + 1]), sl2v, nmu);
               const float2 y = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-              acc[(e >> 1) & 3] = __fadd2_rn(acc[(e >> 1) & 3], y);
+              acc[(e >> 1) & 1] = __fadd2_rn(acc[(e >> 1) & 1], y);
               pk[e >> 1] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
             }
-            ptx::tmem_st_32x32b_x32(tS + 32 * h, pk);
+            tmem_st_x16(tS + 16 * h, pk);
           }
-          const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
-          l = l * alpha + ((a01.x + a01.y) + (a23.x + a23.y));
+          l = l * alpha + ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y));
           ptx::tmem_st_wait();
           ptx::tc_fence_before();
         }
@@ -581,11 +626,11 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         float wa = 1.f, wb = 0.f;  // weights of the two accumulators (one: its own)
         if (!g.dual) {
           // the other half has read what the last exchange left
-          if (no > 0 && !waitw(sh.of, no - 1)) break;
+          if (no > 0 && !waits(sh.of, no - 1)) break;
           sh.xml[X][r] = make_float2(m_ref, l);
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar(&sh.x[X]));
-          if (!waitw(sh.x[X ^ 1], nx)) break;
+          if (!waits(sh.x[X ^ 1], nx)) break;
           const float2 other = sh.xml[X ^ 1][r];
           const float ma = X == 0 ? m_ref : other.x, mb = X == 0 ? other.x : m_ref;
           const float la = X == 0 ? l : other.y, lb = X == 0 ? other.y : l;
@@ -594,78 +639,64 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
           wb = mb == -INFINITY ? 0.f : ptx::ex2(mb - m_ref);
           l = (la == 0.f ? 0.f : la * wa) + (lb == 0.f ? 0.f : lb * wb);
         }
-        if (!(g.dual ? waitw(sh.o[X], nd++) : waitw(sh.oe, nx++))) break;
-        if (!waitw(sh.chk[slot], n / kRing)) break;
+        if (!(g.dual ? waits(sh.o[X], nd++) : waits(sh.oe, nx++))) break;
+        if (!waits(sh.chk[slot], n / kRing)) break;
         ++no;
         ptx::tc_fence_after();
         const bool bad = *reinterpret_cast<const volatile int*>(&it.bad) != 0;
         const float inv = it.w.slot < 0 ? (l == 0.f ? 0.f : (FP8 ? p.v_scale : 1.f) / l) : (FP8 ? p.v_scale : 1.f);
         const int irow = (g.dual ? X * p.RT : 0) + r;
         const size_t pslot = (size_t)(2 * blockIdx.x + (it.w.slot > 0)) * (2 * p.RT);
-        // two row tiles: all columns of this one's; else half of the columns of both
-        const int c0 = g.dual ? 0 : 2 * X, c1 = g.dual ? 4 : 2 * X + 2;
+        // two row tiles: all columns of this one's; else half of the columns of both. An
+        // accumulator without keys (or without a tile) is not read as a number.
+        const int c0 = g.dual ? 0 : 4 * X, c1 = g.dual ? 8 : 4 * X + 4;  // 16 columns each
+        const uint32_t t0 = tO + (g.dual ? X * 128 : 0);
+        const float fa = wa * inv, fb = wb * inv;
         if (any) {
 #pragma unroll 1
           for (int c = c0; c < c1; ++c) {
-            float o[32];
-            if (g.dual) {
-              uint32_t v[32];
-              ptx::tmem_ld_32x32b_x32(tO + X * 128 + 32 * c, v);
-              ptx::tmem_ld_wait();
+            uint32_t v[16], u[16];
+            float o[16];
+            tmem_ld_x16(t0 + 16 * c, v);
+            if (!g.dual) tmem_ld_x16(tO + 128 + 16 * c, u);
+            ptx::tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * inv;
-            } else {
-              uint32_t v[32], u[32];
-              ptx::tmem_ld_32x32b_x32(tO + 32 * c, v);
-              ptx::tmem_ld_32x32b_x32(tO + 128 + 32 * c, u);
-              ptx::tmem_ld_wait();
-              const float fa = wa * inv, fb = wb * inv;
-              if (__all_sync(0xffffffffu, wa != 0.f && wb != 0.f)) {
+            for (int e = 0; e < 16; ++e) o[e] = wa == 0.f ? 0.f : __uint_as_float(v[e]) * fa;
+            if (wb != 0.f) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * fa + __uint_as_float(u[e]) * fb;
-              } else {  // an accumulator without keys (or without a tile) is not read as a number
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  o[e] = (wa == 0.f ? 0.f : __uint_as_float(v[e]) * fa) + (wb == 0.f ? 0.f : __uint_as_float(u[e]) * fb);
-              }
+              for (int e = 0; e < 16; ++e) o[e] += __uint_as_float(u[e]) * fb;
             }
             if (!(l > 0.f)) {  // no key, or a score that is not a number
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = l;
+              for (int e = 0; e < 16; ++e) o[e] = l;
             }
             if (bad && valid) {
-              float fix[32];
-              for (int e = 0; e < 32; ++e) fix[e] = 0.f;
-              repair<FP8>(p, it, pos, 32 * c, fix);
+              float fix[16];
+#pragma unroll 1
+              for (int e = 0; e < 16; ++e) fix[e] = 0.f;
+              repair<FP8>(p, it, pos, 16 * c, fix);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] += fix[e];
+              for (int e = 0; e < 16; ++e) o[e] += fix[e];
             }
             if (valid) {
+              uint32_t w[16];
               if (it.w.slot < 0) {
-                // whole 32-byte sectors where `out` allows
 #pragma unroll
-                for (int e = 0; e < 32; e += 16) {
-                  uint32_t w[8];
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[e + 2 * i], o[e + 2 * i + 1]);
-                  bf16* dst = orow + 32 * c + e;
-                  if (p.out32) {
-                    ptx::st_global_v8(dst, w);
-                  } else {
-                    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                  }
+                for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
+                bf16* dst = orow + 16 * c;
+                if (p.out32) {  // a whole 32-byte sector
+                  st8(dst, w);
+                } else {
+                  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                  *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
                 }
               } else {
                 // [column / 8][row][8]: a warp's store is one run of 1 KB
-                float* dst = p.part + pslot * 128 + ((size_t)(4 * c) * (2 * p.RT) + irow) * 8;
+                float* dst = p.part + pslot * 128 + ((size_t)(2 * c) * (2 * p.RT) + irow) * 8;
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint32_t w[8];
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(o[e + i]);
-                  ptx::st_global_v8(dst + (size_t)e * (2 * p.RT), w);  // the workspace is 256-byte aligned
-                }
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i]);
+                st8(dst, w);
+                st8(dst + (size_t)8 * (2 * p.RT), w + 8);  // the workspace is 256-byte aligned
               }
             }
           }
@@ -683,87 +714,82 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     if (warp == 8) {
       // ------------------------------------------------------------------ work list, TMA
       if (lane == 0) {
-        chunk::Walker walk;
+        chunk::Walker<true> walk;
         walk.init(p.split, sh.start);
         chunk::Piece w;
         int count[2] = {0, 0}, nq[2] = {0, 0};  // tiles (bf16: of both kinds), Q tiles
-        bool more = walk.next(&w);
-        for (int n = 0;; ++n) {
-          const int slot = n % kRing;
-          if (n >= kRing && !wait(sh.ite[slot], n / kRing - 1)) break;
-          if (!more) w.b = -1;
-          ring[slot].w = w;
-          ring[slot].bad = 0;
-          ptx::mbar_arrive(bar(&sh.itf[slot]));
-          if (!more) break;
-          const chunk::Piece cur = w;
+        chunk::Piece cur;
+        bool more = true;
+#pragma unroll 1
+        for (int n = -1;; ++n) {  // item n's tiles are issued once item n + 1 is known
+          if (n >= 0) {
+            const int slot = n % kRing;
+            if (n >= kRing && !wait(sh.ite[slot], n / kRing - 1)) break;
+            if (!more) w.b = -1;
+            ring[slot].w = w;
+            ring[slot].bad = 0;
+            ptx::mbar_arrive(bar(&sh.itf[slot]));
+            if (!more) break;
+            cur = w;
+          }
+          more = walk.next(&w);
+          if (n < 0) continue;
           const Geometry g(p, cur);
-          more = walk.next(&w);  // its loads are in flight while this item's tiles are issued
           if (g.T == 0) continue;
           const int32_t* table = p.table ? p.table + (size_t)cur.b * p.pps + (g.key0 >> 7) : nullptr;
-          auto tile_row = [&](int j) -> int {
-            if (!table) return (cur.b * p.split.n_kv + cur.kvh) * p.split.capacity + g.key0 + j * TK;
-            const int page = table[j];
-            if (page < 0 || page >= p.n_pages) {
-              atomicOr(p.status, DFLASH_DEV_PAGE);
-              return p.oob_row;
-            }
-            return (page * p.split.n_kv + cur.kvh) * TK;
-          };
           bool stop = false;
-          auto load_q = [&](int X) {
-            if (nq[X] > 0 && !wait(sh.qe[X], nq[X] - 1)) {
-              stop = true;
-              return;
+          int page = table ? table[0] : 0;
+#pragma unroll 1
+          for (int i = 0, jk = 0, jv = 0; i <= 2 * g.T; ++i) {
+            // after the first K tile: Q, unless nothing is left to load
+            if (i == 1) {
+#pragma unroll 1
+              for (int X = 0; X < (g.dual ? 2 : 1); ++X) {
+                if (nq[X] > 0 && !wait(sh.qe[X], nq[X] - 1)) {
+                  stop = true;
+                  break;
+                }
+                ++nq[X];
+                ptx::mbar_arrive_expect_tx(bar(&sh.qf[X]), (uint32_t)p.RT * 256);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  tma_load_3d(sbase + X * TILE + h * HALF, &p.q, bar(&sh.qf[X]), 64 * h, cur.kvh * p.split.G,
+                              cur.row0 + (2 * cur.t + X) * p.TQ);
+              }
+              if (stop) break;
             }
-            ++nq[X];
-            ptx::mbar_arrive_expect_tx(bar(&sh.qf[X]), (uint32_t)p.RT * 256);
-            for (int h = 0; h < 2; ++h)
-              tma_load_3d(sbase + X * TILE + h * HALF, &p.q, bar(&sh.qf[X]), 64 * h, cur.kvh * p.split.G,
-                          cur.row0 + (2 * cur.t + X) * p.TQ);
-          };
-          auto load = [&](int which, int row, bool check) {  // 0: a K tile, 1: a V tile
-            int& at = FP8 ? count[which] : count[0];
+            if (i == 2 * g.T) break;
+            const int which = jv < g.T && i == g.v_at(jv);  // 0: a K tile, 1: a V tile
+            if (!which) {
+              // the row of tile jk: of its page (looked up a tile ahead), or in the sequence's slab
+              int row = (cur.b * p.split.n_kv + cur.kvh) * p.split.capacity + g.key0 + jk * TK;
+              if (table) {
+                row = (page * p.split.n_kv + cur.kvh) * TK;
+                if (page < 0 || page >= p.n_pages) {
+                  atomicOr(p.status, DFLASH_DEV_PAGE);
+                  row = p.oob_row;
+                }
+                if (jk + 1 < g.T) page = table[jk + 1];
+              }
+              sh.rows[jk & 3] = row;
+            }
+            const int y = sh.rows[(which ? jv : jk) & 3];
+            int& at = FP8 && which ? count[1] : count[0];
             const int s = at % PL::STAGES, u = at / PL::STAGES, bi = s + which * PL::V_BAR;
             if (u > 0 && !wait(sh.ke[bi], u - 1)) {
               stop = true;
-              return;
+              break;
             }
             const CUtensorMap* map = which ? &p.v : &p.k;
             const uint32_t dst = sbase + PL::OFF_KV + bi * PL::LOAD;
             ptx::mbar_arrive_expect_tx(bar(&sh.kf[bi]), PL::LOAD);
-            ptx::tma_load_2d(dst, map, bar(&sh.kf[bi]), 0, row);
-            if (!FP8) ptx::tma_load_2d(dst + HALF, map, bar(&sh.kf[bi]), 64, row);
-            // the checking warps look at some stages only, so they are told which phase of
-            // the stage's barrier is theirs: the one running now
-            if (!FP8 && check) ptx::mbar_arrive(bar(&sh.aux[s]));
+            ptx::tma_load_2d(dst, map, bar(&sh.kf[bi]), 0, y);
+            if (!FP8) ptx::tma_load_2d(dst + HALF, map, bar(&sh.kf[bi]), 64, y);
+            // the checking warp looks at some stages only, so it is told which phase of the
+            // stage's barrier is its: the one running now
+            if (!FP8 && which && g.cut(p, jv)) ptx::mbar_arrive(bar(&sh.aux[s]));
             ++at;
-          };
-          // tiles in the order of Geometry::k_at / v_at; Q after the first K is under way
-          int row_k = tile_row(0), row_v = row_k, row_k2 = 0;
-          load(0, row_k, false);
-          if (!stop) load_q(0);
-          if (!stop && g.dual) load_q(1);
-          if (g.dual) {
-            for (int j = 0; j < g.T && !stop; ++j) {
-              if (j + 1 < g.T) row_k = tile_row(j + 1);
-              load(1, row_v, g.cut(p, j));
-              if (!stop && j + 1 < g.T) load(0, row_k, false);
-              row_v = row_k;
-            }
-          } else {
-            int row_v2 = 0;  // rows of tiles j, j + 1, j + 2
-            if (g.T > 1 && !stop) {
-              row_v2 = tile_row(1);
-              load(0, row_v2, false);
-            }
-            for (int j = 0; j < g.T && !stop; ++j) {
-              if (j + 2 < g.T) row_k2 = tile_row(j + 2);
-              load(1, row_v, g.cut(p, j));
-              if (!stop && j + 2 < g.T) load(0, row_k2, false);
-              row_v = row_v2;
-              row_v2 = row_k2;
-            }
+            if (which) ++jv; else ++jk;
           }
           if (stop) break;
         }
@@ -968,9 +994,9 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
             alive = waitw(sh.kf[PL::V_BAR + st], a / PL::STAGES) &&
                     (a < PL::C_STAGES || waitw(sh.aux[cs], a / PL::C_STAGES - 1));
             if (!alive) break;
-            if (convert_v(smem + PL::OFF_KV + (PL::V_BAR + st) * PL::LOAD, smem + PL::OFF_C + cs * TILE, lane, g.valid(j),
-                          g.cut(p, j)))
-              *reinterpret_cast<volatile int*>(&ring[slot].bad) = 1;
+            uint8_t* codes = smem + PL::OFF_KV + (PL::V_BAR + st) * PL::LOAD;
+            if (g.cut(p, j) && drop_nan(codes, lane, g.valid(j))) *reinterpret_cast<volatile int*>(&ring[slot].bad) = 1;
+            convert_v(codes, smem + PL::OFF_C + cs * TILE, lane, g.valid(j));
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -1065,7 +1091,7 @@ cudaError_t chunk_attn_tc(const ChunkAttnParams& a, cudaStream_t s) {
   memset(&p, 0, sizeof(p));
   p.TQ = 128 / a.G;
   p.RT = p.TQ * a.G;
-  p.split = {a.cu_rows, a.kv_lens, a.batch, a.rows, a.n_kv, a.G, a.capacity, a.window, 2 * p.RT, 2 * p.TQ, p.RT, TK,
+  p.split = {a.cu_rows, a.kv_lens, a.batch, a.rows, a.n_kv, a.G, a.capacity, a.window, 2 * p.RT, 2 * p.TQ, p.RT, 7,
              a.fp8 ? 14 : 8, a.fp8 ? 6 : 4, 3};
   const long long kv_rows = a.block_table ? (long long)a.n_pages * a.n_kv * TK
                                           : (long long)a.batch * a.n_kv * a.capacity;
