@@ -374,7 +374,7 @@ typedef struct {
  *                   entered
  *   pages_held      int32 [batch]: pages sequence b holds: entries 0 .. pages_held[b]-1 of
  *                   its row of the table (a crop keeps them)
- *   pages_held_out  int32 [batch], may be pages_held
+ *   pages_held_out  int32 [batch], may be pages_held (but not overlap it otherwise)
  *   free_pages      int32 [n_free]: ids of free pages; entries from *taken on are free
  *   taken           int32 [1]; taken_out int32 [1], may be taken
  */
@@ -404,7 +404,8 @@ typedef struct {
  * not changed; dflash_chunk_append sets them layer by layer. Calling again with the same
  * inputs (separate _out arrays) writes the same results.
  * Host errors: null or misaligned pointers, chunk->batch != cache->batch, a pool whose
- * block_table is not the cache's, negative sizes, a cache of more than 2^31 - 1 slots.
+ * block_table is not the cache's, negative sizes, kv_lens that are the cache's lengths, a
+ * cache of more than 2^31 - 1 slots.
  */
 dflash_status dflash_chunk_map(const dflash_kv_cache* cache, int layer, const dflash_chunk* chunk,
                                const dflash_page_pool* pool, cudaStream_t stream);

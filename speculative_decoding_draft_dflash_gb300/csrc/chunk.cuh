@@ -24,6 +24,7 @@ struct ChunkMapParams {
   unsigned* status;
   int batch, rows, capacity, pages_per_seq, n_pages, n_free;
   bool paged;
+  bool alias;  // held_out is held, or taken_out is taken
 };
 cudaError_t chunk_map(const ChunkMapParams& p, cudaStream_t s);
 

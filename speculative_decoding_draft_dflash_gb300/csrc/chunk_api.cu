@@ -64,7 +64,9 @@ DFLASH_API dflash_status dflash_chunk_map(const dflash_kv_cache* c, int layer,
     p.taken_out = pool->taken_out;
     p.pages_per_seq = c->capacity / c->page_size;
     p.n_pages = c->n_pages;
+    p.alias = pool->pages_held_out == pool->pages_held || pool->taken_out == pool->taken;
   }
+  if (ch->kv_lens == c->lens + (size_t)layer * c->batch) return DFLASH_ERR_INVALID_ARG;
   p.status = status_word();
   if (!p.status) return DFLASH_ERR_CUDA;
   p.cu_rows = ch->cu_rows;

@@ -171,8 +171,9 @@ cudaError_t launch(const ChunkAttnParams& p, cudaStream_t s) {
   const int tiles = (int)sizeof(float) * ((RI + 2 * TK) * (DP + 4) + RI * (TK + 4));
   const int scratch = (int)(chunk::kLocateBytes * p.batch);
   const int smem = tiles > scratch ? tiles : scratch;
-  cudaError_t e = cudaFuncSetAttribute(chunk_attn_simt_kernel<DP>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int most = (int)(chunk::kLocateBytes * kChunkMaxBatch);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(chunk_attn_simt_kernel<DP>, tiles > most ? tiles : most);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_ATTN, s);
   chunk_attn_simt_kernel<DP><<<sm_count(), kThreads, smem, s>>>(p);

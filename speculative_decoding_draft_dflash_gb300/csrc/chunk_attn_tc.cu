@@ -58,8 +58,8 @@ struct Plan {
   static constexpr uint32_t OFF_C = OFF_KV + 6 * (TK * 128);  // E4M3: after K and V
   static constexpr uint32_t OFF_END = OFF_KV + 5 * TILE;
   // registers: the softmax warpgroups take what the others give back (setmaxnreg draws on the
-  // launch's own: 384 x 168 = 256 x 200 + 128 x 104)
-  static constexpr int REG_SOFT = 200, REG_REST = 104;
+  // launch's own: 384 x 168 = 256 x 200 + 128 x 104 = 256 x 208 + 128 x 88)
+  static constexpr int REG_SOFT = FP8 ? 200 : 208, REG_REST = FP8 ? 104 : 88;
   // barriers of the stages (Tail::kf, ke): E4M3 V stages follow the K stages
   static constexpr int V_BAR = FP8 ? 3 : 0;
 };
@@ -1073,8 +1073,8 @@ template <bool FP8>
 cudaError_t launch(const Params& p, cudaStream_t s) {
   constexpr size_t smem = Plan<FP8>::OFF_END + sizeof(Tail);
   static_assert(smem <= 227 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(chunk_attn_tc_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(chunk_attn_tc_kernel<FP8>, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_ATTN, s);
   chunk_attn_tc_kernel<FP8><<<sm_count(), Plan<FP8>::THREADS, smem, s>>>(p);

@@ -60,6 +60,20 @@ unsigned long long wait_limit_ns();
 // SMs of the current device (attn_tc.cu)
 int sm_count();
 
+// Raises a kernel's dynamic shared-memory limit once per device.
+struct SmemLimit {
+  unsigned char done[128] = {};
+  template <typename F> cudaError_t raise(F* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 128 && __atomic_load_n(&done[dev], __ATOMIC_ACQUIRE)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 128) __atomic_store_n(&done[dev], 1, __ATOMIC_RELEASE);
+    return e;
+  }
+};
+
 // per-device sticky status word (defined in dflash_api.cu)
 unsigned* status_word();
 
