@@ -45,119 +45,143 @@ __device__ __forceinline__ void publish_lens(const ChunkAppendParams& p) {
 }
 
 // ---------------------------------------------------------------------------
-// bf16, d_h = 128: half a warp per head, 16 bytes per lane, kUnroll heads in flight. Lane l
-// holds elements 8l .. 8l + 7 of a head, its rotation partner is lane l ^ 8.
+// bf16, d_h = 128: half a warp per head; lane l holds elements 4l .. 4l + 3 of both halves, so
+// that a rotation stays in its lane. Norm weight and rotation are one set of coefficients per
+// row, y_lo = inv (a A - b B), y_hi = inv (b C + a D) with A = g_lo cos, B = g_hi sin,
+// C = g_hi cos, D = g_lo sin; per head that leaves the sum of squares (4 shuffles) and 12
+// packed multiply-adds. (One 16-byte load per lane and the partner's elements by 8 shuffles:
+// 57 us for 9911 rows of 32 + 8 + 8 heads, bound by issue slots.)
 // ---------------------------------------------------------------------------
-constexpr int kUnroll = 4;
-constexpr int kHeadsPerUnit = 2 * kUnroll;  // heads of one row that a warp takes
+constexpr int kUnroll = 2;
+constexpr int kWarps = 4;                     // per CTA
+constexpr int kHeadsPerGroup = 2 * kUnroll;  // heads of one row that a warp has in flight
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(h[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
+__device__ __forceinline__ float2 bf2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  uint4 w;
-  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&w);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-  return w;
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
 
-// A unit is `span` groups of 8 heads of one row: the slot, the position and the (cos, sin) pairs
-// are fetched once per unit, and the next group's rows are in flight while one is worked on.
-__global__ void __launch_bounds__(256) chunk_append_bf16_kernel(const ChunkAppendParams p, int span) {
+// A unit is `span` groups of 4 heads of one row: the slot, the position and the coefficients are
+// made once per unit (and kind of head), and the next group's rows are in flight while one is
+// worked on. Long units and few loads in flight per warp suit HBM better than more warps: 9911
+// rows take 49.9 us (4.9 TB/s) with units of 24 heads, 56 with groups of 8, 74 with units of 8,
+// 79 with a fourth CTA of 256 threads per SM.
+__global__ void __launch_bounds__(32 * kWarps) chunk_append_bf16_kernel(const ChunkAppendParams p, int span) {
   publish_lens(p);
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
   const int n_q = p.q ? p.n_h : 0, heads = n_q + 2 * p.n_kv;
-  const int groups = (heads + kHeadsPerUnit - 1) / kHeadsPerUnit, units = (groups + span - 1) / span;
-  const long long unit = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int r = (int)(unit / units);
+  const int groups = (heads + kHeadsPerGroup - 1) / kHeadsPerGroup, units = (groups + span - 1) / span;
+  const unsigned unit = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int r = (int)(unit / (unsigned)units);
   if (r >= p.rows) return;
-  const int g0 = (int)(unit - (long long)r * units) * span, g1 = min(g0 + span, groups);
-  auto fetch = [&](int g, uint4 (&w)[kUnroll]) {
+  const int g0 = (int)(unit - (unsigned)r * units) * span, g1 = min(g0 + span, groups);
+  // elements 4l .. and 64 + 4l .. of head h
+  auto fetch = [&](int g, uint2 (&w)[kUnroll][2]) {
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int h = g * kHeadsPerUnit + half + 2 * i;
+      const int h = g * kHeadsPerGroup + half + 2 * i;
       if (g >= g1 || h >= heads) continue;
       const bf16* src = h < n_q ? (const bf16*)p.q + (size_t)r * p.ld_q + h * 128
                       : h < n_q + p.n_kv ? (const bf16*)p.k + (size_t)r * p.ld_k + (h - n_q) * 128
                                          : (const bf16*)p.v + (size_t)r * p.ld_v + (h - n_q - p.n_kv) * 128;
-      w[i] = __ldcs(reinterpret_cast<const uint4*>(src) + l);
+      w[i][0] = __ldcs(reinterpret_cast<const uint2*>(src) + l);
+      w[i][1] = __ldcs(reinterpret_cast<const uint2*>(src) + 16 + l);
     }
   };
-  uint4 next[kUnroll];
+  uint2 next[kUnroll][2];
   fetch(g0, next);  // before the slot is known: a skipped row is read in vain
   int slot, pos;
   if (!row_live(p, r, &slot, &pos)) return;
-  // (cos, sin) of this lane's 8 pairs; the upper half-head adds where the lower subtracts
-  float c[8], s[8];
+  // (cos, sin) of this lane's four pairs
+  float2 cs[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   if (p.rope) {
-    const float4* t = reinterpret_cast<const float4*>(p.rope + (size_t)pos * 64 + (l & 7) * 8);
-    const float sign = l < 8 ? -1.f : 1.f;
+    const float4* t = reinterpret_cast<const float4*>(p.rope + (size_t)pos * 64 + l * 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const float4 f = __ldg(t + i);
-      c[2 * i] = f.x;
-      s[2 * i] = sign * f.y;
-      c[2 * i + 1] = f.z;
-      s[2 * i + 1] = sign * f.w;
+      cs[i] = make_float2(f.x, f.z);
+      sn[i] = make_float2(f.y, f.w);
     }
   }
   const int u = slot / p.unit_rows;
   const size_t cache0 = (size_t)u * p.n_kv * p.unit_rows + (slot - u * p.unit_rows);  // head 0's row
+  float2 A[2], B[2], C[2], D[2];
+  int kind = -1;  // of head the coefficients are for: 0 Q, 1 K
 #pragma unroll 1
   for (int g = g0; g < g1; ++g) {
-    uint4 w[kUnroll];
+    uint2 w[kUnroll][2];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) w[i] = next[i];
+    for (int i = 0; i < kUnroll; ++i) {
+      w[i][0] = next[i][0];
+      w[i][1] = next[i][1];
+    }
     fetch(g + 1, next);
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int h = g * kHeadsPerUnit + half + 2 * i;
-      const bool is_q = h < n_q, is_v = h >= n_q + p.n_kv;
+      const int h = g * kHeadsPerGroup + half + 2 * i;
       if (h >= heads) continue;
-      float x[8];
-      unpack8(w[i], x);
-      const void* gamma = is_q ? p.gamma_q : p.gamma_k;
-      if (!is_v && gamma) {
-        float ss = 0.f;
+      const int is = h < n_q ? 0 : h < n_q + p.n_kv ? 1 : 2;
+      if (is < 2) {
+        if (is != kind) {
+          kind = is;
+          const bf16* gamma = (const bf16*)(is == 0 ? p.gamma_q : p.gamma_k);
+          uint2 lo = make_uint2(0x3F803F80u, 0x3F803F80u), hi = lo;  // 1
+          if (gamma) {
+            lo = __ldg(reinterpret_cast<const uint2*>(gamma) + l);
+            hi = __ldg(reinterpret_cast<const uint2*>(gamma) + 16 + l);
+          }
+          const float2 gl[2] = {bf2(lo.x), bf2(lo.y)}, gh[2] = {bf2(hi.x), bf2(hi.y)};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffu << (half * 16), ss, o);
-        const float inv = rsqrtf(ss * (1.f / 128.f) + p.eps);
-        float gm[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(gamma) + l), gm);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * gm[e];
-      }
-      if (!is_v && p.rope) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = __shfl_xor_sync(0xffffu << (half * 16), x[e], 8);
-          x[e] = x[e] * c[e] + y * s[e];
+          for (int e = 0; e < 2; ++e) {
+            A[e] = __fmul2_rn(gl[e], cs[e]);
+            B[e] = neg2(__fmul2_rn(gh[e], sn[e]));
+            C[e] = __fmul2_rn(gh[e], cs[e]);
+            D[e] = __fmul2_rn(gl[e], sn[e]);
+          }
         }
-      }
-      if (is_q) {
-        reinterpret_cast<uint4*>((bf16*)p.q_out + (size_t)r * p.n_h * 128 + h * 128)[l] = pack8(x);
-      } else {
-        const size_t at = (cache0 + (size_t)(is_v ? h - n_q - p.n_kv : h - n_q) * p.unit_rows) * 128 + 8 * l;
-        void* cache = is_v ? p.cache_v : p.cache_k;
-        if (p.fp8) {
-          const float inv = is_v ? p.v_inv : p.k_inv;
-          uint2 code;
-          code.x = e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-          code.y = e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-          *reinterpret_cast<uint2*>((uint8_t*)cache + at) = code;
-        } else {
-          *reinterpret_cast<uint4*>((bf16*)cache + at) = pack8(x);
+        const float2 a[2] = {bf2(w[i][0].x), bf2(w[i][0].y)}, b[2] = {bf2(w[i][1].x), bf2(w[i][1].y)};
+        float inv = 1.f;
+        if (is == 0 ? p.gamma_q != nullptr : p.gamma_k != nullptr) {
+          float2 q = __fmul2_rn(a[0], a[0]);
+          q = __ffma2_rn(a[1], a[1], q);
+          q = __ffma2_rn(b[0], b[0], q);
+          q = __ffma2_rn(b[1], b[1], q);
+          float ss = q.x + q.y;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffu << (half * 16), ss, o);
+          inv = rsqrtf(ss * (1.f / 128.f) + p.eps);
         }
+        const float2 n2 = make_float2(inv, inv);
+        float2 y[2], z[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y[e] = __fmul2_rn(__ffma2_rn(a[e], A[e], __fmul2_rn(b[e], B[e])), n2);
+          z[e] = __fmul2_rn(__ffma2_rn(b[e], C[e], __fmul2_rn(a[e], D[e])), n2);
+        }
+        if (is == 1 && p.fp8) {
+          uint8_t* dst = (uint8_t*)p.cache_k + (cache0 + (size_t)(h - n_q) * p.unit_rows) * 128 + 4 * l;
+          *reinterpret_cast<uint32_t*>(dst) = e4m3x4(y[0].x * p.k_inv, y[0].y * p.k_inv, y[1].x * p.k_inv, y[1].y * p.k_inv);
+          *reinterpret_cast<uint32_t*>(dst + 64) = e4m3x4(z[0].x * p.k_inv, z[0].y * p.k_inv, z[1].x * p.k_inv, z[1].y * p.k_inv);
+          continue;
+        }
+        w[i][0] = make_uint2(pack2(y[0]), pack2(y[1]));
+        w[i][1] = make_uint2(pack2(z[0]), pack2(z[1]));
+      } else if (p.fp8) {
+        const float2 a0 = bf2(w[i][0].x), a1 = bf2(w[i][0].y), b0 = bf2(w[i][1].x), b1 = bf2(w[i][1].y);
+        uint8_t* dst = (uint8_t*)p.cache_v + (cache0 + (size_t)(h - n_q - p.n_kv) * p.unit_rows) * 128 + 4 * l;
+        *reinterpret_cast<uint32_t*>(dst) = e4m3x4(a0.x * p.v_inv, a0.y * p.v_inv, a1.x * p.v_inv, a1.y * p.v_inv);
+        *reinterpret_cast<uint32_t*>(dst + 64) = e4m3x4(b0.x * p.v_inv, b0.y * p.v_inv, b1.x * p.v_inv, b1.y * p.v_inv);
+        continue;
       }
+      bf16* dst = is == 0 ? (bf16*)p.q_out + (size_t)r * p.n_h * 128 + h * 128
+                : (bf16*)(is == 1 ? p.cache_k : p.cache_v) +
+                      (cache0 + (size_t)(is == 1 ? h - n_q : h - n_q - p.n_kv) * p.unit_rows) * 128;
+      reinterpret_cast<uint2*>(dst)[l] = w[i][0];
+      reinterpret_cast<uint2*>(dst)[16 + l] = w[i][1];
     }
   }
 }
@@ -220,17 +244,19 @@ __global__ void __launch_bounds__(256) chunk_append_f32_kernel(const ChunkAppend
 
 cudaError_t chunk_append(int dtype, const ChunkAppendParams& p, cudaStream_t s) {
   const int heads = (p.q ? p.n_h : 0) + 2 * p.n_kv;
-  // bf16: a warp per 8 heads while the rows alone do not fill the GPU, else up to 24 heads
-  const int groups = (heads + kHeadsPerUnit - 1) / kHeadsPerUnit;
-  const int span = (long long)p.rows * groups > 96ll * sm_count() ? 3 : 1;
+  // bf16: a warp per 8 heads while the rows alone do not fill the GPU, else per 24 heads (512
+  // rows: 4.7 and 5.9 us, 9911 rows: 74 and 49.9 us)
+  const int groups = (heads + kHeadsPerGroup - 1) / kHeadsPerGroup;
+  const int span = (long long)p.rows * groups > 192ll * sm_count() ? 6 : 2;
   const int units = dtype == DFLASH_F32 ? heads : (groups + span - 1) / span;
-  const long long grid = ((long long)p.rows * units + 7) / 8;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  const int warps = dtype == DFLASH_F32 ? 8 : kWarps;
+  const long long grid = ((long long)p.rows * units + warps - 1) / warps;
+  if (grid > 0x0fffffffll) return cudaErrorInvalidValue;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_APPEND, s);
   if (dtype == DFLASH_F32)
     chunk_append_f32_kernel<<<(unsigned)grid, 256, 0, s>>>(p);
   else
-    chunk_append_bf16_kernel<<<(unsigned)grid, 256, 0, s>>>(p, span);
+    chunk_append_bf16_kernel<<<(unsigned)grid, 32 * kWarps, 0, s>>>(p, span);
   return cudaGetLastError();
 }
 
