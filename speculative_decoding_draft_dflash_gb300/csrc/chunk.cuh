@@ -74,6 +74,8 @@ size_t chunk_attn_workspace(int dtype, int d_h);
 // Carves part, part_ml and merge out of the workspace; false when it is too small.
 bool chunk_attn_carve(int dtype, int d_h, ChunkAttnParams& p, void* workspace, size_t bytes);
 cudaError_t chunk_attn(int dtype, const ChunkAttnParams& p, cudaStream_t s);
+int chunk_attn_simt_item_rows(int d_h);
+int chunk_attn_simt_ctas(int d_h);
 cudaError_t chunk_attn_simt(const ChunkAttnParams& p, cudaStream_t s);  // f32
 cudaError_t chunk_attn_tc(const ChunkAttnParams& p, cudaStream_t s);    // bf16
 int chunk_attn_tc_item_rows(int G);

@@ -4,10 +4,9 @@
 namespace dflash {
 namespace {
 
-constexpr int kSimtRows = 64;   // stacked query rows of an item (chunk_attn_simt.cu)
-constexpr int kTcRows = 256;    // at most (chunk_attn_tc.cu)
-
-int item_rows(int dtype) { return dtype == DFLASH_F32 ? kSimtRows : kTcRows; }
+// Stacked query rows of an item, at most.
+int item_rows(int dtype, int d_h) { return dtype == DFLASH_F32 ? chunk_attn_simt_item_rows(d_h) : 256; }
+int attn_ctas(int dtype, int d_h) { return dtype == DFLASH_F32 ? chunk_attn_simt_ctas(d_h) : sm_count(); }
 
 // CTA c of the first grid axis merges the item that was cut at the end of attention CTA c's
 // share, if one was. Piece 0 is CTA c's partial 1, piece i > 0 is partial 0 of CTA c + i.
@@ -113,10 +112,11 @@ __global__ void __launch_bounds__(256) chunk_merge_bf16_kernel(const ChunkAttnPa
 }
 
 bool carve(int dtype, int d_h, ChunkAttnParams* p, Carver& cv) {
-  const size_t slots = 2 * (size_t)sm_count() * item_rows(dtype);
+  const int ctas = attn_ctas(dtype, d_h);
+  const size_t slots = 2 * (size_t)ctas * item_rows(dtype, d_h);
   float* part = cv.take<float>(slots * d_h);
   float2* ml = cv.take<float2>(slots);
-  int4* merge = cv.take<int4>((size_t)sm_count());
+  int4* merge = cv.take<int4>((size_t)ctas);
   if (p) {
     p->part = part;
     p->part_ml = ml;
@@ -143,7 +143,7 @@ cudaError_t chunk_attn(int dtype, const ChunkAttnParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_MERGE, s);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sm_count(), dtype == DFLASH_F32 ? 8 : 16);  // every row at once
+  cfg.gridDim = dim3(attn_ctas(dtype, p.d_h), 16);  // every row at once
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -152,7 +152,7 @@ cudaError_t chunk_attn(int dtype, const ChunkAttnParams& p, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return dtype == DFLASH_F32
-             ? cudaLaunchKernelEx(&cfg, chunk_merge_f32_kernel, p, kSimtRows)
+             ? cudaLaunchKernelEx(&cfg, chunk_merge_f32_kernel, p, chunk_attn_simt_item_rows(p.d_h))
              : cudaLaunchKernelEx(&cfg, chunk_merge_bf16_kernel, p, chunk_attn_tc_item_rows(p.G));
 }
 
