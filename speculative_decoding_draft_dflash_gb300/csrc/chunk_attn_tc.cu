@@ -130,7 +130,7 @@ __device__ __forceinline__ bool wait_more(uint32_t bar, uint32_t parity, volatil
                                           uint64_t limit_ns) {
   const uint64_t t0 = ptx::globaltimer();
 #pragma unroll 1
-  while (!__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 10000u))) {
+  while (!__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, (uint32_t)min((uint64_t)10000, limit_ns)))) {
     const bool late = ptx::globaltimer() - t0 > limit_ns;
     if (late) {
       *abort_flag = 1;
@@ -294,8 +294,9 @@ struct Cursor {
 
 // A row of Q to E4M3: two terms of q 2^-e (e: the row's largest exponent - 7, so that nothing
 // overflows), the code and the code of its remainder, in place of the bf16 row, each 128 bytes
-// of the swizzled layout. q is then kept to about 2^-8 of itself, as a bf16 product would.
-// Returns e.
+// of the swizzled layout. The remainder of a bf16's 8 bits has at most 4, so the two hold it
+// exactly down to 2^-9 of the row's largest power of two; below, a remainder under the smallest
+// code is rounded, by at most 2^-17 of that power. Returns e.
 __device__ __noinline__ int q_codes(uint8_t* tile, int row) {
   uint8_t* at = tile + row * 128;
   const int sw = row & 7;
@@ -418,7 +419,10 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = ptx::smem_u32(smem);
   if (sbase & 1023) {  // the swizzled tiles would be misplaced
-    if (threadIdx.x == 0) atomicOr(p.status, DFLASH_DEV_TIMEOUT);
+    if (threadIdx.x == 0) {
+      atomicOr(p.status, DFLASH_DEV_TIMEOUT);
+      p.merge[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
     return;
   }
   auto bar = [](uint64_t* b) { return ptx::smem_u32(b); };

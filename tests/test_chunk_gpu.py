@@ -575,3 +575,187 @@ def test_launches_and_trace_kinds(D):
     s.map(), s.append(q), s.attn(q, out)
     assert D.dflash_launch_count() - n0 == 4
     assert [k for k, _ in D.dflash_trace_stop()] == ["chunk_map", "chunk_append", "chunk_attn", "chunk_merge"]
+
+
+# ---------------------------------------------------------------------------
+# calls at the edges of what the documentation allows
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n_free,short", [(1024, False), (40, True)])   # about 100 pages are asked for
+def test_map_most_sequences(D, n_free, short):
+    B = 8192
+    rng = np.random.Generator(np.random.PCG64(5))
+    lens, rows = rng.integers(0, 300, size=B), rng.integers(0, 4, size=B)
+    args = _map_case(D, lens, rows, 512, [0] * B, n_free, 5, 6, 1)
+    D.dflash_chunk_map(args[0], 0, args[1], args[2])
+    _check_map(*args)
+    assert D.dflash_status_get() == (D.DEV_CAPACITY if short else 0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+def test_append_of_one_slot_twice_stores_one_of_the_rows(D, kv):
+    s = Step(D, kv, (4, 2, 128), [10], [300], paged=kv != "f32", seed=40)
+    s.map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    rows = [[x[:, 10 + i].clone() for x in (s.cache.rows(w, 0, 0, 0, 310) for w in "kv")] for i in (7, 290)]
+    at = [int(s.plan.slots[i]) for i in (7, 290)]
+    pos = s.plan.positions.clone()
+    s.plan.slots[290] = at[0]
+    s.append(q)
+    assert torch.equal(s.plan.positions, pos)
+    got = [x[:, 17] for x in (s.cache.rows(w, 0, 0, 0, 310) for w in "kv")]
+    for w in range(2):
+        assert any(torch.equal(got[w], r[w]) for r in rows)
+    assert D.dflash_status_get() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "f32"])
+def test_attn_many_sequences(D, kv):
+    rng = np.random.Generator(np.random.PCG64(41))
+    B = 1500
+    ctx, rows = rng.integers(0, 140, size=B).tolist(), rng.integers(0, 4, size=B).tolist()
+    s = Step(D, kv, (4, 2, 128), ctx, rows, paged=kv != "f32", pad=2, seed=41, spare=0)
+    s.map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    out = torch.full_like(q, 5.0)
+    s.attn(q, out)
+    assert D.dflash_status_get() == 0
+    s.check_attn(q, out)
+    assert (out[int(s.cu[-1]):] == 5.0).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "f32"])
+def test_step_without_new_rows(D, kv):
+    """Padding only: nothing is written, the lengths stay."""
+    s = Step(D, kv, (4, 2, 128), [5, 130], [0, 0], paged=kv != "f32", pad=3, seed=42)
+    s.map()
+    assert s.plan.kv_lens.tolist() == [5, 130] and s.plan.slots.tolist() == [-1] * 3
+    before = s.cache.k.clone()
+    q = torch.full((s.M, s.n_h * s.d), 2.0, dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    out = torch.full_like(q, 5.0)
+    s.attn(q, out)
+    assert (q == 2.0).all() and (out == 5.0).all() and s.cache.lens[0].tolist() == [5, 130]
+    assert torch.equal(s.cache.k.view(torch.uint8), before.view(torch.uint8))
+    assert D.dflash_status_get() == 0
+
+
+@pytest.mark.parametrize("heads", [(4, 1, 2), (4, 1, 130), (4, 4, 254)])
+def test_attn_f32_widths(D, heads):
+    s = Step(D, "f32", heads, [0, 70, 300], [20, 1, 90], paged=False, seed=43)
+    s.map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    out = torch.empty_like(q)
+    s.attn(q, out)
+    s.check_attn(q, out)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_attn_out_at_16_bytes(D, kv):
+    s = Step(D, kv, (8, 2, 128), [3000, 50], [20, 300], seed=44)
+    s.map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    want = torch.empty_like(q)
+    s.attn(q, want)
+    flat = torch.full((q.numel() + 16,), 5.0, dtype=q.dtype, device=DEV)
+    out = flat[8:8 + q.numel()].view_as(q)
+    assert out.data_ptr() % 32 == 16
+    s.attn(q, out)
+    assert torch.equal(out, want)
+    assert (flat[:8] == 5.0).all() and (flat[8 + q.numel():] == 5.0).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("power", [-60, 60])
+def test_attn_queries_of_any_size(D, kv, power):
+    """Queries 2^60 larger or smaller with a scaling that makes up for it: the same scores, so
+    the same bits."""
+    s = Step(D, kv, (4, 2, 128), [200, 0], [3, 150], paged=kv != "f32", seed=45)
+    s.map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    s.attn(q, want, 0, 0.125)
+    s.attn(q * 2.0 ** power, out, 0, 0.125 * 2.0 ** -power)
+    assert torch.equal(out, want)
+    s.check_attn(q, out, 0, 0.125)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "f32"])
+def test_step_beyond_32_bit_offsets(D, kv):
+    """Rows more than 2^32 bytes into K and V."""
+    if kv == "f32":
+        s = Step(D, kv, (8, 8, 64), [5, 700], [3, 40], paged=False, seed=46, spare=2_200_064)
+        assert s.cap * 8 * 64 * 4 > 2 ** 32
+    else:
+        s = Step(D, kv, (32, 8, 128), [700], [40], seed=46, spare=128 * (40000 if kv == "bf16" else 80000))
+        page_bytes = 8 * 128 * 128 * (2 if kv == "bf16" else 1)
+        assert int(s.cache.block_table[0, :6].max()) * page_bytes > 2 ** 32
+    s.map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    out = torch.empty_like(q)
+    s.attn(q, out)
+    assert D.dflash_status_get() == 0
+    s.check_attn(q, out)
+    k, _ = s.cached(len(s.ctx) - 1, s.ctx[-1] + s.rows[-1])
+    assert np.isfinite(k).all() and (k[s.ctx[-1]:] != 0).any()
+
+
+def test_two_graphs_with_their_own_workspaces(D):
+    steps = [Step(D, "bf16", (32, 8, 128), [3000, 50], [20, 300], seed=50 + i) for i in range(2)]
+    graphs, outs, want = [], [], []
+    for s in steps:
+        s.map()
+        q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+        s.append(q)
+        want.append(torch.empty_like(q))
+        s.attn(q, want[-1])
+        outs.append(torch.empty_like(q))
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            s.attn(q, outs[-1])
+        graphs.append((gr, q))
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(10):
+        for (gr, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    assert D.dflash_status_get() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_attn_that_gives_up_leaves_a_working_gpu(D, kv):
+    """With a limit of 1 ns the roles of the kernel stop at their first wait. Copies and MMAs
+    in flight are waited for and tensor memory is freed; the next call is right."""
+    # the warp that checks the tiles at the mask's edge first waits for tens of microseconds
+    s = Step(D, kv, (32, 8, 128), [100_000], [64], seed=60)
+    s.map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    s.attn(q, want)
+    assert D.dflash_status_get() == 0
+    st = 0
+    try:
+        D.dflash_test_wait_limit(1)
+        for _ in range(3):
+            s.attn(q, out)
+            st |= D.dflash_status_get()
+            if st & D.DEV_TIMEOUT:
+                break
+    finally:
+        D.dflash_test_wait_limit(0)
+    assert st == D.DEV_TIMEOUT
+    out.fill_(float("nan"))
+    s.attn(q, out)
+    assert D.dflash_status_get() == 0
+    assert torch.equal(out, want)

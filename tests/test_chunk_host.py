@@ -65,6 +65,8 @@ def test_map_refuses_other_arguments(D):
     assert _map(D, no_pool=True) == INVALID                            # paged without a pool
     assert _map(D, layer=2) == INVALID and _map(D, layer=-1) == INVALID
     assert _map(D, cache=_cache(D, page_size=64)) == INVALID
+    assert _map(D, chunk=_chunk(D, kv_lens=256)) == INVALID            # the cache's own lengths
+    assert _map(D, chunk=_chunk(D, kv_lens=272), layer=1) == INVALID
     assert _map(D, cache=_cache(D, capacity=500)) == INVALID           # not whole pages
     assert _map(D, cache=_cache(D, n_pages=1 << 24)) == UNSUPPORTED    # 2^31 slots
     assert _map(D, cache=_cache(D, batch=8193), chunk=_chunk(D, batch=8193)) == UNSUPPORTED
@@ -118,6 +120,11 @@ def test_attn_refuses_sizes(D):
     assert _attn(D, chunk=_chunk(D, rows=0)) == OK
     assert _attn(D, cache=_cache(D, n_pages=1 << 21)) == UNSUPPORTED    # 2^31 key rows of a layer
     assert _attn(D, dims=_dims(D, n_h=136, n_kv=1)) == UNSUPPORTED      # more than 128 query heads a KV head
+    one = dict(batch=1, paged=False)
+    assert _attn(D, dims=_dims(D, n_h=8, n_kv=1), cache=_cache(D, capacity=(1 << 28) + 1, **one),
+                 chunk=_chunk(D, batch=1)) == UNSUPPORTED
+    assert _attn(D, chunk=_chunk(D, rows=(1 << 28) + 1)) == UNSUPPORTED   # 2^30 stacked rows
+    assert _attn(D, cache=_cache(D, batch=8193), chunk=_chunk(D, batch=8193)) == UNSUPPORTED
     assert D.dflash_chunk_workspace_bytes(_dims(D)) > 0
     assert D.dflash_chunk_workspace_bytes(_dims(D, d_h=64)) == 0
 
