@@ -266,6 +266,13 @@ struct Geometry {
     const int k = key0 + j * TK;
     return k + TK - 1 > first || (p.split.window > 0 && last - k >= p.split.window);
   }
+  // E4M3: which warps turn the Q tile of accumulator X into codes. More than 32 rows: its softmax
+  // warps, a thread per row. At most 32: the checking warp, which is free before the softmax is
+  // through with the last item (64 decoded tokens: 150 us, by the softmax 160; 32 blocks of 64
+  // rows: 68 us, by the softmax 64).
+  __device__ __forceinline__ bool coded_by_softmax(const Params& p, int X) const {
+    return dual || (X == 0 && (last - first + 1) * p.split.G > 32);
+  }
   // keys of tile j that some row may see, counted from its start
   __device__ __forceinline__ int valid(int j) const { return min(TK, last + 1 - (key0 + j * TK)); }
   // Where V_j stands among the item's 2 T operand tiles. Two row tiles: K0 V0 K1 V1 ..;
@@ -518,7 +525,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
       const int step = g.dual ? 1 : 2;
       int done = 0;  // tiles of this accumulator
       if (FP8 && g.T > 0) {
-        if (g.dual) {
+        if (g.coded_by_softmax(p, X)) {
           if (!waits(sh.qf[X], nq)) break;
           if (valid) sh.qexp[X][r] = (signed char)q_codes(smem + X * TILE, r);
           ptx::fence_proxy_async_smem();
@@ -982,10 +989,9 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         bool alive = true;
         if constexpr (FP8) {
           // -------------------------------------------------------------- Q codes
-          // (of two row tiles each softmax warpgroup makes its own)
           if (g.T > 0) alive = waitw(sh.qf[0], nq++);
           if (!alive) break;
-          if (g.T > 0 && !g.dual) {
+          if (g.T > 0 && !g.coded_by_softmax(p, 0)) {
             const int rows = min(p.RT, (g.last - g.first + 1) * p.split.G);
             for (int row = lane; row < rows; row += 32) sh.qexp[0][row] = (signed char)q_codes(smem, row);
             ptx::fence_proxy_async_smem();
