@@ -404,8 +404,8 @@ typedef struct {
  * not changed; dflash_chunk_append sets them layer by layer. Calling again with the same
  * inputs (separate _out arrays) writes the same results.
  * Host errors: null or misaligned pointers, chunk->batch != cache->batch, a pool whose
- * block_table is not the cache's, negative sizes, kv_lens that are the cache's lengths, a
- * cache of more than 2^31 - 1 slots.
+ * block_table is not the cache's, negative sizes, kv_lens that are the cache's lengths;
+ * unsupported: a cache of more than 2^31 - 1 slots, more than 8192 sequences.
  */
 dflash_status dflash_chunk_map(const dflash_kv_cache* cache, int layer, const dflash_chunk* chunk,
                                const dflash_page_pool* pool, cudaStream_t stream);
@@ -424,8 +424,11 @@ dflash_status dflash_chunk_map(const dflash_kv_cache* cache, int layer, const df
  *                  strides multiples of 8. q may be NULL (K and V only; q_out NULL)
  *   gamma_q, gamma_k  device [d_h], or NULL: no norm
  *   rope_table     device table of dflash_rope_table_build, table_len positions, or NULL
- *                  (table_len 0): no rotation
- *   q_out          device [rows][n_h * d_h]; may be q when ld_q = n_h * d_h
+ *                  (table_len 0): no rotation. bf16: 16-byte aligned (a buffer's start is)
+ *   q_out          device [rows][n_h * d_h], bf16: 16-byte aligned; may be q when
+ *                  ld_q = n_h * d_h, else overlapping none of q, k, v
+ * Types and layouts as for the other calls: bf16 with d_h = 128 on a contiguous or paged
+ * cache of bf16 rows or E4M3 codes; f32 (d_h even, at most 256) on a contiguous f32 cache.
  * A slot beyond the cache sets DFLASH_DEV_PAGE, a position beyond the table DFLASH_DEV_ROPE:
  * the row is skipped; a sequence that reaches beyond the table keeps its length. Two rows
  * with the same slot: either one is stored.
@@ -454,7 +457,11 @@ dflash_status dflash_chunk_append(const dflash_dims* dims, const dflash_kv_cache
  * Reads chunk->cu_rows and kv_lens, not slots or positions. kv_lens[b] outside
  * [0, capacity] sets DFLASH_DEV_CAPACITY and the rows are zero; rows that are not a valid
  * range set DFLASH_DEV_ROWS and are skipped; a page id outside the pool sets
- * DFLASH_DEV_PAGE and reads as zeros.
+ * DFLASH_DEV_PAGE and reads as zeros. bf16: weights are rounded to bf16 for the product with
+ * V (E4M3: to f16), sums and maxima are fp32; the same inputs give the same bits.
+ * Unsupported: more than 8192 sequences, a capacity above 2^28, rows * G above 2^30, a layer of
+ * more than 2^31 - 1 key rows (slots * n_kv), bf16 with G above 128. The status word may also
+ * get DFLASH_DEV_TIMEOUT, as from every call with pipeline waits.
  */
 size_t dflash_chunk_workspace_bytes(const dflash_dims* dims);
 dflash_status dflash_chunk_attn(const dflash_dims* dims, const dflash_kv_cache* cache, int layer,

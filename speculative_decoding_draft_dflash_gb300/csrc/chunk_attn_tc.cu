@@ -14,8 +14,29 @@
 //
 // One persistent CTA per SM. Warps: 0-3 softmax of A, 4-7 softmax of B (a thread per row, all
 // 128 columns: no exchange between threads), 8 work list and TMA loads, 9 and 10 MMA issue for
-// A and B, 11 (bf16) check of the V tiles that the mask cuts, (E4M3) Q to codes and V to f16. Tensor memory: S_A, S_B, O_A, O_B of 128 columns each; P (16 bits)
-// overwrites the first half of its S and is the A operand of the PV product from there.
+// A and B, 11 (bf16) check of the V tiles that the mask cuts, (E4M3) Q to codes and V to f16.
+// Tensor memory: S_A, S_B, O_A, O_B of 128 columns each; P (16 bits) overwrites the first half
+// of its S and is the A operand of the PV product from there. P is rounded to bf16 next to a
+// bf16 V, as V was; next to E4M3 values to f16, which holds them exactly.
+//
+// What bounds it. Many rows: the MMAs (1024 cycles a key tile and row tile with both products)
+// and the exponentials (128 x 128 at 16 a cycle and SM: 1024 too), which A and B overlap: 2800
+// to 3000 cycles per key tile of two row tiles, of which 2048 are MMAs. 8192 rows of 32 heads
+// from position 0: 354 us, 1.55 PFLOP/s of the 1.91 of a large matrix product. Few rows: HBM, as
+// long as an item is long (294400 keys of 8 heads read by single tokens: 188 us, 6.4 of 6.8 TB/s);
+// each further item costs about 3.7 us, in which the last tile's chain of S, softmax, PV and
+// epilogue has nothing behind it (32 blocks of 16 tokens over 256 to 4096 keys: 70 us, 4.9 TB/s).
+// E4M3 with few rows: 1990 cycles a tile on long sequences (294400 keys: 127 us, 4.7 TB/s) where
+// HBM would allow 1400, with the tensor pipe busy for 46 %. Neither the conversion of V (a
+// quarter of it: the same time) nor the length of the softmax (below) sets that; shared memory is
+// what remains, which Q, K twice (the codes of Q and of its remainder), V in both forms and the
+// copies take for 1408 cycles a tile at its full rate.
+//
+// Tried and slower. P as three E5M2 terms and V as stored, with no conversion (20 MMAs a tile
+// for 16, and the terms cost the softmax 420 instructions: 64 tokens 150 -> 200 us). Keys x rows
+// for few rows, a key per thread and P through shared memory (64 rows 70 -> 132 us: at 10
+// cycles an instruction the four warps wait for tensor memory and for one another). Q repeated
+// in its tile so that each 32 lanes take a quarter of the keys (64 tokens 150 -> 167 us).
 //
 // A masked key has weight exactly 0, and its V row must not enter even as 0 * NaN. In tiles
 // that are not visible to every row of the item, the checking warps replace what is not finite

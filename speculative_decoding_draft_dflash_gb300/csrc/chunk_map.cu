@@ -14,6 +14,7 @@
 // caller's outputs are the inputs (pages held, pages taken): then the CTAs are one cluster, and
 // the first writes once all have read. (One cluster whose first CTA plans for the others took
 // 13 us for 69687 rows of 256 sequences: two more dependent loads and a cluster barrier.)
+// Measured (replayed in a graph): 512 rows of 32 sequences 3.8 us, 69687 rows of 256 4.5 us.
 #include "chunk.cuh"
 #include "sm100_ptx.cuh"
 

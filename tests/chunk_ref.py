@@ -107,7 +107,14 @@ def attention_bound(out, mag, big, keys, d, dtype):
     exponent's argument by a few half-steps of its size, under the same sum), an exponential
     by 2^-21 relative; both enter numerator and denominator. Sums over the keys: `keys`
     half-steps each (a tile's sum, then one addition per tile or split). bf16: weights are
-    rounded to bf16 once for the product with V, the output once."""
+    rounded to bf16 once for the product with V, the output once.
+
+    An E4M3 cache is held to the bf16 bound: its weights are rounded to f16 (2^-11), which leaves
+    2^-8 - 2^-11 for the queries, whose two codes are off by at most 2^-17 of the row's largest
+    power of two: scores by 2^-17 max|q| sum|k| scaling, weights (numerator and denominator) by
+    twice that. So max|q| sum|k| scaling <= (2^-8 - 2^-11) 2^16 = 224 is asked of the inputs: a
+    normed query of 128 dims has no element above sqrt(128) 1.8 = 20.4, normal keys average below
+    0.9 in magnitude, and 20.4 * 128 * 0.9 * 128^-0.5 = 208."""
     rel = 2 * ((d + 8) * U32 * max(big, 1.0) + 2.0 ** -21 + keys * U32)
     err = mag * rel
     if dtype == "f32":
