@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DP)) chunk_attn_simt_ker
   __shared__ chunk::Start start;
   const chunk::Split<false> split = {p.cu_rows, p.kv_lens, p.batch, p.rows, p.n_kv, p.G, p.capacity,
                               p.window, RI, 0, RI / (RI > 64 ? 2 : 4), 6, 2, 6, RI > 64 ? 3 : 2};
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be scheduled
   chunk::locate(split, smem4, &start, p.status);
   chunk::Walker<false> walk;
   walk.init(split, start);
