@@ -431,7 +431,7 @@ dflash_status dflash_chunk_map(const dflash_kv_cache* cache, int layer, const df
  * cache of bf16 rows or E4M3 codes; f32 (d_h even, at most 256) on a contiguous f32 cache.
  * A slot beyond the cache sets DFLASH_DEV_PAGE, a position beyond the table DFLASH_DEV_ROPE:
  * the row is skipped; a sequence that reaches beyond the table keeps its length. Two rows
- * with the same slot: either one is stored.
+ * with the same slot (no map gives them) leave each element from one or the other.
  */
 dflash_status dflash_chunk_append(const dflash_dims* dims, const dflash_kv_cache* cache, int layer,
                                   const dflash_chunk* chunk, const void* q, long long ld_q,

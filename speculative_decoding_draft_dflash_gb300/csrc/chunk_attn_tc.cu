@@ -27,10 +27,10 @@
 // each further item costs about 3.7 us, in which the last tile's chain of S, softmax, PV and
 // epilogue has nothing behind it (32 blocks of 16 tokens over 256 to 4096 keys: 70 us, 4.9 TB/s).
 // E4M3 with few rows: 1990 cycles a tile on long sequences (294400 keys: 127 us, 4.7 TB/s) where
-// HBM would allow 1400, with the tensor pipe busy for 46 %. Neither the conversion of V (a
-// quarter of it: the same time) nor the length of the softmax (below) sets that; shared memory is
-// what remains, which Q, K twice (the codes of Q and of its remainder), V in both forms and the
-// copies take for 1408 cycles a tile at its full rate.
+// HBM would allow 1400, with the tensor pipe busy for 46 %: the chain of S, softmax and PV, of
+// which the two halves of the keys are all that overlaps. No link of it alone sets the time: with
+// half the MMAs of S it would be 122 us, with half of PV's 124, with a quarter of V converted
+// 120, with all three 116; a softmax of 32 columns a thread is no faster either (below).
 //
 // Tried and slower. P as three E5M2 terms and V as stored, with no conversion (20 MMAs a tile
 // for 16, and the terms cost the softmax 420 instructions: 64 tokens 150 -> 200 us). Keys x rows

@@ -465,18 +465,32 @@ def _rows(t, what, dtype, rows, width):
     lie apart (a slice of a fused projection's output)."""
     if not t.is_cuda:
         raise ValueError(f"{what}: expected a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{what}: element type {t.dtype}, the call needs {dtype}")
-    if t.get_device() != _current_device():
-        raise ValueError(f"{what}: on device {t.get_device()}, the current one is {_current_device()}")
+    dev = _current_device()
     shape, st = t.shape, t.stride()
-    dense = (len(shape) == 2 and shape[1] == width and st[1] == 1) or (
-        len(shape) == 3 and shape[1] * shape[2] == width and st[2] == 1 and
-        (st[1] == shape[2] or shape[1] == 1))
-    if not dense or shape[0] < rows:
+    if len(shape) == 2:
+        dense = shape[1] == width and st[1] == 1
+    else:
+        dense = (len(shape) == 3 and shape[1] * shape[2] == width and st[2] == 1 and
+                 (st[1] == shape[2] or shape[1] == 1))
+    n = shape[0] if dense else -1
+    if n < rows or t.dtype is not dtype or t.get_device() != dev:
+        if t.dtype != dtype:
+            raise ValueError(f"{what}: element type {t.dtype}, the call needs {dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: on device {t.get_device()}, the current one is {dev}")
         raise ValueError(f"{what}: shape {tuple(shape)}, strides {st}; the call needs {rows} rows "
                          f"of {width} dense elements")
-    return t.data_ptr(), st[0] if shape[0] > 1 else width
+    return t.data_ptr(), st[0] if n > 1 else width
+
+
+def _array(t, what, dtype, numel):
+    """_ptr of a tensor (or None) as a plain address: the calls that run once per layer and step
+    pay for every object they make."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
+    return _ptr(t, what, dtype, numel)  # (says what is wrong)
 
 
 def _chunk(plan, cache):
@@ -504,17 +518,18 @@ def dflash_chunk_append(dims, cache, layer, plan, q, k, v, gamma_q, gamma_k, rop
                         q_out, stream=None):
     """Norm, RoPE and store of a step's rows in one layer; q and q_out may be None."""
     desc, et, d_h, rows = _desc(dims, cache), _et(dims), dims.d_h, plan.rows
-    qw, kw = dims.n_h * d_h, dims.n_kv * d_h
+    qw, kw, table_len = dims.n_h * d_h, dims.n_kv * d_h, int(table_len)
     qp, ldq = (None, 0) if q is None else _rows(q, "q", et, rows, qw)
     kp, ldk = _rows(k, "k", et, rows, kw)
     vp, ldv = _rows(v, "v", et, rows, kw)
     _check(_lib.dflash_chunk_append(ctypes.byref(dims), ctypes.byref(desc), int(layer),
                                     _chunk(plan, desc), qp, ldq, kp, ldk, vp, ldv,
-                                    _ptr(gamma_q, "gamma_q", et, d_h),
-                                    _ptr(gamma_k, "gamma_k", et, d_h),
-                                    None if rope_table is None else _rope(dims, rope_table, table_len),
-                                    int(table_len), _ptr(q_out, "q_out", et, rows * qw),
-                                    _stream(stream)), "dflash_chunk_append")
+                                    _array(gamma_q, "gamma_q", et, d_h),
+                                    _array(gamma_k, "gamma_k", et, d_h),
+                                    _array(rope_table, "rope_table", torch.float32,
+                                           max(0, table_len) * d_h), table_len,
+                                    _array(q_out, "q_out", et, rows * qw), _stream(stream)),
+           "dflash_chunk_append")
 
 
 def dflash_chunk_workspace_bytes(dims):
@@ -529,7 +544,7 @@ def dflash_chunk_attn(dims, cache, layer, plan, q, sliding_window, scaling, out,
     qp, ldq = _rows(q, "q", et, plan.rows, qw)
     _check(_lib.dflash_chunk_attn(ctypes.byref(dims), ctypes.byref(desc), int(layer),
                                   _chunk(plan, desc), qp, ldq, int(sliding_window), float(scaling),
-                                  _ptr(out, "out", et, plan.rows * qw), *_ws(workspace),
+                                  _array(out, "out", et, plan.rows * qw), *_ws(workspace),
                                   _stream(stream)), "dflash_chunk_attn")
 
 

@@ -593,7 +593,7 @@ def test_map_most_sequences(D, n_free, short):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "f32"])
-def test_append_of_one_slot_twice_stores_one_of_the_rows(D, kv):
+def test_append_of_one_slot_twice_stores_elements_of_the_two_rows(D, kv):
     s = Step(D, kv, (4, 2, 128), [10], [300], paged=kv != "f32", seed=40)
     s.map()
     q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
@@ -605,8 +605,8 @@ def test_append_of_one_slot_twice_stores_one_of_the_rows(D, kv):
     s.append(q)
     assert torch.equal(s.plan.positions, pos)
     got = [x[:, 17] for x in (s.cache.rows(w, 0, 0, 0, 310) for w in "kv")]
-    for w in range(2):
-        assert any(torch.equal(got[w], r[w]) for r in rows)
+    for w in range(2):   # (no order among the rows' heads is promised)
+        assert ((got[w] == rows[0][w]) | (got[w] == rows[1][w])).all()
     assert D.dflash_status_get() == 0
 
 
