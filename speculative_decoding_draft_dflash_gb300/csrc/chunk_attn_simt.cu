@@ -16,11 +16,12 @@
 // each: the next K tile is copied in while the PV product runs, the next V tile during the next
 // scores. Two CTAs share an SM up to d_h 64, and one computes while the other waits at a barrier.
 //
-// Measured on 6 prompts of 65 to 600 rows over up to 900 held, 8 heads of 64: 133 us, where the
-// multiply-adds of whole tiles alone are 47; the pipe is busy for half of the time, and shares of
-// about six tiles a CTA end up to a fifth apart. The same with 64-row items, one CTA per SM and
-// single multiply-adds: 189 us; pairs alone 176, 128-row items 168, two CTAs 148, idle warps
-// skipped 144, Q read a row per thread 134.
+// Measured on 6 prompts of 65 to 600 rows over up to 900 held, 8 heads of 64: 131 us, where the
+// multiply-adds of whole tiles alone are 47. On one prompt of 8192 rows, where neither ragged tiles
+// nor uneven shares (up to a fifth apart at six tiles a CTA) count: 1.64 ms, 42 TFLOP/s, the pipe
+// busy for half of the time. The same with 64-row items, one CTA per SM and single multiply-adds:
+// 189 us; pairs alone 176, 128-row items 168, two CTAs 148, idle warps skipped 144, Q read a row
+// per thread 133, no mask where every row sees every key 131.
 #include "chunk.cuh"
 
 namespace dflash {
@@ -97,13 +98,10 @@ __device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Pie
     Qs[(c0 + 2) * LQ + r] = x.z;
     Qs[(c0 + 3) * LQ + r] = x.w;
   }
-  int pos[RPT];
   float m[RPT], l[RPT];
   float2 o[RPT][DP / 32];  // columns 4 tx + 64 c .. + 3 in pairs
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
-    const int r = ty * RPT + i;
-    pos[i] = r < rows ? w.kv - w.n + (r0 + r) / p.G : -1;
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
@@ -117,6 +115,7 @@ __device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Pie
   for (int j = w.tile0; j < w.tile1; ++j) {
     const int k0 = w.k0 + j * TK;
     const bool sees = k0 <= wlast && k0 + TK > wfirst;
+    const bool open = k0 + TK - 1 <= first && (p.window <= 0 || last - k0 < p.window);  // every key by every row
     const bool more = j + 1 < w.tile1;
     copy_wait<1>();  // K_j (V_j may be on its way)
     __syncthreads();
@@ -169,12 +168,17 @@ __device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Pie
     for (int i = 0; i < RPT; ++i) {
       float mx = m[i];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int key = k0 + tx + 16 * k;
-        const bool in = key <= pos[i] && (p.window <= 0 || pos[i] - key < p.window);
-        s[i][k] = in ? s[i][k] * p.scaling : -INFINITY;
-        mx = fmaxf(mx, s[i][k]);
+      for (int k = 0; k < 4; ++k) s[i][k] *= p.scaling;
+      if (!open) {
+        const int r = ty * RPT + i, pos = r < rows ? w.kv - w.n + (r0 + r) / p.G : -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = k0 + tx + 16 * k;
+          if (key > pos || (p.window > 0 && pos - key >= p.window)) s[i][k] = -INFINITY;
+        }
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx = fmaxf(mx, s[i][k]);
 #pragma unroll
       for (int of = 8; of > 0; of >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
       const float ref = mx == -INFINITY ? 0.f : mx;
@@ -195,7 +199,7 @@ __device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Pie
     __syncthreads();  // (and P)
     // A key that a row does not see has weight 0, and its value must not enter even as 0 * NaN:
     // where the mask cuts a tile that holds such values, zero weights are skipped.
-    bool plain = k0 + TK - 1 <= first && (p.window <= 0 || last - k0 < p.window);
+    bool plain = open;
     if (!plain) {
       float zero = 0.f;
       for (int i = threadIdx.x; i < TK * DP / 4; i += kThreads) {
