@@ -52,9 +52,7 @@ __device__ __forceinline__ void publish_lens(const ChunkAppendParams& p) {
 // packed multiply-adds. (One 16-byte load per lane and the partner's elements by 8 shuffles:
 // 57 us for 9911 rows of 32 + 8 + 8 heads, bound by issue slots.)
 // ---------------------------------------------------------------------------
-constexpr int kUnroll = 2;
 constexpr int kWarps = 4;                     // per CTA
-constexpr int kHeadsPerGroup = 2 * kUnroll;  // heads of one row that a warp has in flight
 
 __device__ __forceinline__ float2 bf2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -65,35 +63,48 @@ __device__ __forceinline__ uint32_t pack2(float2 v) {
 }
 __device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
 
-// A unit is `span` groups of 4 heads of one row: the slot, the position and the coefficients are
-// made once per unit (and kind of head), and the next group's rows are in flight while one is
-// worked on. Long units and few loads in flight per warp suit HBM better than more warps: 9911
-// rows take 49.9 us (4.9 TB/s) with units of 24 heads, 56 with groups of 8, 74 with units of 8,
-// 79 with a fourth CTA of 256 threads per SM.
-__global__ void __launch_bounds__(32 * kWarps) chunk_append_bf16_kernel(const ChunkAppendParams p, int span) {
+// A unit is `span` heads of one row, two at a time: the slot, the position and the coefficients
+// are made once per unit (and kind of head), and the next 2 U heads are in flight while as many are
+// worked on. Addresses advance by a step and are looked up again where a tensor ends; Q, K and V
+// take the same way (V's products are not used), so the halves of a warp stay together. Bound
+// by HBM and issue slots: 9911 rows of 32 + 8 + 8 heads 46.2 us (5.3 TB/s; with addresses and
+// branches per head 49.9), 512 rows 4.2 us, five prompts on E4M3 20.8 us. More warps instead of
+// long units, and fewer registers with more CTAs, were slower (56 to 79 us).
+template <bool FP8, int U>
+__global__ void __launch_bounds__(32 * kWarps, U == 2 ? 7 : 5) chunk_append_bf16_kernel(const ChunkAppendParams p, int span) {
   publish_lens(p);
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-  const int n_q = p.q ? p.n_h : 0, heads = n_q + 2 * p.n_kv;
-  const int groups = (heads + kHeadsPerGroup - 1) / kHeadsPerGroup, units = (groups + span - 1) / span;
+  const int n_q = p.q ? p.n_h : 0, n_k = n_q + p.n_kv, heads = n_k + p.n_kv;
+  const int units = (heads + span - 1) / span;
   const unsigned unit = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int r = (int)(unit / (unsigned)units);
   if (r >= p.rows) return;
-  const int g0 = (int)(unit - (unsigned)r * units) * span, g1 = min(g0 + span, groups);
-  // elements 4l .. and 64 + 4l .. of head h
-  auto fetch = [&](int g, uint2 (&w)[kUnroll][2]) {
+  const int h0 = (int)(unit - (unsigned)r * units) * span, h1 = min(h0 + span, heads);
+  // Where this half warp reads: head lh, up to the end of its tensor.
+  int lh = h0 + half, lend = 0;
+  const uint2* src = nullptr;
+  auto seek = [&]() {
+    const bf16* t = lh < n_q ? (const bf16*)p.q + (size_t)r * p.ld_q + lh * 128
+                  : lh < n_k ? (const bf16*)p.k + (size_t)r * p.ld_k + (lh - n_q) * 128
+                             : (const bf16*)p.v + (size_t)r * p.ld_v + (lh - n_k) * 128;
+    src = reinterpret_cast<const uint2*>(t) + l;
+    lend = min(h1, lh < n_q ? n_q : lh < n_k ? n_k : heads);
+  };
+  // elements 4l .. and 64 + 4l .. of the next heads
+  auto fetch = [&](uint2 (&w)[U][2]) {
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int h = g * kHeadsPerGroup + half + 2 * i;
-      if (g >= g1 || h >= heads) continue;
-      const bf16* src = h < n_q ? (const bf16*)p.q + (size_t)r * p.ld_q + h * 128
-                      : h < n_q + p.n_kv ? (const bf16*)p.k + (size_t)r * p.ld_k + (h - n_q) * 128
-                                         : (const bf16*)p.v + (size_t)r * p.ld_v + (h - n_q - p.n_kv) * 128;
-      w[i][0] = __ldcs(reinterpret_cast<const uint2*>(src) + l);
-      w[i][1] = __ldcs(reinterpret_cast<const uint2*>(src) + 16 + l);
+    for (int i = 0; i < U; ++i) {
+      if (lh >= lend && lh < h1) seek();
+      if (lh < h1) {
+        w[i][0] = __ldcs(src);
+        w[i][1] = __ldcs(src + 16);
+      }
+      src += 64;
+      lh += 2;
     }
   };
-  uint2 next[kUnroll][2];
-  fetch(g0, next);  // before the slot is known: a skipped row is read in vain
+  uint2 next[U][2] = {};
+  fetch(next);  // before the slot is known: a skipped row is read in vain
   int slot, pos;
   if (!row_live(p, r, &slot, &pos)) return;
   // (cos, sin) of this lane's four pairs
@@ -109,79 +120,86 @@ __global__ void __launch_bounds__(32 * kWarps) chunk_append_bf16_kernel(const Ch
   }
   const int u = slot / p.unit_rows;
   const size_t cache0 = (size_t)u * p.n_kv * p.unit_rows + (slot - u * p.unit_rows);  // head 0's row
+  // Where it writes: head h of kind 0 Q, 1 K, 2 V, the coefficients of that kind.
+  int h = h0 + half, hend = h, kind = 0;
+  char* dst = nullptr;
+  long long step = 0;
+  bool norm = false;
   float2 A[2], B[2], C[2], D[2];
-  int kind = -1;  // of head the coefficients are for: 0 Q, 1 K
-#pragma unroll 1
-  for (int g = g0; g < g1; ++g) {
-    uint2 w[kUnroll][2];
+  auto turn = [&]() {
+    kind = h < n_q ? 0 : h < n_k ? 1 : 2;
+    hend = min(h1, kind == 0 ? n_q : kind == 1 ? n_k : heads);
+    const int kh = h - (kind == 0 ? 0 : kind == 1 ? n_q : n_k);
+    const int bytes = FP8 && kind > 0 ? 128 : 256;
+    const size_t row = kind == 0 ? (size_t)r * p.n_h + kh : cache0 + (size_t)kh * p.unit_rows;
+    dst = (char*)(kind == 0 ? p.q_out : kind == 1 ? p.cache_k : p.cache_v) + row * bytes + l * (bytes >> 5);
+    step = 2ll * bytes * (kind == 0 ? 1 : p.unit_rows);
+    const bf16* gamma = (const bf16*)(kind == 0 ? p.gamma_q : p.gamma_k);
+    norm = gamma != nullptr;
+    uint2 lo = make_uint2(0x3F803F80u, 0x3F803F80u), hi = lo;  // 1
+    if (norm) {
+      lo = __ldg(reinterpret_cast<const uint2*>(gamma) + l);
+      hi = __ldg(reinterpret_cast<const uint2*>(gamma) + 16 + l);
+    }
+    const float2 gl[2] = {bf2(lo.x), bf2(lo.y)}, gh[2] = {bf2(hi.x), bf2(hi.y)};
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
+    for (int e = 0; e < 2; ++e) {
+      A[e] = __fmul2_rn(gl[e], cs[e]);
+      B[e] = neg2(__fmul2_rn(gh[e], sn[e]));
+      C[e] = __fmul2_rn(gh[e], cs[e]);
+      D[e] = __fmul2_rn(gl[e], sn[e]);
+    }
+  };
+  const int pairs = (h1 - h0 + 1) >> 1;
+#pragma unroll 1
+  for (int s = 0; s < pairs; s += U) {
+    uint2 w[U][2];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
       w[i][0] = next[i][0];
       w[i][1] = next[i][1];
     }
-    fetch(g + 1, next);
+    fetch(next);
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int h = g * kHeadsPerGroup + half + 2 * i;
-      if (h >= heads) continue;
-      const int is = h < n_q ? 0 : h < n_q + p.n_kv ? 1 : 2;
-      if (is < 2) {
-        if (is != kind) {
-          kind = is;
-          const bf16* gamma = (const bf16*)(is == 0 ? p.gamma_q : p.gamma_k);
-          uint2 lo = make_uint2(0x3F803F80u, 0x3F803F80u), hi = lo;  // 1
-          if (gamma) {
-            lo = __ldg(reinterpret_cast<const uint2*>(gamma) + l);
-            hi = __ldg(reinterpret_cast<const uint2*>(gamma) + 16 + l);
-          }
-          const float2 gl[2] = {bf2(lo.x), bf2(lo.y)}, gh[2] = {bf2(hi.x), bf2(hi.y)};
+    for (int i = 0; i < U; ++i) {  // (both halves of the warp stay together)
+      if (h >= hend && h < h1) turn();
+      const float2 a[2] = {bf2(w[i][0].x), bf2(w[i][0].y)}, b[2] = {bf2(w[i][1].x), bf2(w[i][1].y)};
+      float2 q = __fmul2_rn(a[0], a[0]);
+      q = __ffma2_rn(a[1], a[1], q);
+      q = __ffma2_rn(b[0], b[0], q);
+      q = __ffma2_rn(b[1], b[1], q);
+      float ss = q.x + q.y;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            A[e] = __fmul2_rn(gl[e], cs[e]);
-            B[e] = neg2(__fmul2_rn(gh[e], sn[e]));
-            C[e] = __fmul2_rn(gh[e], cs[e]);
-            D[e] = __fmul2_rn(gl[e], sn[e]);
-          }
-        }
-        const float2 a[2] = {bf2(w[i][0].x), bf2(w[i][0].y)}, b[2] = {bf2(w[i][1].x), bf2(w[i][1].y)};
-        float inv = 1.f;
-        if (is == 0 ? p.gamma_q != nullptr : p.gamma_k != nullptr) {
-          float2 q = __fmul2_rn(a[0], a[0]);
-          q = __ffma2_rn(a[1], a[1], q);
-          q = __ffma2_rn(b[0], b[0], q);
-          q = __ffma2_rn(b[1], b[1], q);
-          float ss = q.x + q.y;
+      for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = norm ? rsqrtf(ss * (1.f / 128.f) + p.eps) : 1.f;
+      const float2 n2 = make_float2(inv, inv);
+      float2 y[2], z[2];
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffu << (half * 16), ss, o);
-          inv = rsqrtf(ss * (1.f / 128.f) + p.eps);
-        }
-        const float2 n2 = make_float2(inv, inv);
-        float2 y[2], z[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          y[e] = __fmul2_rn(__ffma2_rn(a[e], A[e], __fmul2_rn(b[e], B[e])), n2);
-          z[e] = __fmul2_rn(__ffma2_rn(b[e], C[e], __fmul2_rn(a[e], D[e])), n2);
-        }
-        if (is == 1 && p.fp8) {
-          uint8_t* dst = (uint8_t*)p.cache_k + (cache0 + (size_t)(h - n_q) * p.unit_rows) * 128 + 4 * l;
-          *reinterpret_cast<uint32_t*>(dst) = e4m3x4(y[0].x * p.k_inv, y[0].y * p.k_inv, y[1].x * p.k_inv, y[1].y * p.k_inv);
-          *reinterpret_cast<uint32_t*>(dst + 64) = e4m3x4(z[0].x * p.k_inv, z[0].y * p.k_inv, z[1].x * p.k_inv, z[1].y * p.k_inv);
-          continue;
-        }
-        w[i][0] = make_uint2(pack2(y[0]), pack2(y[1]));
-        w[i][1] = make_uint2(pack2(z[0]), pack2(z[1]));
-      } else if (p.fp8) {
-        const float2 a0 = bf2(w[i][0].x), a1 = bf2(w[i][0].y), b0 = bf2(w[i][1].x), b1 = bf2(w[i][1].y);
-        uint8_t* dst = (uint8_t*)p.cache_v + (cache0 + (size_t)(h - n_q - p.n_kv) * p.unit_rows) * 128 + 4 * l;
-        *reinterpret_cast<uint32_t*>(dst) = e4m3x4(a0.x * p.v_inv, a0.y * p.v_inv, a1.x * p.v_inv, a1.y * p.v_inv);
-        *reinterpret_cast<uint32_t*>(dst + 64) = e4m3x4(b0.x * p.v_inv, b0.y * p.v_inv, b1.x * p.v_inv, b1.y * p.v_inv);
-        continue;
+      for (int e = 0; e < 2; ++e) {
+        y[e] = __fmul2_rn(__ffma2_rn(a[e], A[e], __fmul2_rn(b[e], B[e])), n2);
+        z[e] = __fmul2_rn(__ffma2_rn(b[e], C[e], __fmul2_rn(a[e], D[e])), n2);
       }
-      bf16* dst = is == 0 ? (bf16*)p.q_out + (size_t)r * p.n_h * 128 + h * 128
-                : (bf16*)(is == 1 ? p.cache_k : p.cache_v) +
-                      (cache0 + (size_t)(is == 1 ? h - n_q : h - n_q - p.n_kv) * p.unit_rows) * 128;
-      reinterpret_cast<uint2*>(dst)[l] = w[i][0];
-      reinterpret_cast<uint2*>(dst)[16 + l] = w[i][1];
+      if (h < h1) {
+        if (FP8 && kind > 0) {
+          const float f = kind == 1 ? p.k_inv : p.v_inv;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // V is stored as it is
+            y[e] = kind == 1 ? y[e] : a[e];
+            z[e] = kind == 1 ? z[e] : b[e];
+          }
+          *reinterpret_cast<uint32_t*>(dst) = e4m3x4(y[0].x * f, y[0].y * f, y[1].x * f, y[1].y * f);
+          *reinterpret_cast<uint32_t*>(dst + 64) = e4m3x4(z[0].x * f, z[0].y * f, z[1].x * f, z[1].y * f);
+        } else {
+          if (kind < 2) {
+            w[i][0] = make_uint2(pack2(y[0]), pack2(y[1]));
+            w[i][1] = make_uint2(pack2(z[0]), pack2(z[1]));
+          }
+          *reinterpret_cast<uint2*>(dst) = w[i][0];
+          *reinterpret_cast<uint2*>(dst + 128) = w[i][1];
+        }
+      }
+      dst += step;
+      h += 2;
     }
   }
 }
@@ -244,19 +262,24 @@ __global__ void __launch_bounds__(256) chunk_append_f32_kernel(const ChunkAppend
 
 cudaError_t chunk_append(int dtype, const ChunkAppendParams& p, cudaStream_t s) {
   const int heads = (p.q ? p.n_h : 0) + 2 * p.n_kv;
-  // bf16: a warp per 8 heads while the rows alone do not fill the GPU, else per 24 heads (512
-  // rows: 4.7 and 5.9 us, 9911 rows: 74 and 49.9 us)
-  const int groups = (heads + kHeadsPerGroup - 1) / kHeadsPerGroup;
-  const int span = (long long)p.rows * groups > 192ll * sm_count() ? 6 : 2;
-  const int units = dtype == DFLASH_F32 ? heads : (groups + span - 1) / span;
+  // bf16: a warp per 8 heads while the rows alone do not fill the GPU, else per 48, with four heads
+  // of each half warp in flight instead of two (512 rows: 4.2 and 5.6 us, 9911 rows: 60 and 46.2).
+  // Next to E4M3 rows two stay in flight (four: 31 us instead of 20.8).
+  const bool many = (long long)p.rows * heads > 768ll * sm_count();
+  const int span = many ? 48 : 8;
+  const int units = dtype == DFLASH_F32 ? heads : (heads + span - 1) / span;
   const int warps = dtype == DFLASH_F32 ? 8 : kWarps;
   const long long grid = ((long long)p.rows * units + warps - 1) / warps;
   if (grid > 0x0fffffffll) return cudaErrorInvalidValue;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_APPEND, s);
   if (dtype == DFLASH_F32)
     chunk_append_f32_kernel<<<(unsigned)grid, 256, 0, s>>>(p);
+  else if (p.fp8)
+    chunk_append_bf16_kernel<true, 2><<<(unsigned)grid, 32 * kWarps, 0, s>>>(p, span);
+  else if (many)
+    chunk_append_bf16_kernel<false, 4><<<(unsigned)grid, 32 * kWarps, 0, s>>>(p, span);
   else
-    chunk_append_bf16_kernel<<<(unsigned)grid, 32 * kWarps, 0, s>>>(p, span);
+    chunk_append_bf16_kernel<false, 2><<<(unsigned)grid, 32 * kWarps, 0, s>>>(p, span);
   return cudaGetLastError();
 }
 
