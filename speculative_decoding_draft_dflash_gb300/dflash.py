@@ -121,7 +121,7 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 
 def _stream(stream):
     if stream is None:
-        return c_void_p(_current_raw_stream(_current_device()))
+        return _current_raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return c_void_p(stream.cuda_stream)
     return c_void_p(int(stream))
@@ -463,9 +463,9 @@ def _rows(t, what, dtype, rows, width):
     """(address, elements between rows) of `rows` rows of `width` elements: a CUDA tensor
     [>= rows][width] (or [>= rows][heads][d_h]) whose rows are dense; the rows themselves may
     lie apart (a slice of a fused projection's output)."""
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{what}: expected a CUDA tensor")
-    dev = _current_device()
     shape, st = t.shape, t.stride()
     if len(shape) == 2:
         dense = shape[1] == width and st[1] == 1
@@ -473,11 +473,11 @@ def _rows(t, what, dtype, rows, width):
         dense = (len(shape) == 3 and shape[1] * shape[2] == width and st[2] == 1 and
                  (st[1] == shape[2] or shape[1] == 1))
     n = shape[0] if dense else -1
-    if n < rows or t.dtype is not dtype or t.get_device() != dev:
+    if n < rows or t.dtype is not dtype or dev != _current_device():
         if t.dtype != dtype:
             raise ValueError(f"{what}: element type {t.dtype}, the call needs {dtype}")
-        if t.get_device() != dev:
-            raise ValueError(f"{what}: on device {t.get_device()}, the current one is {dev}")
+        if dev != _current_device():
+            raise ValueError(f"{what}: on device {dev}, the current one is {_current_device()}")
         raise ValueError(f"{what}: shape {tuple(shape)}, strides {st}; the call needs {rows} rows "
                          f"of {width} dense elements")
     return t.data_ptr(), st[0] if n > 1 else width
@@ -488,7 +488,7 @@ def _array(t, what, dtype, numel):
     pay for every object they make."""
     if t is None or isinstance(t, int):
         return t
-    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
+    if t.dtype is dtype and t.get_device() >= 0 and t.numel() >= numel and t.is_contiguous():
         return t.data_ptr()
     return _ptr(t, what, dtype, numel)  # (says what is wrong)
 
