@@ -886,8 +886,6 @@ __global__ void attn_combine_kernel(AttnTcParams p, const int* merge_list, const
   }
 }
 
-}  // namespace
-
 int sm_count() {
   static std::mutex mu;
   static int count[128] = {};
@@ -902,8 +900,6 @@ int sm_count() {
   }
   return count[dev];
 }
-
-namespace {
 
 template <bool NARROW, bool FP8>
 cudaError_t launch_attn(const AttnTcParams& p, int grid, cudaStream_t s) {

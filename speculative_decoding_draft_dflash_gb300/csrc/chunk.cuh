@@ -26,6 +26,8 @@ struct ChunkMapParams {
   bool paged;
   bool alias;  // held_out is held, or taken_out is taken
 };
+int chunk_sms();  // SMs of the current device
+
 cudaError_t chunk_map(const ChunkMapParams& p, cudaStream_t s);
 
 struct ChunkAppendParams {

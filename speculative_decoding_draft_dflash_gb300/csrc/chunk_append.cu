@@ -265,7 +265,7 @@ cudaError_t chunk_append(int dtype, const ChunkAppendParams& p, cudaStream_t s) 
   // bf16: a warp per 8 heads while the rows alone do not fill the GPU, else per 48, with four heads
   // of each half warp in flight instead of two (512 rows: 4.2 and 5.6 us, 9911 rows: 60 and 46.2).
   // Next to E4M3 rows two stay in flight (four: 31 us instead of 20.8).
-  const bool many = (long long)p.rows * heads > 768ll * sm_count();
+  const bool many = (long long)p.rows * heads > 768ll * chunk_sms();
   const int span = many ? 48 : 8;
   const int units = dtype == DFLASH_F32 ? heads : (heads + span - 1) / span;
   const int warps = dtype == DFLASH_F32 ? 8 : kWarps;

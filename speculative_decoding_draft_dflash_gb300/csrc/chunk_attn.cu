@@ -6,7 +6,7 @@ namespace {
 
 // Stacked query rows of an item, at most.
 int item_rows(int dtype, int d_h) { return dtype == DFLASH_F32 ? chunk_attn_simt_item_rows(d_h) : 256; }
-int attn_ctas(int dtype, int d_h) { return dtype == DFLASH_F32 ? chunk_attn_simt_ctas(d_h) : sm_count(); }
+int attn_ctas(int dtype, int d_h) { return dtype == DFLASH_F32 ? chunk_attn_simt_ctas(d_h) : chunk_sms(); }
 
 // CTA c of the first grid axis merges the item that was cut at the end of attention CTA c's
 // share, if one was. Piece 0 is CTA c's partial 1, piece i > 0 is partial 0 of CTA c + i.
@@ -126,6 +126,17 @@ bool carve(int dtype, int d_h, ChunkAttnParams* p, Carver& cv) {
 }
 
 }  // namespace
+
+int chunk_sms() {
+  static int count[128] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 148;
+  int n = __atomic_load_n(&count[dev], __ATOMIC_RELAXED);
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  __atomic_store_n(&count[dev], n, __ATOMIC_RELAXED);
+  return n;
+}
 
 size_t chunk_attn_workspace(int dtype, int d_h) {
   Carver cv(nullptr, ~size_t(0));

@@ -322,7 +322,7 @@ cudaError_t launch(const ChunkAttnParams& p, cudaStream_t s) {
 }  // namespace
 
 int chunk_attn_simt_item_rows(int d_h) { return item_rows(d_h); }
-int chunk_attn_simt_ctas(int d_h) { return sm_count() * ctas_per_sm(d_h); }
+int chunk_attn_simt_ctas(int d_h) { return chunk_sms() * ctas_per_sm(d_h); }
 
 cudaError_t chunk_attn_simt(const ChunkAttnParams& p, cudaStream_t s) {
   if (p.d_h <= 64) return launch<64>(p, s);

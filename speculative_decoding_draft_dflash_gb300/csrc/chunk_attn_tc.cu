@@ -50,10 +50,7 @@
 
 namespace dflash {
 
-// 3-D view [rows][heads][128] of bf16 rows ld elements apart, box {64, box_heads, box_rows},
-// 128-byte swizzle (gemm_tc.cu); and the 2-D maps of the cache.
-bool encode_3d_bf16(CUtensorMap* m, const void* base, long long rows, int heads, long long ld,
-                    int box_heads, int box_rows);
+// The 2-D maps of the cache (gemm_tc.cu).
 bool encode_2d_bf16(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows);
 bool encode_2d_u8(CUtensorMap* m, const void* base, long long rows, int box_rows);
 
@@ -1108,8 +1105,33 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   cudaError_t e = limit.raise(chunk_attn_tc_kernel<FP8>, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_ATTN, s);
-  chunk_attn_tc_kernel<FP8><<<sm_count(), Plan<FP8>::THREADS, smem, s>>>(p);
+  chunk_attn_tc_kernel<FP8><<<chunk_sms(), Plan<FP8>::THREADS, smem, s>>>(p);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+namespace {
+
+// [rows][heads][128] view of bf16 rows ld elements apart, box {64 columns, box_heads heads,
+// box_rows rows}, 128-byte swizzle, zero fill.
+bool encode_3d_bf16(CUtensorMap* m, const void* base, long long rows, int heads, long long ld,
+                    int box_heads, int box_rows) {
+  static const decltype(&cuTensorMapEncodeTiled) fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return (decltype(&cuTensorMapEncodeTiled))(ok ? f : nullptr);
+  }();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {256, (cuuint64_t)ld * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace

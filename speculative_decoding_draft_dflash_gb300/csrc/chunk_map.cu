@@ -172,7 +172,7 @@ cudaError_t chunk_map(const ChunkMapParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_MAP, s);
   // a row per thread; a cluster is eight CTAs at most
-  const long long full = ((long long)p.rows + kThreads - 1) / kThreads, most = p.alias ? 8 : sm_count();
+  const long long full = ((long long)p.rows + kThreads - 1) / kThreads, most = p.alias ? 8 : chunk_sms();
   const int ctas = (int)(full < 1 ? 1 : full > most ? most : full);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);

@@ -57,9 +57,6 @@ struct Carver {
 // test lowered it with dflash_test_wait_limit; dflash_api.cu).
 unsigned long long wait_limit_ns();
 
-// SMs of the current device (attn_tc.cu)
-int sm_count();
-
 // Raises a kernel's dynamic shared-memory limit once per device.
 struct SmemLimit {
   unsigned char done[128] = {};

@@ -959,21 +959,6 @@ bool encode_2d_bf16(CUtensorMap* m, const void* base, long long rows, int cols, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [rows][heads][128] view of bf16 rows ld elements apart, box {64 columns, box_heads heads,
-// box_rows rows}, 128-byte swizzle, zero fill.
-bool encode_3d_bf16(CUtensorMap* m, const void* base, long long rows, int heads, long long ld,
-                    int box_heads, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)rows};
-  cuuint64_t strides[2] = {256, (cuuint64_t)ld * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // byte matrix [rows][128], box {128 bytes, box_rows rows}, 128-byte swizzle, zero fill.
 bool encode_2d_u8(CUtensorMap* m, const void* base, long long rows, int box_rows) {
   EncodeTiledFn fn = encode_fn();
