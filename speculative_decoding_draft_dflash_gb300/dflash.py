@@ -258,6 +258,7 @@ class KVCache:
             self.v = torch.zeros(shape, dtype=td, device=device)
             self.desc = dflash_kv_cache(self.k.data_ptr(), self.v.data_ptr(), self.lens.data_ptr(),
                                         n_layers, batch, capacity)
+        self.device = self.k.get_device()
         if self.fp8:
             # host array the descriptor points to; kept alive with the cache
             self._scales_c = (c_float * (2 * n_layers))(*self.scales.ravel().tolist())
@@ -298,6 +299,12 @@ class KVCache:
         self.v[layer, pages, :, r] = V.permute(1, 0, 2).to(self.v.dtype)
 
 
+def _one_device(device, **tensors):
+    for what, t in tensors.items():
+        if t.get_device() != device:
+            raise ValueError(f"{what}: on device {t.get_device()}, the others are on {device}")
+
+
 class ChunkPlan:
     """The rows of one step (dflash_chunk): cu_rows int32 [batch + 1] groups `rows` rows by
     sequence; kv_lens [batch], slots [rows] and positions [rows] are what dflash_chunk_map
@@ -320,6 +327,7 @@ class ChunkPlan:
                                  _ptr(self.slots, "slots", i32, self.rows),
                                  _ptr(self.positions, "positions", i32, self.rows),
                                  self.batch, self.rows)
+        _one_device(self.device, kv_lens=self.kv_lens, slots=self.slots, positions=self.positions)
         self.ref = ctypes.byref(self.desc)
 
 
@@ -330,7 +338,7 @@ class PagePool:
 
     def __init__(self, pages_held, free_pages, taken, pages_held_out=None, taken_out=None):
         i32, batch = torch.int32, int(pages_held.numel())
-        self.batch = batch
+        self.batch, self.device = batch, pages_held.get_device()
         self.pages_held, self.free_pages, self.taken = pages_held, free_pages, taken
         self.pages_held_out = pages_held if pages_held_out is None else pages_held_out
         self.taken_out = taken if taken_out is None else taken_out
@@ -339,6 +347,8 @@ class PagePool:
                                      _ptr(free_pages, "free_pages", i32), int(free_pages.numel()),
                                      _ptr(taken, "taken", i32, 1),
                                      _ptr(self.taken_out, "taken_out", i32, 1))
+        _one_device(self.device, pages_held_out=self.pages_held_out, free_pages=free_pages,
+                    taken=taken, taken_out=self.taken_out)
         self.ref = ctypes.byref(self.desc)
 
 
@@ -483,20 +493,23 @@ def _rows(t, what, dtype, rows, width):
     return t.data_ptr(), st[0] if n > 1 else width
 
 
-def _array(t, what, dtype, numel):
-    """_ptr of a tensor (or None) as a plain address: the calls that run once per layer and step
-    pay for every object they make."""
+def _array(t, what, dtype, numel, device):
+    """_ptr of a tensor (or None) as a plain address, on the device of the call's plan: the calls
+    that run once per layer and step pay for every object they make."""
     if t is None or isinstance(t, int):
         return t
-    if t.dtype is dtype and t.get_device() >= 0 and t.numel() >= numel and t.is_contiguous():
+    if t.dtype is dtype and t.get_device() == device and t.numel() >= numel and t.is_contiguous():
         return t.data_ptr()
-    return _ptr(t, what, dtype, numel)  # (says what is wrong)
+    _ptr(t, what, dtype, numel)  # (says what is wrong)
+    raise ValueError(f"{what}: on device {t.get_device()}, the plan is on {device}")
 
 
-def _chunk(plan, cache):
-    """C descriptor of a plan, checked against the cache's batch and the current device."""
-    if plan.batch != cache.batch:
-        raise ValueError(f"chunk plan: {plan.batch} sequences, the cache has {cache.batch}")
+def _chunk(plan, desc, cache):
+    """C descriptor of a plan, checked against the cache and the current device."""
+    if plan.batch != desc.batch:
+        raise ValueError(f"chunk plan: {plan.batch} sequences, the cache has {desc.batch}")
+    if cache is not desc and cache.device != plan.device:
+        raise ValueError(f"cache: on device {cache.device}, the plan is on {plan.device}")
     if plan.device != _current_device():
         raise ValueError(f"chunk plan: on device {plan.device}, the current one is {_current_device()}")
     return plan.ref
@@ -508,8 +521,10 @@ def dflash_chunk_map(cache, layer, plan, pool=None, stream=None):
     if pool is not None:
         if pool.batch < desc.batch:
             raise ValueError(f"page pool: {pool.batch} sequences, the cache has {desc.batch}")
+        if pool.device != plan.device:
+            raise ValueError(f"page pool: on device {pool.device}, the plan is on {plan.device}")
         pool.desc.block_table = desc.block_table
-    _check(_lib.dflash_chunk_map(ctypes.byref(desc), int(layer), _chunk(plan, desc),
+    _check(_lib.dflash_chunk_map(ctypes.byref(desc), int(layer), _chunk(plan, desc, cache),
                                  None if pool is None else pool.ref, _stream(stream)),
            "dflash_chunk_map")
 
@@ -517,18 +532,18 @@ def dflash_chunk_map(cache, layer, plan, pool=None, stream=None):
 def dflash_chunk_append(dims, cache, layer, plan, q, k, v, gamma_q, gamma_k, rope_table, table_len,
                         q_out, stream=None):
     """Norm, RoPE and store of a step's rows in one layer; q and q_out may be None."""
-    desc, et, d_h, rows = _desc(dims, cache), _et(dims), dims.d_h, plan.rows
+    desc, et, d_h, rows, dev = _desc(dims, cache), _et(dims), dims.d_h, plan.rows, plan.device
     qw, kw, table_len = dims.n_h * d_h, dims.n_kv * d_h, int(table_len)
     qp, ldq = (None, 0) if q is None else _rows(q, "q", et, rows, qw)
     kp, ldk = _rows(k, "k", et, rows, kw)
     vp, ldv = _rows(v, "v", et, rows, kw)
     _check(_lib.dflash_chunk_append(ctypes.byref(dims), ctypes.byref(desc), int(layer),
-                                    _chunk(plan, desc), qp, ldq, kp, ldk, vp, ldv,
-                                    _array(gamma_q, "gamma_q", et, d_h),
-                                    _array(gamma_k, "gamma_k", et, d_h),
+                                    _chunk(plan, desc, cache), qp, ldq, kp, ldk, vp, ldv,
+                                    _array(gamma_q, "gamma_q", et, d_h, dev),
+                                    _array(gamma_k, "gamma_k", et, d_h, dev),
                                     _array(rope_table, "rope_table", torch.float32,
-                                           max(0, table_len) * d_h), table_len,
-                                    _array(q_out, "q_out", et, rows * qw), _stream(stream)),
+                                           max(0, table_len) * d_h, dev), table_len,
+                                    _array(q_out, "q_out", et, rows * qw, dev), _stream(stream)),
            "dflash_chunk_append")
 
 
@@ -542,9 +557,11 @@ def dflash_chunk_attn(dims, cache, layer, plan, q, sliding_window, scaling, out,
     desc, et = _desc(dims, cache), _et(dims)
     qw = dims.n_h * dims.d_h
     qp, ldq = _rows(q, "q", et, plan.rows, qw)
+    if isinstance(workspace, torch.Tensor) and workspace.get_device() != plan.device:
+        raise ValueError(f"workspace: on device {workspace.get_device()}, the plan is on {plan.device}")
     _check(_lib.dflash_chunk_attn(ctypes.byref(dims), ctypes.byref(desc), int(layer),
-                                  _chunk(plan, desc), qp, ldq, int(sliding_window), float(scaling),
-                                  _array(out, "out", et, plan.rows * qw), *_ws(workspace),
+                                  _chunk(plan, desc, cache), qp, ldq, int(sliding_window), float(scaling),
+                                  _array(out, "out", et, plan.rows * qw, plan.device), *_ws(workspace),
                                   _stream(stream)), "dflash_chunk_attn")
 
 

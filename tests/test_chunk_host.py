@@ -140,3 +140,22 @@ def test_binding_refuses_host_and_mismatched_tensors(D):
         D.PagePool(torch.zeros(4), torch.zeros(4), torch.zeros(1))
     with pytest.raises(ValueError):
         D._rows(torch.zeros(4, 8, dtype=torch.bfloat16), "q", torch.bfloat16, 4, 8)
+
+
+def test_binding_refuses_other_devices(D):
+    """What belongs to a step lies on the plan's device. (A plan of device 3 stands in, and what
+    it meets lies in host memory, which is no device.)"""
+    import types
+
+    import torch
+    plan = types.SimpleNamespace(batch=2, rows=4, device=3, ref=None)
+    cache = D.KVCache(1, 2, 2, 128, 64, "f32", device="cpu")
+    with pytest.raises(ValueError, match="cache"):
+        D.dflash_chunk_map(cache, 0, plan)
+    pool = types.SimpleNamespace(batch=2, device=-1)
+    with pytest.raises(ValueError, match="page pool"):
+        D.dflash_chunk_map(cache, 0, plan, pool)
+    for t in (torch.zeros(4), torch.zeros(8, dtype=torch.int32)[::2]):
+        with pytest.raises(ValueError):
+            D._array(t, "out", torch.float32, 4, 3)
+    assert D._array(None, "out", torch.float32, 4, 3) is None and D._array(64, "out", torch.float32, 4, 3) == 64
