@@ -458,7 +458,8 @@ dflash_status dflash_chunk_append(const dflash_dims* dims, const dflash_kv_cache
  * [0, capacity] sets DFLASH_DEV_CAPACITY and the rows are zero; rows that are not a valid
  * range set DFLASH_DEV_ROWS and are skipped; a page id outside the pool sets
  * DFLASH_DEV_PAGE and reads as zeros. bf16: weights are rounded to bf16 for the product with
- * V (E4M3: to f16), sums and maxima are fp32; the same inputs give the same bits.
+ * V; E4M3: to f16 with 7 bits of headroom, which is relative (2^-11) down to 2^-21 of the row's
+ * largest weight and 2^-32 of it below. Sums and maxima are fp32; the same inputs give the same bits.
  * Unsupported: more than 8192 sequences, a capacity above 2^28, rows * G above 2^30, a layer of
  * more than 2^31 - 1 key rows (slots * n_kv), bf16 with G above 128. The status word may also
  * get DFLASH_DEV_TIMEOUT, as from every call with pipeline waits.

@@ -17,7 +17,11 @@
 // A and B, 11 (bf16) check of the V tiles that the mask cuts, (E4M3) Q to codes and V to f16.
 // Tensor memory: S_A, S_B, O_A, O_B of 128 columns each; P (16 bits) overwrites the first half
 // of its S and is the A operand of the PV product from there. P is rounded to bf16 next to a
-// bf16 V, as V was; next to E4M3 values to f16, which holds them exactly.
+// bf16 V, as V was; next to E4M3 values to f16, which holds them exactly. f16 has few exponents:
+// weights and sums there carry a factor 2^7 (p stays below 2^15 of f16's 65504), which every
+// quotient divides out again. So a weight keeps 11 bits down to 2^-21 of the row's reference, and
+// one below 2^-32 is lost from the product (without the factor 2^-14 and 2^-25: 8191 keys of weight
+// 2^-25.5 behind one of weight 1 and value 0 lost half of their output).
 //
 // What bounds it. Many rows: the MMAs (1024 cycles a key tile and row tile with both products)
 // and the exponentials (128 x 128 at 16 a cycle and SM: 1024 too), which A and B overlap: 2800
@@ -60,6 +64,8 @@ constexpr int TK = 128;                   // keys of a tile (2^7)
 constexpr uint32_t TILE = 128 * 128 * 2;  // a 16-bit tile
 constexpr uint32_t HALF = TILE / 2;       // its 64-column box
 constexpr int kRing = 4;                  // items in flight between the roles
+
+constexpr float kShiftF16 = 7.f;          // log2 of the factor of weights rounded to f16
 
 constexpr uint32_t TM_S = 0, TM_O = 256;  // tensor-memory columns of S_A; O_A (B: + 128)
 
@@ -617,7 +623,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
               ptx::tmem_st_32x32b_x32(tO + X * 128 + 32 * c, v);
             }
           }
-          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          const float mu = (m_ref == -INFINITY ? 0.f : m_ref) - (FP8 ? kShiftF16 : 0.f);
           const float2 sl2v = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
