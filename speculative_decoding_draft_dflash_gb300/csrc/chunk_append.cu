@@ -70,7 +70,8 @@ __device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y
 // by HBM and issue slots: 9911 rows of 32 + 8 + 8 heads 46.2 us (5.3 TB/s; with addresses and
 // branches per head 49.9), 512 rows 4.2 us, five prompts on E4M3 20.8 us. More warps instead of
 // long units, and fewer registers with more CTAs, were slower (56 to 79 us).
-template <bool FP8, int U>
+// ROPE false: the pairs are not mixed at all (an infinity times a sine of 0 would be a NaN).
+template <bool FP8, int U, bool ROPE>
 __global__ void __launch_bounds__(32 * kWarps, U == 2 ? 7 : 5) chunk_append_bf16_kernel(const ChunkAppendParams p, int span) {
   publish_lens(p);
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(32 * kWarps, U == 2 ? 7 : 5) chunk_append_bf16
   if (!row_live(p, r, &slot, &pos)) return;
   // (cos, sin) of this lane's four pairs
   float2 cs[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  if (p.rope) {
+  if (ROPE) {
     const float4* t = reinterpret_cast<const float4*>(p.rope + (size_t)pos * 64 + l * 4);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -176,8 +177,8 @@ __global__ void __launch_bounds__(32 * kWarps, U == 2 ? 7 : 5) chunk_append_bf16
       float2 y[2], z[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        y[e] = __fmul2_rn(__ffma2_rn(a[e], A[e], __fmul2_rn(b[e], B[e])), n2);
-        z[e] = __fmul2_rn(__ffma2_rn(b[e], C[e], __fmul2_rn(a[e], D[e])), n2);
+        y[e] = __fmul2_rn(ROPE ? __ffma2_rn(a[e], A[e], __fmul2_rn(b[e], B[e])) : __fmul2_rn(a[e], A[e]), n2);
+        z[e] = __fmul2_rn(ROPE ? __ffma2_rn(b[e], C[e], __fmul2_rn(a[e], D[e])) : __fmul2_rn(b[e], C[e]), n2);
       }
       if (h < h1) {
         if (FP8 && kind > 0) {
@@ -258,6 +259,17 @@ __global__ void __launch_bounds__(256) chunk_append_f32_kernel(const ChunkAppend
   }
 }
 
+template <bool ROPE>
+void launch_bf16(const ChunkAppendParams& p, unsigned grid, int span, bool many, cudaStream_t s) {
+  constexpr int threads = 32 * kWarps;
+  if (p.fp8)
+    chunk_append_bf16_kernel<true, 2, ROPE><<<grid, threads, 0, s>>>(p, span);
+  else if (many)
+    chunk_append_bf16_kernel<false, 4, ROPE><<<grid, threads, 0, s>>>(p, span);
+  else
+    chunk_append_bf16_kernel<false, 2, ROPE><<<grid, threads, 0, s>>>(p, span);
+}
+
 }  // namespace
 
 cudaError_t chunk_append(int dtype, const ChunkAppendParams& p, cudaStream_t s) {
@@ -274,12 +286,10 @@ cudaError_t chunk_append(int dtype, const ChunkAppendParams& p, cudaStream_t s) 
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_APPEND, s);
   if (dtype == DFLASH_F32)
     chunk_append_f32_kernel<<<(unsigned)grid, 256, 0, s>>>(p);
-  else if (p.fp8)
-    chunk_append_bf16_kernel<true, 2><<<(unsigned)grid, 32 * kWarps, 0, s>>>(p, span);
-  else if (many)
-    chunk_append_bf16_kernel<false, 4><<<(unsigned)grid, 32 * kWarps, 0, s>>>(p, span);
+  else if (p.rope)
+    launch_bf16<true>(p, (unsigned)grid, span, many, s);
   else
-    chunk_append_bf16_kernel<false, 2><<<(unsigned)grid, 32 * kWarps, 0, s>>>(p, span);
+    launch_bf16<false>(p, (unsigned)grid, span, many, s);
   return cudaGetLastError();
 }
 

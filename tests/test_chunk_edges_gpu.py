@@ -48,3 +48,37 @@ def test_attn_fp8_long_tail_behind_a_strong_key(D, B, heads, ctx, n, bits):
         # a tail that was lost would be off by ref: the bound is at most 4300 / 4001 / 2 1.25 / 1.12 of it
         assert (ref > 0).all() and (tol < 0.75 * ref).all()
         assert (np.abs(on[lo:hi] - ref) <= tol).all(), b
+
+
+# ---------------------------------------------------------------------------
+# append
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [[9, 60], [900, 700]])
+@pytest.mark.parametrize("norm", [False, True])
+def test_append_without_rotation_keeps_infinities_apart(D, kv, rows, norm):
+    """No rotation: an element that is not finite does not reach its partner d_h / 2 away. Without
+    a norm either the rows go through as they are."""
+    s = Step(D, kv, (64, 8, 128), [5, 100], rows, paged=kv != "f32", seed=75)
+    s.map()
+    for x in (s.q, s.k):
+        x[3, 7], x[5, 64 + 9], x[6, 128 + 1] = float("inf"), -float("inf"), float("nan")
+        x[8] *= -0.0
+    q_out = torch.empty((s.M, s.n_h * 128), dtype=s.q.dtype, device=DEV)
+    gq, gk = (s.gq, s.gk) if norm else (None, None)
+    D.dflash_chunk_append(s.dims, s.cache, 0, s.plan, s.q, s.k, s.v, gq, gk, None, 0, q_out)
+    assert D.dflash_status_get() == 0
+    k_out = torch.cat([s.cache.rows("k", 0, b, s.ctx[b], s.ctx[b] + rows[b]) for b in range(2)], 1)
+    for x, got, gamma, n in ((s.q, q_out.view(s.M, -1, 128), gq, s.n_h), (s.k, k_out.permute(1, 0, 2), gk, s.n_kv)):
+        x = x.reshape(s.M, n, 128)
+        if not norm:
+            same = (got == x) | (torch.isnan(got) & torch.isnan(x))
+            assert same.all() and torch.equal(torch.signbit(got[8]), torch.signbit(x[8]))
+            continue
+        with np.errstate(invalid="ignore"):
+            y, mag = R.norm_rope(np64(x), np64(gamma), 0, rope=False)
+        g = np64(got)
+        assert (np.isnan(g) == np.isnan(y)).all()
+        fin = np.isfinite(y)
+        assert (np.abs(g - y)[fin] <= R.append_bound(y, mag, 128, "f32" if kv == "f32" else "bf16")[fin]).all()
