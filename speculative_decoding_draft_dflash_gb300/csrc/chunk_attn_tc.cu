@@ -566,7 +566,9 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
         alive = waits(sh.s[X], ns++);
         if (!alive) break;
         {
-          if (FP8 && done == 0) sl2 = ldexpf(p.sl2, sh.qexp[g.dual ? X : 0][r]);
+          // never 0 (or infinity): masked scores of -infinity have to stay that when scaled, and
+          // scores that small do not tell the keys apart
+          if (FP8 && done == 0) sl2 = fminf(fmaxf(ldexpf(p.sl2, sh.qexp[g.dual ? X : 0][r]), FLT_MIN), FLT_MAX);
           ptx::tc_fence_after();
           uint32_t raw[4][32];
 #pragma unroll

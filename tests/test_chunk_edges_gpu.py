@@ -50,6 +50,24 @@ def test_attn_fp8_long_tail_behind_a_strong_key(D, B, heads, ctx, n, bits):
         assert (np.abs(on[lo:hi] - ref) <= tol).all(), b
 
 
+@pytest.mark.parametrize("n", [1, 150])
+@pytest.mark.parametrize("k_scale,scaling", [(1e-12, 0.125), (0.5, 1e-30)])
+def test_attn_fp8_scores_below_the_smallest_float(D, n, k_scale, scaling):
+    """Scores that vanish (a query of zeros next to a small scale): every visible key counts the
+    same, and masked keys still nothing."""
+    s = Step(D, "fp8", (4, 2, 128), [200, 3], [n, n], seed=73)
+    s.map()
+    s.append(torch.empty((s.M, 512), dtype=torch.bfloat16, device=DEV))
+    s.cache._scales_c[0] = s.cache.scales[0, 0] = k_scale
+    q = torch.randn((s.M, 512), generator=torch.Generator().manual_seed(1)).to(DEV, torch.bfloat16)
+    q[:, :256] = 0
+    q[:, 256:384] *= 2.0 ** -100
+    out = torch.empty_like(q)
+    s.attn(q, out, 0, scaling)
+    assert D.dflash_status_get() == 0
+    s.check_attn(q, out, 0, scaling)
+
+
 # ---------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------
