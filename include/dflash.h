@@ -445,7 +445,8 @@ dflash_status dflash_chunk_append(const dflash_dims* dims, const dflash_kv_cache
  * rows of sequence b is at p = kv_lens[b] - n + i and sees the cached rows j <= p, with a
  * sliding window W > 0 those with p - j < W:
  *   out = softmax(q K^T * scaling) V, query head h reading KV head h / G (G = n_h / n_kv)
- * A row that sees no key (a refused sequence; p < 0) is zero. What the cache holds at rows a
+ * A row that sees no key (a refused sequence; p < 0) is zero; one that sees keys, all of them at a
+ * score of minus infinity, is NaN. What the cache holds at rows a
  * query does not see never reaches it, NaN and infinity included. Rows of padding are left as they were.
  *   q      device rows of n_h * d_h elements, ld_q elements apart (at least the row; a
  *          multiple of 8 for bf16); 16-byte aligned

@@ -11,7 +11,9 @@ int attn_ctas(int dtype, int d_h) { return dtype == DFLASH_F32 ? chunk_attn_simt
 // CTA c of the first grid axis merges the item that was cut at the end of attention CTA c's
 // share, if one was. Piece 0 is CTA c's partial 1, piece i > 0 is partial 0 of CTA c + i.
 // out = sum_i w_i o_i / sum_i w_i l_i, w_i = exp(max_i - max). (f32 keeps its maxima in the
-// natural domain, bf16 in log2 units.) Bound by L2: a partial of 256 rows is 128 KB.
+// natural domain, bf16 in log2 units.) A row that sees keys, all of them at a score of minus
+// infinity, has l_i = 0 and the lowest finite maximum: its sum is 0 like that of a row that sees
+// no key, but the result is NaN. Bound by L2: a partial of 256 rows is 128 KB.
 __device__ __forceinline__ float piece_weight(float mx, float M, bool natural) {
   return mx == -INFINITY ? 0.f : natural ? expf(mx - M) : exp2f(mx - M);
 }
@@ -55,7 +57,7 @@ __global__ void __launch_bounds__(256) chunk_merge_f32_kernel(const ChunkAttnPar
         }
       }
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float inv = L == 0.f ? (M == -INFINITY ? 0.f : NAN) : 1.f / L;
     const int token = (r0 + r) / p.G, g = r0 + r - token * p.G;
     float* dst = (float*)p.out + ((size_t)(row0 + token) * p.n_h + m.y * p.G + g) * p.d_h;
 #pragma unroll
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(256) chunk_merge_bf16_kernel(const ChunkAttnPa
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = acc[e] * keep + (w == 0.f ? 0.f : w * v[e]);  // (0: keys unseen)
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float inv = L == 0.f ? (M == -INFINITY ? 0.f : NAN) : 1.f / L;
     const int token = (r0 + r) / p.G, g = r0 + r - token * p.G;
     bf16* dst = (bf16*)p.out + ((size_t)(row0 + token) * p.n_h + m.y * p.G + g) * 128 + c8 * 8;
     uint4 w;

@@ -22,6 +22,8 @@
 // busy for half of the time. The same with 64-row items, one CTA per SM and single multiply-adds:
 // 189 us; pairs alone 176, 128-row items 168, two CTAs 148, idle warps skipped 144, Q read a row
 // per thread 133, no mask where every row sees every key 131.
+#include <float.h>
+
 #include "chunk.cuh"
 
 namespace dflash {
@@ -262,13 +264,15 @@ __device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Pie
     const size_t part = (size_t)(2 * blockIdx.x + (w.slot > 0)) * item_rows(DP) + r;
     const int token = (r0 + r) / p.G, g = r0 + r - token * p.G;
     float* dst = w.slot < 0 ? (float*)p.out + ((size_t)(w.row0 + token) * p.n_h + w.kvh * p.G + g) * d : p.part + part * d;
-    const float inv = w.slot >= 0 ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+    // no weight at all: 0 where no key is seen, else (every score minus infinity) NaN
+    const float inv = w.slot >= 0 ? 1.f : sum != 0.f ? 1.f / sum : w.kv - w.n + token >= 0 ? NAN : 0.f;
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e) {
       const int c = tx * 4 + 64 * (e >> 1) + 2 * (e & 1);  // (d is even)
       if (c < d) *reinterpret_cast<float2*>(dst + c) = make_float2(o[i][e].x * inv, o[i][e].y * inv);
     }
-    if (w.slot >= 0 && tx == 0) p.part_ml[part] = make_float2(m[i], sum);
+    if (w.slot >= 0 && tx == 0)
+      p.part_ml[part] = make_float2(sum == 0.f && w.kv - w.n + token >= 0 ? -FLT_MAX : m[i], sum);
   }
 }
 

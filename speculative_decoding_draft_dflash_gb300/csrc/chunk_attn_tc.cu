@@ -703,9 +703,11 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] += __uint_as_float(u[e]) * fb;
             }
-            if (!(l > 0.f)) {  // no key, or a score that is not a number
+            if (!(l > 0.f)) {  // no key (or none in this piece), or a score that is not a number
+              // no weight at all on keys that are seen: every score is minus infinity
+              const float none = l == 0.f && it.w.slot < 0 && pos >= 0 ? NAN : l;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = l;
+              for (int e = 0; e < 16; ++e) o[e] = none;
             }
             if (bad && valid) {
               float fix[16];
@@ -737,7 +739,8 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
               }
             }
           }
-          if (it.w.slot >= 0 && valid && (g.dual || X == 0)) p.part_ml[pslot + irow] = make_float2(m_ref, l);
+          if (it.w.slot >= 0 && valid && (g.dual || X == 0))
+            p.part_ml[pslot + irow] = make_float2(l == 0.f && pos >= 0 ? -FLT_MAX : m_ref, l);
         }
         ptx::tc_fence_before();
         __syncwarp();

@@ -68,6 +68,61 @@ def test_attn_fp8_scores_below_the_smallest_float(D, n, k_scale, scaling):
     s.check_attn(q, out, 0, scaling)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("window", [0, 40])
+def test_attn_rows_whose_scores_all_overflow(D, kv, window):
+    """Rows that see keys, all at a score of minus infinity, have no softmax: NaN, not the zeros
+    of a row that sees none. (Next to an E4M3 cache a query of infinities is NaN by itself.)"""
+    s = Step(D, kv, (4, 2, 128), [700, 0, 9], [3, 150, 4], paged=kv != "f32", seed=74)
+    s.map()
+    q = torch.ones((s.M, 512), dtype=s.q.dtype, device=DEV)
+    s.append(torch.empty_like(q))
+    # every key has a positive first element (the sign of V does not matter)
+    for b in range(s.B):
+        K, V = (s.cache.rows(w, 0, b, 0, s.ctx[b] + s.rows[b]) for w in "kv")
+        K, V = K.float().clone(), V.float().clone()
+        K[:, :, 0] = 1.0
+        if kv == "fp8":
+            K, V = (x.to(torch.float8_e4m3fn).view(torch.uint8) for x in (K, V))
+        s.cache.set_rows(0, b, K.to(s.cache.k.dtype), V.to(s.cache.v.dtype))
+    plain = torch.empty_like(q)
+    s.attn(q, plain, window)
+    hurt = [0, 2, 3, 60, 152, 154]
+    q[hurt, 0] = -float("inf")                       # head 0 only
+    s.plan.kv_lens[2] = 2                            # rows 153 and 154 see no key
+    out = torch.empty_like(q)
+    s.attn(q, out, window)
+    seen = [r for r in hurt if r < 153]
+    assert torch.isnan(out[seen, :128]).all()
+    assert (out[153:155] == 0).all()
+    rest = [r for r in range(153) if r not in hurt]
+    assert torch.equal(out[rest], plain[rest]) and torch.equal(out[seen, 128:], plain[seen, 128:])
+    assert D.dflash_status_get() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+@pytest.mark.parametrize("ctx,n", [(9000, 3), (700, 150)])
+def test_attn_some_keys_at_minus_infinity(D, kv, ctx, n):
+    """Visible keys at a score of minus infinity weigh nothing, also where they are all that a piece
+    of the key axis has."""
+    s = Step(D, kv, (4, 2, 128), [ctx], [n], paged=kv != "f32", seed=78)
+    s.map()
+    s.append(torch.empty((s.M, 512), dtype=s.q.dtype, device=DEV))
+    K, V = (s.cache.rows(w, 0, 0, 0, ctx + n).clone() for w in "kv")
+    K[:, :300, 0] = float("inf")
+    s.cache.set_rows(0, 0, K, V)
+    q = s.q.reshape(s.M, 4, 128).clone()
+    q[:, :, 0] = -1.0
+    q = q.reshape(s.M, 512)
+    out = torch.empty_like(q)
+    s.attn(q, out)
+    assert D.dflash_status_get() == 0
+    k, v = s.cached(0, ctx + n)
+    ref, mag, big, keys = R.attention(np64(q).reshape(s.M, 4, 128), k[300:], v[300:], ctx + n - 300, n, 2, 0, 128 ** -0.5)
+    tol = R.attention_bound(ref, mag, big, keys, 128, kv)
+    assert (np.abs(np64(out).reshape(s.M, 4, 128) - ref) <= tol).all()
+
+
 # ---------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------
