@@ -349,7 +349,6 @@ class PagePool:
                                      _ptr(self.taken_out, "taken_out", i32, 1))
         _one_device(self.device, pages_held_out=self.pages_held_out, free_pages=free_pages,
                     taken=taken, taken_out=self.taken_out)
-        self.ref = ctypes.byref(self.desc)
 
 
 # ---------------------------------------------------------------------------
@@ -518,14 +517,17 @@ def _chunk(plan, desc, cache):
 def dflash_chunk_map(cache, layer, plan, pool=None, stream=None):
     """Pages, slots, positions and lengths of a step, from the lengths of `layer`."""
     desc = cache.desc if isinstance(cache, KVCache) else cache
+    own = None
     if pool is not None:
         if pool.batch < desc.batch:
             raise ValueError(f"page pool: {pool.batch} sequences, the cache has {desc.batch}")
         if pool.device != plan.device:
             raise ValueError(f"page pool: on device {pool.device}, the plan is on {plan.device}")
-        pool.desc.block_table = desc.block_table
+        # a descriptor of this call's own: another thread may use the pool with another cache
+        own = dflash_page_pool.from_buffer_copy(pool.desc)
+        own.block_table = desc.block_table
     _check(_lib.dflash_chunk_map(ctypes.byref(desc), int(layer), _chunk(plan, desc, cache),
-                                 None if pool is None else pool.ref, _stream(stream)),
+                                 None if own is None else ctypes.byref(own), _stream(stream)),
            "dflash_chunk_map")
 
 
