@@ -260,11 +260,11 @@ __global__ void __launch_bounds__(256) chunk_append_f32_kernel(const ChunkAppend
 }
 
 template <bool ROPE>
-void launch_bf16(const ChunkAppendParams& p, unsigned grid, int span, bool many, cudaStream_t s) {
+void launch_bf16(const ChunkAppendParams& p, unsigned grid, int span, bool four, cudaStream_t s) {
   constexpr int threads = 32 * kWarps;
   if (p.fp8)
     chunk_append_bf16_kernel<true, 2, ROPE><<<grid, threads, 0, s>>>(p, span);
-  else if (many)
+  else if (four)
     chunk_append_bf16_kernel<false, 4, ROPE><<<grid, threads, 0, s>>>(p, span);
   else
     chunk_append_bf16_kernel<false, 2, ROPE><<<grid, threads, 0, s>>>(p, span);
@@ -274,11 +274,22 @@ void launch_bf16(const ChunkAppendParams& p, unsigned grid, int span, bool many,
 
 cudaError_t chunk_append(int dtype, const ChunkAppendParams& p, cudaStream_t s) {
   const int heads = (p.q ? p.n_h : 0) + 2 * p.n_kv;
-  // bf16: a warp per 8 heads while the rows alone do not fill the GPU, else per 48, with four heads
-  // of each half warp in flight instead of two (512 rows: 4.2 and 5.6 us, 9911 rows: 60 and 46.2).
-  // Next to E4M3 rows two stay in flight (four: 31 us instead of 20.8).
-  const bool many = (long long)p.rows * heads > 768ll * chunk_sms();
-  const int span = many ? 48 : 8;
+  // bf16: a warp per 8 heads while the step is small. Once units of 48 heads keep 16 warps of an SM
+  // busy (of the 20 that fit), a row is cut into as few units of at most 48 as it takes, even in
+  // number of heads and alike in size. us with 8 heads and with long units, by heads of a row:
+  //   rows x heads     48 (one unit)   72 (two of 36)   80 (two of 40)   130 (three of 44)
+  //   25 000           4.5    8.4      4.5    7.4       4.5    7.7       4.5    7.8
+  //   60 000           8.4    9.6      8.7    8.7       8.4    8.8       8.3    9.1
+  //   120 000         17.0   14.0     17.3   17.6      17.3   13.8      16.8   13.9
+  //   500 000         60.5   47.2     60.9   47.5      60.3   47.6      61.1   46.6
+  // Units of 48 and a short rest instead of equal ones: 72 heads 48.5, 80 heads 48.9 us.
+  // Long units have four heads of each half warp in flight instead of two (500 000: 24 heads 50.2
+  // and 51.7 us, 48 heads 47.2 and 52.1), short ones do not gain by it (18 heads 60.3 and 58.0, 7
+  // heads 97 and 78). Next to E4M3 rows two stay in flight (four: 31 us instead of 20.8).
+  const bool many = (long long)p.rows * heads > 16ll * 48 * chunk_sms();
+  const int per_row = (heads + 47) / 48;
+  const int span = many ? ((heads + per_row - 1) / per_row + 1) & ~1 : 8;
+  const bool four = span >= 24;
   const int units = dtype == DFLASH_F32 ? heads : (heads + span - 1) / span;
   const int warps = dtype == DFLASH_F32 ? 8 : kWarps;
   const long long grid = ((long long)p.rows * units + warps - 1) / warps;
@@ -287,9 +298,9 @@ cudaError_t chunk_append(int dtype, const ChunkAppendParams& p, cudaStream_t s) 
   if (dtype == DFLASH_F32)
     chunk_append_f32_kernel<<<(unsigned)grid, 256, 0, s>>>(p);
   else if (p.rope)
-    launch_bf16<true>(p, (unsigned)grid, span, many, s);
+    launch_bf16<true>(p, (unsigned)grid, span, four, s);
   else
-    launch_bf16<false>(p, (unsigned)grid, span, many, s);
+    launch_bf16<false>(p, (unsigned)grid, span, four, s);
   return cudaGetLastError();
 }
 

@@ -155,3 +155,61 @@ def test_append_without_rotation_keeps_infinities_apart(D, kv, rows, norm):
         assert (np.isnan(g) == np.isnan(y)).all()
         fin = np.isfinite(y)
         assert (np.abs(g - y)[fin] <= R.append_bound(y, mag, 128, "f32" if kv == "f32" else "bf16")[fin]).all()
+
+
+LARGE = [("bf16", (32, 8), True, True), ("bf16", (5, 1), False, False), ("bf16", (14, 2), True, True),
+         ("bf16", (64, 4), True, False), ("bf16", (128, 1), False, True), ("fp8", (32, 8), True, True),
+         ("fp8", (5, 1), True, False), ("fp8", (64, 4), False, True), ("fp8", (128, 1), True, True)]
+
+
+@pytest.mark.parametrize("kv,heads,paged,fused", LARGE)
+@pytest.mark.parametrize("mode", ["apart", "in place", "no queries"])
+def test_append_of_a_large_step(D, kv, heads, paged, fused, mode):
+    """Steps of more than 768 heads per SM (150,000 of up to 160 SMs): a warp takes several heads of
+    a row, across the ends of Q, K and V, with an odd number of heads and short last units too."""
+    n_h, n_kv = heads
+    if mode == "no queries":
+        n_h = n_kv
+    total = (0 if mode == "no queries" else n_h) + 2 * n_kv
+    M = -(-150_000 // total)
+    rows = [M // 2 - 3, 1, 0, M - M // 2 + 2]
+    if mode == "in place":
+        fused = False
+    s = Step(D, kv, (n_h, n_kv, 128), [0, 130, 9, 77], rows, paged, layers=2, layer=1, pad=5, seed=76, fused=fused)
+    s.map()
+    q, q_out = s.q, torch.full((s.M, n_h * 128), 7.0, dtype=s.q.dtype, device=DEV)
+    if mode == "no queries":
+        q = q_out = None
+    elif mode == "in place":
+        q = q_out = s.q.clone()
+    D.dflash_chunk_append(s.dims, s.cache, 1, s.plan, q, s.k, s.v, s.gq, s.gk, s.table, s.cap, q_out)
+    assert D.dflash_status_get() == 0
+    assert s.cache.lens.tolist() == [s.ctx, [c + n for c, n in zip(s.ctx, rows)]]
+    pos = s.plan.positions.tolist()
+    rng = np.random.Generator(np.random.PCG64(76))
+    cached = [[np64(s.cache.rows(w, 1, b, 0, s.ctx[b] + rows[b], codes=True)) for w in "kv"] for b in range(s.B)]
+    for b in range(s.B):
+        lo, hi = int(s.cu[b]), int(s.cu[b + 1])
+        # V goes through unchanged: all rows; Q and K: a sample of rows, the first and the last
+        for r in sorted({lo, hi - 1, *rng.integers(lo, max(lo + 1, hi), size=300).tolist()}) if hi > lo else []:
+            for name, x, gamma, n in (("q", q, s.gq, n_h), ("k", s.k, s.gk, n_kv), ("v", s.v, None, n_kv)):
+                if x is None:
+                    continue
+                src = s.q if name == "q" else x
+                y, mag = R.norm_rope(np64(src[r]).reshape(n, 128), None if gamma is None else np64(gamma),
+                                     pos[r], rope=name != "v")
+                out = "bf16"
+                if name == "q":
+                    got = np64(q_out[r]).reshape(n, 128)
+                else:
+                    got = cached[b]["kv".index(name)][:, pos[r]]
+                    if kv == "fp8":
+                        sc, out = s.scales[1]["kv".index(name)], "e4m3"
+                        y, mag = y / sc, mag / sc
+                assert (np.abs(got - y) <= R.append_bound(y, mag, 128, out)).all(), (b, r, name)
+    if mode == "apart":
+        assert (q_out[int(s.cu[-1]):] == 7.0).all()
+    if kv == "bf16":
+        for b in range(s.B):
+            want = s.v[int(s.cu[b]):int(s.cu[b + 1])].reshape(-1, n_kv, 128).permute(1, 0, 2)
+            assert torch.equal(s.cache.rows("v", 1, b, s.ctx[b], s.ctx[b] + rows[b]), want)
