@@ -351,8 +351,10 @@ dflash_status dflash_accept(const int32_t* block_ids, const int32_t* posterior, 
  * The rows of one step, grouped by sequence: rows cu_rows[b] .. cu_rows[b+1]-1 are the new
  * rows of sequence b, in order. All device memory owned by the caller, 4-byte aligned.
  *   cu_rows    int32 [batch + 1], cu_rows[0] = 0, non-decreasing, cu_rows[batch] <= rows.
- *              Rows cu_rows[batch] .. rows-1 are padding (a captured step of fixed size):
- *              no call reads or writes anything of theirs but their slot and position
+ *              Rows cu_rows[batch] .. rows-1 are padding (a captured step of fixed size). They
+ *              belong to the arrays: q, k and v of every call are readable for all `rows` rows.
+ *              Their values are never used, and nothing of theirs is written but their slot and
+ *              position
  *   kv_lens    int32 [batch]: rows sequence b holds once the step's rows are in, 0 for a
  *              refused sequence. The last new row of b is at position kv_lens[b] - 1
  *   slots      int32 [rows]: where a row's K and V go: page * 128 + row of the page (paged)
@@ -417,7 +419,8 @@ dflash_status dflash_chunk_map(const dflash_kv_cache* cache, int layer, const df
  *   K at s   = RoPE_p(RMSNorm_{gamma_k}(k[r]))   per head, in the cache's element type
  *   V at s   = v[r]
  * then lens[layer][b] = kv_lens[b] for every sequence with kv_lens[b] > 0. Rows with slot
- * -1 are skipped, their q_out left as it was.
+ * -1 are skipped, their q_out left as it was. With chunk->rows 0 nothing is done, to the lengths
+ * either.
  *   q, k, v        device rows of n_h * d_h, n_kv * d_h, n_kv * d_h elements of dims->dtype,
  *                  consecutive rows ld_q, ld_k, ld_v elements apart (at least the row;
  *                  slices of a fused projection's rows are fine). bf16: 16-byte aligned,

@@ -213,3 +213,30 @@ def test_append_of_a_large_step(D, kv, heads, paged, fused, mode):
         for b in range(s.B):
             want = s.v[int(s.cu[b]):int(s.cu[b + 1])].reshape(-1, n_kv, 128).permute(1, 0, 2)
             assert torch.equal(s.cache.rows("v", 1, b, s.ctx[b], s.ctx[b] + rows[b]), want)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "f32"])
+def test_padding_rows_are_readable_and_never_used(D, kv):
+    """Rows behind the last sequence belong to the arrays of a call; what they hold changes nothing."""
+    outs = []
+    for fill in (0.0, float("nan"), float("inf")):
+        s = Step(D, kv, (8, 2, 128), [200, 3], [40, 70], paged=kv != "f32", pad=40, seed=77, fused=False)
+        s.map()
+        e = int(s.cu[-1])
+        for x in (s.q, s.k, s.v):
+            x[e:] = fill
+        q = torch.zeros_like(s.q)
+        s.append(q)
+        q[e:] = fill
+        out = torch.full_like(q, 5.0)
+        s.attn(q, out, 100)
+        assert (out[e:] == 5.0).all()
+        outs.append((q[:e].clone(), out[:e], s.cache.k.view(torch.uint8), s.cache.v.view(torch.uint8)))
+    for o in outs[1:]:
+        for a, b in zip(outs[0], o):
+            assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        D.dflash_chunk_attn(s.dims, s.cache, 0, s.plan, q[:e], 0, 0.0, out, s.ws)
+    with pytest.raises(ValueError):
+        D.dflash_chunk_append(s.dims, s.cache, 0, s.plan, s.q, s.k[:e], s.v, s.gq, s.gk, s.table, s.cap, q)
+    assert D.dflash_status_get() == 0
