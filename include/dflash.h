@@ -463,7 +463,11 @@ dflash_status dflash_chunk_append(const dflash_dims* dims, const dflash_kv_cache
  * range set DFLASH_DEV_ROWS and are skipped; a page id outside the pool sets
  * DFLASH_DEV_PAGE and reads as zeros. bf16: weights are rounded to bf16 for the product with
  * V; E4M3: to f16 with 7 bits of headroom, which is relative (2^-11) down to 2^-21 of the row's
- * largest weight and 2^-32 of it below. Sums and maxima are fp32; the same inputs give the same bits.
+ * largest weight and 2^-32 of it below. E4M3: a query row of a head is held as two E4M3 codes an
+ * element under one power of two, exactly down to 2^-9 of the row's largest power of two and to
+ * 2^-17 of it below, so that scores move by at most 2^-17 max|q| sum|k| scaling (queries whose
+ * elements differ by less than about 2^10 lose less than the cache's own rounding of k). Sums and
+ * maxima are fp32; the same inputs give the same bits.
  * Unsupported: more than 8192 sequences, a capacity above 2^28, rows * G above 2^30, a layer of
  * more than 2^31 - 1 key rows (slots * n_kv), bf16 with G above 128. The status word may also
  * get DFLASH_DEV_TIMEOUT, as from every call with pipeline waits.

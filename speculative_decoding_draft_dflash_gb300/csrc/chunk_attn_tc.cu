@@ -327,7 +327,9 @@ struct Cursor {
 // overflows), the code and the code of its remainder, in place of the bf16 row, each 128 bytes
 // of the swizzled layout. The remainder of a bf16's 8 bits has at most 4, so the two hold it
 // exactly down to 2^-9 of the row's largest power of two; below, a remainder under the smallest
-// code is rounded, by at most 2^-17 of that power. Returns e.
+// code is rounded, by at most 2^-17 of that power. So an outlier of 2^p among elements around 1
+// moves scores by about 2^(p - 18) rms (random keys around 1, scaling 128^-1/2), where the cache's
+// rounding of the keys has moved them by about 2^-5: noticed from p = 12 on. Returns e.
 __device__ __noinline__ int q_codes(uint8_t* tile, int row) {
   uint8_t* at = tile + row * 128;
   const int sw = row & 7;

@@ -50,6 +50,39 @@ def test_attn_fp8_long_tail_behind_a_strong_key(D, B, heads, ctx, n, bits):
         assert (np.abs(on[lo:hi] - ref) <= tol).all(), b
 
 
+@pytest.mark.parametrize("n", [1, 40, 150])
+@pytest.mark.parametrize("power", [4, 8, 10])
+def test_attn_fp8_queries_with_outliers(D, n, power):
+    """Query rows with two elements 2^power above the rest, whose keys are small. A query next to
+    an E4M3 cache is two codes, each element off by at most 2^-17 of its row's largest power of
+    two: scores by e = 2^-17 max|q| sum|k| scaling, and a weight, relative, by exp(2 e) - 1 (its own
+    score and the sum's). The rest of the bound is the ordinary one."""
+    s = Step(D, "fp8", (8, 2, 128), [300, 0, 77], [n, n, n], seed=71)
+    s.map()
+    far = [5, 100]
+    for b in range(s.B):
+        tot = s.ctx[b] + n
+        K = torch.randn((2, tot, 128), generator=torch.Generator().manual_seed(b))
+        K[:, :, far] *= 2.0 ** -power
+        V = torch.randn((2, tot, 128), generator=torch.Generator().manual_seed(9 + b))
+        s.cache.set_rows(0, b, *(x.to(torch.float8_e4m3fn).view(torch.uint8).to(DEV) for x in (K, V)))
+    q = torch.randn((s.M, s.n_h, 128), generator=torch.Generator().manual_seed(72))
+    q[:, :, far] *= 2.0 ** power
+    q = q.reshape(s.M, -1).to(DEV, torch.bfloat16)
+    out = torch.empty_like(q)
+    s.attn(q, out)
+    assert D.dflash_status_get() == 0
+    qn, on = np64(q).reshape(s.M, s.n_h, 128), np64(out).reshape(s.M, s.n_h, 128)
+    sc = 128 ** -0.5
+    for b in range(s.B):
+        lo, hi = int(s.cu[b]), int(s.cu[b + 1])
+        k, v = s.cached(b, s.ctx[b] + n)
+        ref, mag, big, keys = R.attention(qn[lo:hi], k, v, s.ctx[b] + n, n, s.G, 0, sc)
+        e = 2.0 ** -17 * np.abs(qn[lo:hi]).max(-1) * np.abs(k).sum(-1).max() * sc      # [n][n_h]
+        tol = R.attention_bound(ref, mag, big, keys, 128, "bf16") + 1.01 * mag * np.expm1(2 * e)[..., None]
+        assert (np.abs(on[lo:hi] - ref) <= tol).all(), b
+
+
 @pytest.mark.parametrize("n", [1, 150])
 @pytest.mark.parametrize("k_scale,scaling", [(1e-12, 0.125), (0.5, 1e-30)])
 def test_attn_fp8_scores_below_the_smallest_float(D, n, k_scale, scaling):
