@@ -273,3 +273,107 @@ def test_padding_rows_are_readable_and_never_used(D, kv):
     with pytest.raises(ValueError):
         D.dflash_chunk_append(s.dims, s.cache, 0, s.plan, s.q, s.k[:e], s.v, s.gq, s.gk, s.table, s.cap, q)
     assert D.dflash_status_get() == 0
+
+
+# ---------------------------------------------------------------------------
+# rounds
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_rounds_leave_the_accepted_rows_in_the_cache(D, kv, graph):
+    """Map, append, attention, acceptance and crop over many rounds, call by call and as a graph.
+    After each round the cache holds the rows of the accepted tokens, made in float64 from
+    their projections at their positions, and nothing that was rejected; the attention is
+    compared with one over those rows."""
+    B, bs, L, n_h, n_kv, d, cap = 5, 6, 2, 8, 2, 128, 384
+    g = torch.Generator().manual_seed(2)
+    dt = torch.bfloat16
+    fp8 = kv == "fp8"
+    scales = [[0.5, 0.25], [0.125, 0.0625]]
+    dims = D.make_dims(n_h * d, n_h, n_kv, d, 1, bs, 1e-6, dt)
+    n_pages = B * (cap // 128)
+    cache = D.KVCache(L, B, n_kv, cap, d, dt, DEV, page_table=torch.full((B, cap // 128), -1), n_pages=n_pages,
+                      kv="fp8" if fp8 else "bf16", kv_scales=scales if fp8 else None)
+    pool = D.PagePool(i32([0] * B), i32(np.random.default_rng(4).permutation(n_pages)), i32([0]))
+    M = B * bs
+    plan = D.ChunkPlan(i32(np.arange(B + 1) * bs), M)
+    table = torch.empty((cap, d // 2, 2), dtype=torch.float32, device=DEV)
+    D.dflash_rope_table_build(1e6, d, cap, table)
+    gq, gk = ((1 + 0.2 * torch.randn(d, generator=g)).to(DEV, dt) for _ in range(2))
+    ws = torch.empty(D.dflash_chunk_workspace_bytes(dims), dtype=torch.uint8, device=DEV)
+    x = [torch.zeros((M, (n_h + 2 * n_kv) * d), dtype=dt, device=DEV) for _ in range(L)]
+    q = [torch.empty((M, n_h * d), dtype=dt, device=DEV) for _ in range(L)]
+    out = [torch.empty_like(q[0]) for _ in range(L)]
+    ids, post = (torch.zeros((B, bs), dtype=torch.int32, device=DEV) for _ in range(2))
+    start = cache.lens[0].clone()
+    acc, nxt, anchor = (torch.zeros(B, dtype=torch.int32, device=DEV) for _ in range(3))
+    ncu = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+
+    def step():
+        start.copy_(cache.lens[0])
+        D.dflash_chunk_map(cache, 0, plan, pool)
+        for l in range(L):
+            a, b, c = x[l].split((n_h * d, n_kv * d, n_kv * d), 1)
+            D.dflash_chunk_append(dims, cache, l, plan, a, b, c, gq, gk, table, cap, q[l])
+            D.dflash_chunk_attn(dims, cache, l, plan, q[l], 0 if l == 0 else 50, 0.0, out[l], ws)
+        D.dflash_accept(ids, post, start, acc, ncu, nxt, anchor)
+        D.dflash_cache_crop(cache, nxt)
+
+    if graph:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()                                   # warm-up, then back to the empty cache
+        torch.cuda.current_stream().wait_stream(side)
+        cache.lens.zero_(), pool.pages_held.zero_(), pool.taken.zero_(), cache.block_table.fill_(-1)
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            step()
+    gk64 = np64(gk)
+    # accepted rows in float64, [layer][sequence] -> list of (K, bound, V) of one row [n_kv][d]
+    held = [[[] for _ in range(B)] for _ in range(L)]
+
+    def block(l, b, start_pos):
+        """K, its bound, and V of the block's rows, in the cache's units (E4M3: codes' values)."""
+        rows = np64(x[l][b * bs:(b + 1) * bs])[:, n_h * d:].reshape(bs, 2, n_kv, d)
+        res = []
+        for i in range(bs):
+            y, mag = R.norm_rope(rows[i, 0], gk64, start_pos + i)
+            v = rows[i, 1]
+            if fp8:
+                y, mag, v = y / scales[l][0], mag / scales[l][0], v / scales[l][1]
+            vb = R.append_bound(v, np.abs(v), d, "e4m3") if fp8 else 0.0 * v
+            res.append((y, R.append_bound(y, mag, d, "e4m3" if fp8 else "bf16"), v, vb))
+        return res
+
+    for rnd in range(40):
+        for l in range(L):
+            x[l].copy_(torch.randn(x[l].shape, generator=g))
+        ids.copy_(torch.randint(0, 3, (B, bs), generator=g))
+        post.copy_(torch.randint(0, 3, (B, bs), generator=g))
+        gr.replay() if graph else step()
+        torch.cuda.synchronize()
+        a = acc.tolist()
+        check = rnd % 13 == 12 or rnd == 0
+        for l in range(L):
+            for b in range(B):
+                n0 = len(held[l][b])
+                rows = block(l, b, n0)
+                # what the attention saw: all rows of the block, the cache's older rows
+                now = held[l][b] + rows
+                K, V = (np64(cache.rows(w, l, b, 0, n0 + bs, codes=True)).transpose(1, 0, 2) for w in "kv")
+                assert (np.abs(K - np.stack([r[0] for r in now])) <= np.stack([r[1] for r in now])).all(), (rnd, l, b)
+                assert (np.abs(V - np.stack([r[2] for r in now])) <= np.stack([r[3] for r in now])).all(), (rnd, l, b)
+                held[l][b] += rows[:a[b] + 1]
+                if not check:
+                    continue
+                # (K and V as stored: they have just been held to the rows)
+                sk, sv = scales[l] if fp8 else (1.0, 1.0)
+                qr = np64(q[l][b * bs:(b + 1) * bs]).reshape(bs, n_h, d)
+                ref, mag, big, keys = R.attention(qr, K * sk, V * sv, n0 + bs, bs, n_h // n_kv, 0 if l == 0 else 50,
+                                                  d ** -0.5)
+                got = np64(out[l][b * bs:(b + 1) * bs]).reshape(bs, n_h, d)
+                assert (np.abs(got - ref) <= R.attention_bound(ref, mag, big, keys, d, "bf16")).all(), (rnd, l, b)
+        assert cache.lens.tolist() == [[len(held[0][b]) for b in range(B)]] * L
+    assert D.dflash_status_get() == 0
