@@ -192,7 +192,9 @@ DFLASH_API dflash_status dflash_chunk_attn(const dflash_dims* d, const dflash_kv
   p.d_h = d->d_h;
   p.G = d->n_h / d->n_kv;
   p.capacity = c->capacity;
-  p.window = sliding_window;
+  // No two rows of a sequence are a capacity apart: a window that large is none, and one that is
+  // smaller can be taken from any position without leaving 32 bits.
+  p.window = sliding_window < c->capacity ? sliding_window : 0;
   p.scaling = scaling > 0.f ? scaling : 1.f / sqrtf((float)d->d_h);
   p.fp8 = kv_fp8(c);
   p.k_scale = kv_scale(c, layer, 0);

@@ -1,7 +1,5 @@
 """The chunk step at the edges that its first tests leave out: weights and queries of extreme
 spread, values that are not finite, large steps, what a round leaves in the cache."""
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -154,6 +152,23 @@ def test_attn_some_keys_at_minus_infinity(D, kv, ctx, n):
     ref, mag, big, keys = R.attention(np64(q).reshape(s.M, 4, 128), k[300:], v[300:], ctx + n - 300, n, 2, 0, 128 ** -0.5)
     tol = R.attention_bound(ref, mag, big, keys, 128, kv)
     assert (np.abs(np64(out).reshape(s.M, 4, 128) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 64, 1000, 384, 383])
+def test_attn_windows_as_long_as_the_cache_and_longer(D, kv, window):
+    """Also where a sequence holds fewer rows than it has new ones, so that the first are at negative
+    positions and see nothing."""
+    s = Step(D, kv, (4, 2, 128), [0, 100], [150, 130], paged=kv != "f32", pad=1, seed=79, spare=0 if kv != "f32" else 128)
+    s.map()
+    q = torch.empty((s.M, 512), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    s.plan.kv_lens[0] = 98
+    out = torch.full_like(q, 5.0)
+    s.attn(q, out, window)
+    assert D.dflash_status_get() == 0
+    assert (out[:52] == 0).all() and (out[280:] == 5.0).all()
+    s.check_attn(q, out, window)
 
 
 # ---------------------------------------------------------------------------
