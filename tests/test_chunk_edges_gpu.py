@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import chunk_ref as R
-from test_chunk_gpu import DEV, D, Step, i32, np64  # noqa: F401  (D is the module's fixture)
+from test_chunk_gpu import DEV, D, Step, _check_map, _map_case, i32, np64  # noqa: F401  (D is the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -171,6 +171,22 @@ def test_attn_windows_as_long_as_the_cache_and_longer(D, kv, window):
     s.check_attn(q, out, window)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("ctx,rows,spare", [([40], [9], -79), ([0, 130], [1, 70], -55), ([0], [1], -127)])
+def test_attn_contiguous_capacities_that_end_inside_a_tile(D, kv, ctx, rows, spare):
+    """One KV head, so that the last tile reaches past the end of the cache."""
+    s = Step(D, kv, (4, 1, 128), ctx, rows, paged=False, seed=80, spare=spare)
+    assert s.cap == max(c + n for c, n in zip(ctx, rows)) + (0 if spare != -55 else 1)
+    s.map()
+    q = torch.empty((s.M, 512), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    out = torch.empty_like(q)
+    for window in (0, 5):
+        s.attn(q, out, window)
+        s.check_attn(q, out, window)
+    assert D.dflash_status_get() == 0
+
+
 # ---------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------
@@ -287,6 +303,24 @@ def test_padding_rows_are_readable_and_never_used(D, kv):
         D.dflash_chunk_attn(s.dims, s.cache, 0, s.plan, q[:e], 0, 0.0, out, s.ws)
     with pytest.raises(ValueError):
         D.dflash_chunk_append(s.dims, s.cache, 0, s.plan, s.q, s.k[:e], s.v, s.gq, s.gk, s.table, s.cap, q)
+    assert D.dflash_status_get() == 0
+
+
+# ---------------------------------------------------------------------------
+# map
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [1, 2500, 4500, 5500, 7000, 8192, 8193, 70_000])
+def test_map_in_place_of_any_size(D, rows):
+    """Outputs in place of the inputs (a PagePool's default): one to eight CTAs wait for one
+    another, and more rows than they have threads."""
+    rng = np.random.Generator(np.random.PCG64(rows))
+    B = 1 if rows == 1 else 256
+    lens = rng.integers(0, 2000, size=B)
+    n = rng.multinomial(rows - 1, [1 / B] * B) if B > 1 else np.array([rows])
+    args = _map_case(D, lens, n, 2560, rng.integers(0, 2, size=B), 6 * B, rows - int(n.sum()), rows, 3, True)
+    D.dflash_chunk_map(args[0], 0, args[1], args[2])
+    _check_map(*args)
     assert D.dflash_status_get() == 0
 
 
