@@ -66,10 +66,12 @@ __device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y
 // A unit is `span` heads of one row, two at a time: the slot, the position and the coefficients
 // are made once per unit (and kind of head), and the next 2 U heads are in flight while as many are
 // worked on. Addresses advance by a step and are looked up again where a tensor ends; Q, K and V
-// take the same way (V's products are not used), so the halves of a warp stay together. Bound
-// by HBM and issue slots: 9911 rows of 32 + 8 + 8 heads 46.2 us (5.3 TB/s; with addresses and
-// branches per head 49.9), 512 rows 4.2 us, five prompts on E4M3 20.8 us. More warps instead of
-// long units, and fewer registers with more CTAs, were slower (56 to 79 us).
+// take the same way (V's products are not used), so the halves of a warp stay together.
+// 9911 rows of 32 + 8 + 8 heads 46 us (5.3 TB/s; with addresses and branches per head 49.9), 512
+// rows 4.2 us, five prompts on E4M3 20.7 us. No unit is at its limit (issue slots 53 %, E4M3 57 %, DRAM
+// 53 and 32 %): an issued instruction waits 1.8 cycles on a load, on E4M3 3.4, where a lane's 8 bytes
+// loaded and 4 stored make as many instructions of half the bytes. More warps instead of long
+// units, and fewer registers with more CTAs, were slower (56 to 79 us).
 // ROPE false: the pairs are not mixed at all (an infinity times a sine of 0 would be a NaN).
 template <bool FP8, int U, bool ROPE>
 __global__ void __launch_bounds__(32 * kWarps, U == 2 ? 7 : 5) chunk_append_bf16_kernel(const ChunkAppendParams p, int span) {

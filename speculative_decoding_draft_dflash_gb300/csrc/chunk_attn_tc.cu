@@ -17,24 +17,31 @@
 // A and B, 11 (bf16) check of the V tiles that the mask cuts, (E4M3) Q to codes and V to f16.
 // Tensor memory: S_A, S_B, O_A, O_B of 128 columns each; P (16 bits) overwrites the first half
 // of its S and is the A operand of the PV product from there. P is rounded to bf16 next to a
-// bf16 V, as V was; next to E4M3 values to f16, which holds them exactly. f16 has few exponents:
-// weights and sums there carry a factor 2^7 (p stays below 2^15 of f16's 65504), which every
-// quotient divides out again. So a weight keeps 11 bits down to 2^-21 of the row's reference, and
-// one below 2^-32 is lost from the product (without the factor 2^-14 and 2^-25: 8191 keys of weight
-// 2^-25.5 behind one of weight 1 and value 0 lost half of their output).
+// bf16 V: both operands of an MMA have one type, and f16 does not hold every bf16 value. Relative
+// errors, root mean square against 64 bits: 0.0023, of which the output's own rounding to bf16 is
+// 0.0017. (A second term of P for the remainder would add half of a tile's MMAs again.) Next to
+// E4M3 values P is rounded to f16, which holds them exactly (0.0017 in all). f16 has few
+// exponents: weights and sums there carry a factor 2^7 (p stays below 2^15 of f16's 65504), which
+// every quotient divides out again. So a weight keeps 11 bits down to 2^-21 of the row's reference,
+// and one below 2^-32 is lost from the product (without the factor 2^-14 and 2^-25: 8191 keys of
+// weight 2^-25.5 behind one of weight 1 and value 0 lost half of their output).
 //
 // What bounds it. Many rows: the MMAs (1024 cycles a key tile and row tile with both products)
 // and the exponentials (128 x 128 at 16 a cycle and SM: 1024 too), which A and B overlap: 2800
 // to 3000 cycles per key tile of two row tiles, of which 2048 are MMAs. 8192 rows of 32 heads
-// from position 0: 354 us, 1.55 PFLOP/s of the 1.91 of a large matrix product. Few rows: HBM, as
-// long as an item is long (294400 keys of 8 heads read by single tokens: 188 us, 6.4 of 6.8 TB/s);
-// each further item costs about 3.7 us, in which the last tile's chain of S, softmax, PV and
-// epilogue has nothing behind it (32 blocks of 16 tokens over 256 to 4096 keys: 70 us, 4.9 TB/s).
+// from position 0: 354 us in a short run, 1.55 PFLOP/s of the 1.91 of a large matrix product, and
+// 378 us once calls follow one another for a second (the power limit lowers the clock; the matrix
+// product then runs at 1.72). Few rows: HBM, as long as an item is long (294400 keys of 8 heads read
+// by single tokens: 187 us, 6.4 of 6.8 TB/s); each further item costs about 3.7 us, in which the
+// last tile's chain of S, softmax, PV and epilogue has nothing behind it, as both accumulators end
+// together (32 blocks of 16 tokens over 256 to 4096 keys: 70 us, 4.9 TB/s).
 // E4M3 with few rows: 1990 cycles a tile on long sequences (294400 keys: 127 us, 4.7 TB/s) where
-// HBM would allow 1400, with the tensor pipe busy for 46 %: the chain of S, softmax and PV, of
-// which the two halves of the keys are all that overlaps. No link of it alone sets the time: with
+// HBM would allow 1400, with the tensor pipe busy for 46 %. Not the chain of S, softmax and PV: with
 // half the MMAs of S it would be 122 us, with half of PV's 124, with a quarter of V converted
-// 120, with all three 116; a softmax of 32 columns a thread is no faster either (below).
+// 120, with all three 116, and a softmax of 32 columns a thread is no faster (below). What fits is
+// the loads in flight: of the six stages of 16 KB one K tile is being multiplied and one V tile
+// converted, which leaves about 64 KB on their way, where bf16 has about 96 of 160 KB; at 4.7 and
+// 6.4 TB/s over 152 SMs both come to 2.1 to 2.3 us a load. Deeper rings have not been tried.
 //
 // Tried and slower. P as three E5M2 terms and V as stored, with no conversion (20 MMAs a tile
 // for 16, and the terms cost the softmax 420 instructions: 64 tokens 150 -> 200 us). Keys x rows
@@ -1157,6 +1164,21 @@ cudaError_t chunk_attn_tc(const ChunkAttnParams& a, cudaStream_t s) {
   memset(&p, 0, sizeof(p));
   p.TQ = 128 / a.G;
   p.RT = p.TQ * a.G;
+  // Cost units of the work split: an item (its start, and its end with nothing behind it), a key tile
+  // of two row tiles, and of one. Measured, us in a replayed graph, by the item's cost:
+  //   bf16                          0     4     8    12    16    24
+  //   32 blocks of 16 rows       72.9  70.1  70.3  70.2  71.1  72.1
+  //   8192-row prompt             421   389   351   374   376   383
+  //   12 chunks of 100 to 900     242   189   162   159   166   172
+  //   24 x 5 to 40 rows, G = 8  104.3  79.4  77.6  77.9  77.9  80.3
+  //   E4M3                          0     7    14    20    24    36
+  //   64 tokens                 168.6 158.3 151.1 152.6 154.0 158.9
+  //   32 blocks of 16 rows      100.2  69.7  64.8  64.4  64.3  66.2
+  //   8192-row prompt             543   495   455   427   413   420
+  //   12 chunks of 100 to 900     300   278   235   207   205   201
+  // (E4M3 stays at what is best for single tokens.) A tile of one row tile at 3/4 or half of one
+  // of two instead of at the same: 34 tokens and 6 chunks 110.9 (bf16, 3 : 4), 114.8 (2 : 4), 120.6
+  // (4 : 4); E4M3 121.6 (3 : 6), 133.4 (2 : 6), 151.1 (6 : 6).
   p.split = {a.cu_rows, a.kv_lens, a.batch, a.rows, a.n_kv, a.G, a.capacity, a.window, 2 * p.RT, 2 * p.TQ, p.RT, 7,
              a.fp8 ? 14 : 8, a.fp8 ? 6 : 4, 3};
   const long long kv_rows = a.block_table ? (long long)a.n_pages * a.n_kv * TK
