@@ -221,6 +221,30 @@ def test_append_without_rotation_keeps_infinities_apart(D, kv, rows, norm):
         assert (np.abs(g - y)[fin] <= R.append_bound(y, mag, 128, "f32" if kv == "f32" else "bf16")[fin]).all()
 
 
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("rows", [[9, 60], [900, 700]])
+def test_append_fp8_without_rotation(D, norm, rows):
+    """E4M3 codes of rows that are not rotated; an infinity saturates, its partner is untouched."""
+    s = Step(D, "fp8", (64, 8, 128), [5, 100], rows, seed=81)
+    s.map()
+    s.v[3, 7], s.v[4, 70] = float("inf"), -float("inf")
+    if not norm:
+        s.k[3, 7], s.k[4, 70] = float("inf"), -float("inf")
+    q_out = torch.empty((s.M, s.n_h * 128), dtype=s.q.dtype, device=DEV)
+    gq, gk = (s.gq, s.gk) if norm else (None, None)
+    D.dflash_chunk_append(s.dims, s.cache, 0, s.plan, s.q, s.k, s.v, gq, gk, None, 0, q_out)
+    assert D.dflash_status_get() == 0
+    for w, x, gamma in (("k", s.k, gk), ("v", s.v, None)):
+        got = np64(torch.cat([s.cache.rows(w, 0, b, s.ctx[b], s.ctx[b] + rows[b], codes=True) for b in range(2)], 1)
+                   .permute(1, 0, 2))
+        y, mag = R.norm_rope(np64(x).reshape(s.M, 8, 128), None if gamma is None else np64(gamma), 0, rope=False)
+        sc = s.scales[0]["kv".index(w)]
+        y, mag = np.clip(y / sc, -448, 448), np.clip(mag / sc, 0, 448)
+        assert (np.abs(got - y) <= R.append_bound(y, mag, 128, "e4m3")).all(), w
+    y, mag = R.norm_rope(np64(s.q).reshape(s.M, 64, 128), None if gq is None else np64(gq), 0, rope=False)
+    assert (np.abs(np64(q_out).reshape(s.M, 64, 128) - y) <= R.append_bound(y, mag, 128, "bf16")).all()
+
+
 LARGE = [("bf16", (32, 8), True, True), ("bf16", (5, 1), False, False), ("bf16", (14, 2), True, True),
          ("bf16", (64, 4), True, False), ("bf16", (128, 1), False, True), ("fp8", (32, 8), True, True),
          ("fp8", (5, 1), True, False), ("fp8", (64, 4), False, True), ("fp8", (128, 1), True, True)]
