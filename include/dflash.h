@@ -60,6 +60,7 @@ typedef enum { DFLASH_F32 = 0, DFLASH_BF16 = 1, DFLASH_FP8_E4M3 = 2 } dflash_dty
 #define DFLASH_DEV_ROWS      8u  /* cu_rows not non-decreasing or beyond M */
 #define DFLASH_DEV_TIMEOUT  16u  /* an internal pipeline wait gave up (kernel returned early) */
 #define DFLASH_DEV_PAGE     32u  /* a page id or a slot outside the cache: not read, not written */
+#define DFLASH_DEV_TREE     64u  /* a parent, a path or a node count that is none: sequence skipped */
 
 /*
  * Model dimensions.
@@ -479,6 +480,148 @@ dflash_status dflash_chunk_attn(const dflash_dims* dims, const dflash_kv_cache* 
                                 size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Trees: several continuations of one sequence behind its committed rows.
+ *
+ * A drafter that is unsure proposes a tree of tokens instead of a chain, and the target verifies
+ * all of them in one step; a beam search keeps its hypotheses as the leaves of one. The cache
+ * holds a sequence's committed rows and, behind them, a row per node of its tree in the order in
+ * which they came (a parent before its children). A node sees the committed rows and its
+ * ancestors, and sits at the position of its depth, not of its slot.
+ *
+ *   select  beams x vocabulary -> the k best continuations: tokens, parents, scores
+ *   map     parents -> positions, depths, ancestor masks (after dflash_chunk_map, before
+ *           dflash_chunk_append, which rotates by those positions)
+ *   attn    softmax(q K^T scaling) V over the committed rows and the ancestors
+ *   accept  tokens and the target's posterior -> the accepted path from node 0
+ *   commit  that path's K and V rows behind the committed ones, in every layer
+ *
+ * Reordering the states of a beam search is a matter of parents and masks alone: no row of the
+ * cache moves until a path is committed.
+ * (KV Cache + Speculative Decoding Interview Cheat Sheet, on drafters whose candidates form a tree:
+ * one pass verifies all of them under a tree mask. DFlash KV Injection Walkthrough, Steps 5-7: the
+ * block's tokens, the verification and the state update, for the tree with one leaf.)
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * The trees of a batch, device memory owned by the caller, 4-byte aligned. It stays with the
+ * cache from step to step; a step's rows are the newest nodes.
+ *   nodes    int32 [batch]: nodes of each sequence's tree, the last rows of its cache
+ *   depths   int32 [batch][max_nodes]: edges between a node and its tree's root
+ *   masks    uint32 [batch][max_nodes][max_nodes / 32]: bit u % 32 of word u / 32 of a node's row
+ *            set where the node sees node u. dflash_tree_map sets the ancestors and the node
+ *            itself; a caller may write other masks (dflash_tree_attn lets no node see a later one)
+ *   max_nodes  a multiple of 32, at most 4096; batch at most 4096
+ */
+typedef struct {
+  int32_t* nodes;
+  int32_t* depths;
+  uint32_t* masks;
+  int batch, max_nodes;
+} dflash_tree;
+
+/*
+ * Plans the trees of a step whose rows dflash_chunk_map has planned. Row i (from 0) of the n new
+ * rows of sequence b is node t = before + i, before = nodes_before[b], with parents[row] = u its
+ * parent's node, -1 <= u < t (-1: none, the node follows the committed rows):
+ *   depths[t] = depths[u] + 1 (0 without a parent), masks[t] = masks[u] and bit t,
+ *   positions[row] = kv_lens[b] - n - before + depths[t], nodes[b] = before + n.
+ * Refused, with slots, positions -1, kv_lens 0 and nodes[b] = before, so that the calls that
+ * follow skip the sequence: a parent outside its range, more than max_nodes nodes, more nodes
+ * than rows held (DFLASH_DEV_TREE); rows that are not a valid range (DFLASH_DEV_ROWS); a sequence
+ * the chunk map refused (kv_lens 0, new rows). The pages it was given stay its own. Rows of padding
+ * are left as they were.
+ *   parents       device int32 [rows]
+ *   nodes_before  device int32 [batch], may be tree->nodes; NULL: every tree begins with this step
+ * Host errors: null or misaligned pointers, tree->batch != chunk->batch, max_nodes that is not a
+ * positive multiple of 32; unsupported: max_nodes or batch above 4096.
+ */
+dflash_status dflash_tree_map(const dflash_chunk* chunk, const dflash_tree* tree, const int32_t* parents,
+                              const int32_t* nodes_before, cudaStream_t stream);
+
+/*
+ * dflash_chunk_attn with the trees' masks in place of the causal one. A new row that is node t of
+ * sequence b, with c = kv_lens[b] - nodes[b] committed rows, is at position c + depths[t] and sees
+ * the cached rows j < c and of the tree's rows c + u those of its mask with u <= t; with a sliding
+ * window W > 0 of both those whose position (j, c + depths[u]) is less than W before its own.
+ * Arguments, layouts, types, numerics, workspace (dflash_chunk_workspace_bytes) and limits are those of
+ * dflash_chunk_attn; at most 4096 sequences. A row that sees no key (an empty mask and no
+ * committed row, a refused sequence) is zero. nodes[b] below the step's rows, above max_nodes or above
+ * kv_lens[b] sets DFLASH_DEV_TREE and the sequence's rows are zero. Reads depths with a window only.
+ */
+dflash_status dflash_tree_attn(const dflash_dims* dims, const dflash_kv_cache* cache, int layer,
+                               const dflash_chunk* chunk, const dflash_tree* tree, const void* q,
+                               long long ld_q, int sliding_window, float scaling, void* out,
+                               void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Acceptance of verified trees. The rows of a step are whole trees (row i of a sequence is node
+ * i). From node 0, the anchor, the path goes on to the lowest node u with parents[u] the node it is
+ * at and tokens[u] == posterior of that node, the target's next token there, for at most max_path nodes:
+ *   path[b]         the path's nodes, 0 first, -1 behind the last
+ *   accept_len[b]   a: nodes of the path less the anchor
+ *   next_cu_rows    running sum of a + 1 (rows of the next inject), [0] = 0
+ *   ctx_next[b]     ctx_len[b] + a + 1
+ *   next_anchor[b]  posterior at the path's last node
+ * A sequence without rows, or refused (kv_lens[b] <= 0): a = -1, no path, anchor -1; the same for rows that
+ * are not a valid range (DFLASH_DEV_ROWS).
+ *   parents, tokens, posterior  device int32 [rows]; ctx_len int32 [batch], may be ctx_next
+ *   path  device int32 [batch][max_path]; next_cu_rows [batch + 1]; the others [batch]
+ * Reads chunk->cu_rows and kv_lens. Unsupported: more than 8192 sequences.
+ */
+dflash_status dflash_tree_accept(const dflash_chunk* chunk, const int32_t* parents, const int32_t* tokens,
+                                 const int32_t* posterior, const int32_t* ctx_len, int max_path,
+                                 int32_t* path, int32_t* accept_len, int32_t* next_cu_rows,
+                                 int32_t* ctx_next, int32_t* next_anchor, cudaStream_t stream);
+
+/*
+ * Commits the accepted path of every sequence with a = accept_len[b] >= 0: in each layer, the K and
+ * V rows of the nodes path[b][0 .. a] (row ctx_len[b] + node) become rows ctx_len[b] + 0 .. a, and
+ * the length lens[layer][b] = ctx_len[b] + a + 1. Nothing else of the cache changes. The tree is used
+ * up: the next dflash_tree_map begins a new one (nodes_before NULL or 0).
+ * accept_len -1 leaves a sequence as it is. A path that does not ascend within 0 .. nodes[b]-1, or
+ * has a >= max_path, or nodes that reach beyond the capacity: DFLASH_DEV_TREE, the sequence is left as it
+ * is. A page id outside the pool sets DFLASH_DEV_PAGE and the rows in it are not moved.
+ *   ctx_len, accept_len  device int32 [batch]; path device int32 [batch][max_path]
+ * Reads tree->nodes only. Host errors as for the other calls of the cache; unsupported: more than 4096
+ * sequences or 32767 layers.
+ */
+dflash_status dflash_tree_commit(const dflash_dims* dims, const dflash_kv_cache* cache, const dflash_tree* tree,
+                                 const int32_t* ctx_len, const int32_t* path, int max_path,
+                                 const int32_t* accept_len, cudaStream_t stream);
+
+/*
+ * The k best continuations of every sequence's beams by accumulated log-probability:
+ *   score(i, v) = scores[b][i] + log softmax(logits[b][i])[v]
+ * best first, equal scores by the lowest i * vocab + v:
+ *   tokens[b][j] = v, parents[b][j] = parent_base + i, scores_out[b][j] = score
+ * With beams 1 and k 1 that is the greedy token of each row; with parent_base the number of the
+ * level's first node, parents are those of dflash_tree_map. Scores are compared in 64 bits, in which the
+ * log-sum is within about 10^-8 (scores nearer than that to one another may change places), and
+ * rounded to f32 once. A beam whose score is not finite, or whose row holds NaN, plus infinity or no
+ * finite logit, has no probability: all its scores are minus infinity. So is that of a logit of
+ * minus infinity.
+ *   dtype       DFLASH_F32 or DFLASH_BF16, of the logits
+ *   logits      device; the row of beam i of sequence b starts ld_seq * b + ld_beam * i elements on.
+ *               ld_beam 0: one row for all beams of a sequence, read once. Any strides and any alignment of
+ *               an element; rows are dense
+ *   scores      device f32 [batch][beams], or NULL: 0
+ *   tokens, parents, scores_out  device, rows of k elements ld_out apart (>= k); parents and
+ *               scores_out may be NULL; none may overlap another or scores
+ *   workspace   dflash_beam_workspace_bytes of the same sizes, 256-byte aligned, of the calls that
+ *               run one after another
+ * The same inputs give the same bits. Host errors: sizes that are not positive, k above beams *
+ * vocab, a negative stride or parent_base; unsupported: beams or k above 128, beams * vocab above
+ * 2^31 - 1, batch * beams above 2^20.
+ */
+size_t dflash_beam_workspace_bytes(int batch, int beams, int vocab, int k);
+dflash_status dflash_beam_select(int dtype, const void* logits, long long ld_seq, long long ld_beam,
+                                 const float* scores, int batch, int beams, int vocab, int k,
+                                 int parent_base, int32_t* tokens, int32_t* parents, float* scores_out,
+                                 long long ld_out, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the current device's sticky
  * status word into *device_status (a mask of DFLASH_DEV_* bits). Returns
  * DFLASH_OK when the word was zero, DFLASH_ERR_DEVICE when not, and
@@ -507,6 +650,11 @@ const char* dflash_status_string(dflash_status s);
 #define DFLASH_KERNEL_CHUNK_APPEND 12  /* a step's norm, RoPE and cache rows */
 #define DFLASH_KERNEL_CHUNK_ATTN   13  /* causal attention of a step's rows */
 #define DFLASH_KERNEL_CHUNK_MERGE  14  /* merge of its split ranges */
+#define DFLASH_KERNEL_TREE_MAP     15  /* positions and masks of a step's tree rows */
+#define DFLASH_KERNEL_TREE_ACCEPT  16  /* the accepted path of a tree */
+#define DFLASH_KERNEL_TREE_COMMIT  17  /* that path's cache rows moved up */
+#define DFLASH_KERNEL_BEAM_SCAN    18  /* sums and best logits of pieces of the vocabulary */
+#define DFLASH_KERNEL_BEAM_MERGE   19  /* the best of all beams */
 
 /*
  * Starts recording a CUDA event pair around every launch whose kind bit

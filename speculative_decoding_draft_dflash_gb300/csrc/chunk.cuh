@@ -54,6 +54,16 @@ struct ChunkAppendParams {
 };
 cudaError_t chunk_append(int dtype, const ChunkAppendParams& p, cudaStream_t s);
 
+// The trees of a step (dflash_tree): which rows of their own tree its rows see.
+struct TreeRows {
+  const int32_t* nodes;   // [batch]; null: no trees, a row sees every row before it
+  const int32_t* depths;  // [batch][max_nodes]
+  const uint32_t* masks;  // [batch][max_nodes][max_nodes / 32]
+  int max_nodes;
+};
+constexpr int kTreeMaxBatch = 4096;
+constexpr int kTreeMaxNodes = 4096;
+
 struct ChunkAttnParams {
   const int32_t* cu_rows;
   const int32_t* kv_lens;
@@ -70,6 +80,7 @@ struct ChunkAttnParams {
   int batch, rows, n_h, n_kv, d_h, G, capacity, pages_per_seq, n_pages, window;
   float scaling, k_scale, v_scale;
   bool fp8;
+  TreeRows tree;
 };
 
 size_t chunk_attn_workspace(int dtype, int d_h);
@@ -80,6 +91,8 @@ int chunk_attn_simt_item_rows(int d_h);
 int chunk_attn_simt_ctas(int d_h);
 cudaError_t chunk_attn_simt(const ChunkAttnParams& p, cudaStream_t s);  // f32
 cudaError_t chunk_attn_tc(const ChunkAttnParams& p, cudaStream_t s);    // bf16
+cudaError_t tree_attn_simt(const ChunkAttnParams& p, cudaStream_t s);   // the same with trees
+cudaError_t tree_attn_tc(const ChunkAttnParams& p, cudaStream_t s);
 int chunk_attn_tc_item_rows(int G);
 
 // ---------------------------------------------------------------------------
@@ -98,7 +111,10 @@ namespace chunk {
 // TOKENS: an item is item_tokens whole tokens; else item_rows stacked rows wherever they end.
 // (The functions here are compiled into a kernel whose code has to stay small: what does not
 // fit the instruction cache is fetched again and again by warps that do different things.)
-template <bool TOKENS>
+// TREE: a sequence's last rows are the nodes of a tree (the step's rows the newest of them), the
+// rows before them committed. A row sees no key behind its own, as without a tree, so items, spans
+// and costs are the same; only a window's first key depends on the tree.
+template <bool TOKENS, bool TREE = false>
 struct Split {
   const int32_t* cu_rows;
   const int32_t* kv_lens;
@@ -109,15 +125,23 @@ struct Split {
   int tile_shift;  // log2 of a tile's keys
   // Cost units: an item, a key tile of an item, and of one of at most half_rows rows.
   int item_cost, tile_cost, half_cost;
+  const int32_t* nodes;  // TREE: nodes of each sequence's tree
+  int max_nodes;
 };
 
+template <bool TREE>
 struct Seq {
   int row0, n, kv;  // first row, new rows, rows held (0: refused)
 };
+template <>
+struct Seq<true> {
+  int row0, n, kv;
+  int ctx;          // committed rows: kv less the tree's nodes
+};
 
-template <bool TOKENS>
-__device__ __forceinline__ Seq load_seq(const Split<TOKENS>& p, int b, unsigned* bad) {
-  Seq s;
+template <bool TOKENS, bool TREE>
+__device__ __forceinline__ Seq<TREE> load_seq(const Split<TOKENS, TREE>& p, int b, unsigned* bad) {
+  Seq<TREE> s;
   s.row0 = p.cu_rows[b];
   s.n = p.cu_rows[b + 1] - s.row0;
   s.kv = p.kv_lens[b];
@@ -129,19 +153,28 @@ __device__ __forceinline__ Seq load_seq(const Split<TOKENS>& p, int b, unsigned*
     *bad |= DFLASH_DEV_CAPACITY;
     s.kv = 0;
   }
+  if constexpr (TREE) {
+    const int nodes = p.nodes[b];
+    s.ctx = s.kv - nodes;
+    if (s.kv > 0 && (nodes < s.n || nodes > p.max_nodes || s.ctx < 0)) {
+      *bad |= DFLASH_DEV_TREE;
+      s.kv = 0;
+    }
+    if (s.kv == 0) s.ctx = 0;
+  }
   return s;
 }
 
 // (rows * G fits 31 bits)
-template <bool TOKENS>
-__device__ __forceinline__ int n_items(const Split<TOKENS>& p, const Seq& s) {
+template <bool TOKENS, bool TREE>
+__device__ __forceinline__ int n_items(const Split<TOKENS, TREE>& p, const Seq<TREE>& s) {
   if (TOKENS) return (int)((unsigned)(s.n + p.item_tokens - 1) / (unsigned)p.item_tokens);
   return (int)((unsigned)(s.n * p.G + p.item_rows - 1) / (unsigned)p.item_rows);
 }
 
 // Positions of the first and the last row of item t.
-template <bool TOKENS>
-__device__ __forceinline__ int2 item_span(const Split<TOKENS>& p, const Seq& s, int t) {
+template <bool TOKENS, bool TREE>
+__device__ __forceinline__ int2 item_span(const Split<TOKENS, TREE>& p, const Seq<TREE>& s, int t) {
   const int p0 = s.kv - s.n;
   if (TOKENS) return make_int2(p0 + t * p.item_tokens, p0 + min((t + 1) * p.item_tokens, s.n) - 1);
   const unsigned r0 = t * p.item_rows, r1 = min(r0 + p.item_rows, (unsigned)(s.n * p.G));
@@ -149,39 +182,42 @@ __device__ __forceinline__ int2 item_span(const Split<TOKENS>& p, const Seq& s, 
 }
 
 // First key (a multiple of the tile) and key tiles of item t.
-template <bool TOKENS>
-__device__ __forceinline__ int2 item_keys(const Split<TOKENS>& p, const Seq& s, int t) {
+template <bool TOKENS, bool TREE>
+__device__ __forceinline__ int2 item_keys(const Split<TOKENS, TREE>& p, const Seq<TREE>& s, int t) {
   const int2 span = item_span(p, s, t);
   if (span.y < 0) return make_int2(0, 0);
   int k0 = 0;
-  if (p.window > 0 && span.x >= p.window) k0 = (span.x - p.window + 1) >> p.tile_shift << p.tile_shift;
+  int least = span.x;  // the lowest position of a row
+  if constexpr (TREE) least = s.ctx;
+  if (p.window > 0 && least >= p.window) k0 = (least - p.window + 1) >> p.tile_shift << p.tile_shift;
   return make_int2(k0, ((span.y - k0) >> p.tile_shift) + 1);
 }
 
 // Cost units of a key tile of item t, and of the whole item.
-template <bool TOKENS>
-__device__ __forceinline__ int tile_units(const Split<TOKENS>& p, const Seq& s, int t) {
+template <bool TOKENS, bool TREE>
+__device__ __forceinline__ int tile_units(const Split<TOKENS, TREE>& p, const Seq<TREE>& s, int t) {
   return s.n * p.G - t * p.item_rows > p.half_rows ? p.tile_cost : p.half_cost;
 }
-template <bool TOKENS>
-__device__ __forceinline__ int item_units(const Split<TOKENS>& p, const Seq& s, int t) {
+template <bool TOKENS, bool TREE>
+__device__ __forceinline__ int item_units(const Split<TOKENS, TREE>& p, const Seq<TREE>& s, int t) {
   return p.item_cost + tile_units(p, s, t) * item_keys(p, s, t).y;
 }
 
 // A CTA's share and where it starts.
+template <bool TREE>
 struct Start {
   long long begin, end;  // on the cost line
   long long total;
   int ctas;              // CTAs with a share
   int b, kvh, t;         // the item that holds `begin`
   int off;               // cost units of it before `begin`
-  Seq s;                 // its sequence
+  Seq<TREE> s;           // its sequence
 };
 
 // CTAs that get a share: large enough for a key tile, so that every CTA inside a cut item has
 // at least one.
-template <bool TOKENS>
-__device__ __forceinline__ int active_ctas(const Split<TOKENS>& p, long long total, int ctas) {
+template <bool TOKENS, bool TREE>
+__device__ __forceinline__ int active_ctas(const Split<TOKENS, TREE>& p, long long total, int ctas) {
   const int least = max(p.tile_cost, p.half_cost);
   return total >= (long long)ctas * least ? ctas : max(1, (int)(total / least));
 }
@@ -190,15 +226,16 @@ static __device__ __noinline__ long long bound(long long total, int active, int 
 }
 
 // Shared scratch of locate: every sequence and its cost.
-constexpr size_t kLocateBytes = sizeof(Seq) + sizeof(long long);  // per sequence
+template <bool TREE>
+constexpr size_t kLocateBytes = sizeof(Seq<TREE>) + sizeof(long long);  // per sequence
 
 // Run by all threads of the CTA; `scratch` is 16-byte aligned shared memory of kLocateBytes per
 // sequence (free again after the call and a __syncthreads), `st` shared. A thread per sequence
 // reads the lengths; then eight lanes per sequence add up its items.
-template <bool TOKENS>
-__device__ __noinline__ void locate(const Split<TOKENS>& p, void* scratch, Start* st, unsigned* status) {
+template <bool TOKENS, bool TREE>
+__device__ __noinline__ void locate(const Split<TOKENS, TREE>& p, void* scratch, Start<TREE>* st, unsigned* status) {
   long long* cost = reinterpret_cast<long long*>(scratch);
-  Seq* seq = reinterpret_cast<Seq*>(cost + p.batch);
+  Seq<TREE>* seq = reinterpret_cast<Seq<TREE>*>(cost + p.batch);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned bad = 0;
 #pragma unroll 1
@@ -210,7 +247,7 @@ __device__ __noinline__ void locate(const Split<TOKENS>& p, void* scratch, Start
     const int b = base + (threadIdx.x >> 3);
     long long sum = 0;
     if (b < p.batch) {
-      const Seq s = seq[b];
+      const Seq<TREE> s = seq[b];
       const int items = n_items(p, s);
 #pragma unroll 1
       for (int t = threadIdx.x & 7; t < items; t += 8) sum += item_units(p, s, t);
@@ -247,7 +284,7 @@ __device__ __noinline__ void locate(const Split<TOKENS>& p, void* scratch, Start
         if (cost[mid] > begin) hi = mid; else lo = mid + 1;
       }
       b = lo;
-      const Seq s = seq[b];
+      const Seq<TREE> s = seq[b];
       const long long before = b > 0 ? cost[b - 1] : 0;
       const long long per_head = bound(cost[b] - before, p.n_kv, 1);
       int kvh = 0;
@@ -297,24 +334,30 @@ __device__ __noinline__ void locate(const Split<TOKENS>& p, void* scratch, Start
 }
 
 // One piece of work: key tiles [tile0, tile1) of item t of (b, kvh).
-struct Piece {
+struct PieceOf {
   int b, kvh, t;
   int row0, n, kv;   // of the sequence
   int k0;            // first key of the item
   int tile0, tile1;
   int slot;          // -1: the whole item; else partial slot 0 or 1 of this CTA
 };
+template <bool TREE>
+struct Piece : PieceOf {};
+template <>
+struct Piece<true> : PieceOf {
+  int ctx;
+};
 
 // Walks a CTA's share piece by piece (one thread, or all threads of a warp alike).
-template <bool TOKENS>
+template <bool TOKENS, bool TREE>
 struct Walker {
-  Split<TOKENS> p;
-  Seq s;
+  Split<TOKENS, TREE> p;
+  Seq<TREE> s;
   long long at, end, total;
   int ctas, b, kvh, t, off;
   int4 merge;  // what to merge: {b, kvh, t, pieces}, pieces 0 when nothing was cut here
 
-  __device__ __forceinline__ void init(const Split<TOKENS>& split, const Start& st) {
+  __device__ __forceinline__ void init(const Split<TOKENS, TREE>& split, const Start<TREE>& st) {
     p = split;
     at = st.begin;
     end = st.end;
@@ -328,7 +371,7 @@ struct Walker {
     s = st.s;
   }
 
-  __device__ __forceinline__ bool next(Piece* w) {
+  __device__ __forceinline__ bool next(Piece<TREE>* w) {
     while (at < end) {
       const int items = n_items(p, s);
       if (t >= items) {  // next KV head, next sequence
@@ -353,6 +396,7 @@ struct Walker {
       w->row0 = s.row0;
       w->n = s.n;
       w->kv = s.kv;
+      if constexpr (TREE) w->ctx = s.ctx;
       w->k0 = keys.x;
       w->tile0 = tile0;
       w->tile1 = tile1;
@@ -378,6 +422,36 @@ struct Walker {
     return false;
   }
 };
+
+// Which of the keys k .. k + 31 the node `node` (none: -1) of sequence b's tree sees, as bits.
+// Committed keys by the window alone; keys of the tree by the node's mask, up to its own, and
+// by the window: a node's position is the committed rows plus its depth. (A window as deep as
+// the node cuts nothing from its tree, so depths are compared where it is not.)
+static __device__ __noinline__ uint32_t tree_bits(const TreeRows& t, int b, int node, int ctx, int k, int window) {
+  if (node < 0) return 0;
+  const int u0 = k - ctx;  // node of bit 0
+  const size_t row = (size_t)b * t.max_nodes;
+  const int depth = window > 0 ? t.depths[row + node] : 0;
+  uint32_t committed = u0 >= 0 ? 0u : u0 <= -32 ? 0xffffffffu : (1u << -u0) - 1u;
+  if (window > 0) {
+    const int l0 = ctx + depth - window + 1 - k;  // the first bit that the window leaves
+    committed &= l0 <= 0 ? 0xffffffffu : l0 > 31 ? 0u : 0xffffffffu << l0;
+  }
+  if (u0 <= -32 || u0 > node) return committed;
+  const int words = t.max_nodes >> 5, i = u0 >> 5;  // (u0 >> 5 is -1 for -31 .. -1)
+  const uint32_t* m = t.masks + (row + node) * words;
+  const uint32_t lo = i >= 0 ? m[i] : 0u, hi = i + 1 < words ? m[i + 1] : 0u;
+  uint32_t bits = __funnelshift_r(lo, hi, u0 & 31);
+  const int last = node - u0;  // >= 0
+  bits &= last >= 31 ? 0xffffffffu : (2u << last) - 1u;
+  if (window > 0 && depth >= window) {
+    for (uint32_t left = bits; left; left &= left - 1) {
+      const int e = __ffs(left) - 1;
+      if (depth - t.depths[row + u0 + e] >= window) bits &= ~(1u << e);
+    }
+  }
+  return committed | bits;
+}
 
 }  // namespace chunk
 }  // namespace dflash

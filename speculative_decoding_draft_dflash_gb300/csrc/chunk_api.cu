@@ -148,10 +148,12 @@ DFLASH_API size_t dflash_chunk_workspace_bytes(const dflash_dims* d) {
   return chunk_attn_workspace(d->dtype, d->d_h);
 }
 
-DFLASH_API dflash_status dflash_chunk_attn(const dflash_dims* d, const dflash_kv_cache* c, int layer,
-                                           const dflash_chunk* ch, const void* q, long long ld_q,
-                                           int sliding_window, float scaling, void* out,
-                                           void* workspace, size_t ws_bytes, cudaStream_t stream) {
+namespace {
+
+// dflash_chunk_attn (tree null) and dflash_tree_attn.
+dflash_status attention(const dflash_dims* d, const dflash_kv_cache* c, int layer, const dflash_chunk* ch,
+                        const dflash_tree* tree, const void* q, long long ld_q, int sliding_window, float scaling,
+                        void* out, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   dflash_status st = check_dims(d);
   if (st != DFLASH_OK) return st;
   st = check_cache(c, layer);
@@ -160,6 +162,12 @@ DFLASH_API dflash_status dflash_chunk_attn(const dflash_dims* d, const dflash_kv
   if (st != DFLASH_OK) return st;
   st = check_chunk(c, ch, false);
   if (st != DFLASH_OK) return st;
+  if (tree) {
+    if (!tree->nodes || !tree->depths || !tree->masks || !aligned4(tree->nodes) || !aligned4(tree->depths) ||
+        !aligned4(tree->masks) || tree->batch != c->batch || tree->max_nodes <= 0 || tree->max_nodes % 32)
+      return DFLASH_ERR_INVALID_ARG;
+    if (tree->max_nodes > kTreeMaxNodes || c->batch > kTreeMaxBatch) return DFLASH_ERR_UNSUPPORTED;
+  }
   // key rows of one layer are addressed with 32-bit row numbers
   if (cache_slots(c) * d->n_kv > 0x7fffffffll || c->capacity > (1 << 28)) return DFLASH_ERR_UNSUPPORTED;
   if ((long long)ch->rows * (d->n_h / d->n_kv) > (1 << 30)) return DFLASH_ERR_UNSUPPORTED;
@@ -199,5 +207,23 @@ DFLASH_API dflash_status dflash_chunk_attn(const dflash_dims* d, const dflash_kv
   p.fp8 = kv_fp8(c);
   p.k_scale = kv_scale(c, layer, 0);
   p.v_scale = kv_scale(c, layer, 1);
+  if (tree) p.tree = {tree->nodes, tree->depths, tree->masks, tree->max_nodes};
   return cuda_status(chunk_attn(d->dtype, p, stream));
+}
+
+}  // namespace
+
+DFLASH_API dflash_status dflash_chunk_attn(const dflash_dims* d, const dflash_kv_cache* c, int layer,
+                                           const dflash_chunk* ch, const void* q, long long ld_q,
+                                           int sliding_window, float scaling, void* out,
+                                           void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  return attention(d, c, layer, ch, nullptr, q, ld_q, sliding_window, scaling, out, workspace, ws_bytes, stream);
+}
+
+DFLASH_API dflash_status dflash_tree_attn(const dflash_dims* d, const dflash_kv_cache* c, int layer,
+                                          const dflash_chunk* ch, const dflash_tree* tree, const void* q,
+                                          long long ld_q, int sliding_window, float scaling, void* out,
+                                          void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (!tree) return DFLASH_ERR_INVALID_ARG;
+  return attention(d, c, layer, ch, tree, q, ld_q, sliding_window, scaling, out, workspace, ws_bytes, stream);
 }

@@ -152,7 +152,9 @@ bool chunk_attn_carve(int dtype, int d_h, ChunkAttnParams& p, void* workspace, s
 }
 
 cudaError_t chunk_attn(int dtype, const ChunkAttnParams& p, cudaStream_t s) {
-  cudaError_t e = dtype == DFLASH_F32 ? chunk_attn_simt(p, s) : chunk_attn_tc(p, s);
+  const bool f32 = dtype == DFLASH_F32;
+  cudaError_t e = p.tree.nodes ? (f32 ? tree_attn_simt(p, s) : tree_attn_tc(p, s))
+                               : (f32 ? chunk_attn_simt(p, s) : chunk_attn_tc(p, s));
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_MERGE, s);
   cudaLaunchConfig_t cfg = {};

@@ -68,8 +68,8 @@ __device__ __forceinline__ void load_tile(float* dst, const float* src, int d, i
 }
 
 // One piece of work. RPT: query rows per thread (the item has at most 16 RPT).
-template <int DP, int RPT>
-__device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Piece& w, int r0, int rows, float* Qs,
+template <int DP, int RPT, bool TREE>
+__device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Piece<TREE>& w, int r0, int rows, float* Qs,
                                       float* Ks, float* Vs, float* Ps) {
   constexpr int LD = DP + 4, LQ = item_rows(DP) + 4;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, d = p.d_h;
@@ -101,6 +101,7 @@ __device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Pie
     Qs[(c0 + 3) * LQ + r] = x.w;
   }
   float m[RPT], l[RPT];
+  [[maybe_unused]] unsigned seen = 0;  // TREE: rows that have seen a key, whatever its score
   float2 o[RPT][DP / 32];  // columns 4 tx + 64 c .. + 3 in pairs
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
@@ -113,11 +114,16 @@ __device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Pie
   // Keys of this warp's 2 RPT rows: a warp skips the products of a tile that none of them sees.
   const int wr = (ty & ~1) * RPT;
   const int wlast = wr < rows ? w.kv - w.n + (r0 + min(wr + 2 * RPT, rows) - 1) / p.G : -1;
-  const int wfirst = p.window > 0 ? w.kv - w.n + (r0 + wr) / p.G - p.window + 1 : 0;
+  int wfirst = p.window > 0 ? w.kv - w.n + (r0 + wr) / p.G - p.window + 1 : 0;
+  int closed = first + 1;  // the first key that not every row sees, but for the window
+  if constexpr (TREE) {
+    closed = w.ctx;
+    if (p.window > 0) wfirst = w.ctx - p.window + 1;
+  }
   for (int j = w.tile0; j < w.tile1; ++j) {
     const int k0 = w.k0 + j * TK;
     const bool sees = k0 <= wlast && k0 + TK > wfirst;
-    const bool open = k0 + TK - 1 <= first && (p.window <= 0 || last - k0 < p.window);  // every key by every row
+    const bool open = k0 + TK <= closed && (p.window <= 0 || last - k0 < p.window);  // every key by every row
     const bool more = j + 1 < w.tile1;
     copy_wait<1>();  // K_j (V_j may be on its way)
     __syncthreads();
@@ -176,8 +182,19 @@ __device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Pie
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int key = k0 + tx + 16 * k;
-          if (key > pos || (p.window > 0 && pos - key >= p.window)) s[i][k] = -INFINITY;
+          if (!TREE && (key > pos || (p.window > 0 && pos - key >= p.window))) s[i][k] = -INFINITY;
         }
+        if constexpr (TREE) {
+          const int node = pos < 0 ? -1 : pos - w.ctx;
+          const uint32_t b0 = chunk::tree_bits(p.tree, w.b, node, w.ctx, k0, p.window);
+          const uint32_t b1 = chunk::tree_bits(p.tree, w.b, node, w.ctx, k0 + 32, p.window);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (((k < 2 ? b0 : b1) >> (tx + 16 * (k & 1)) & 1) == 0) s[i][k] = -INFINITY;
+          if (b0 | b1) seen |= 1u << i;
+        }
+      } else if constexpr (TREE) {
+        seen |= 1u << i;
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx = fmaxf(mx, s[i][k]);
@@ -265,18 +282,19 @@ __device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Pie
     const int token = (r0 + r) / p.G, g = r0 + r - token * p.G;
     float* dst = w.slot < 0 ? (float*)p.out + ((size_t)(w.row0 + token) * p.n_h + w.kvh * p.G + g) * d : p.part + part * d;
     // no weight at all: 0 where no key is seen, else (every score minus infinity) NaN
-    const float inv = w.slot >= 0 ? 1.f : sum != 0.f ? 1.f / sum : w.kv - w.n + token >= 0 ? NAN : 0.f;
+    const bool sees_any = TREE ? (seen >> i & 1) != 0 : w.kv - w.n + token >= 0;
+    const float inv = w.slot >= 0 ? 1.f : sum != 0.f ? 1.f / sum : sees_any ? NAN : 0.f;
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e) {
       const int c = tx * 4 + 64 * (e >> 1) + 2 * (e & 1);  // (d is even)
       if (c < d) *reinterpret_cast<float2*>(dst + c) = make_float2(o[i][e].x * inv, o[i][e].y * inv);
     }
     if (w.slot >= 0 && tx == 0)
-      p.part_ml[part] = make_float2(sum == 0.f && w.kv - w.n + token >= 0 ? -FLT_MAX : m[i], sum);
+      p.part_ml[part] = make_float2(sum == 0.f && sees_any ? -FLT_MAX : m[i], sum);
   }
 }
 
-template <int DP>
+template <int DP, bool TREE>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(DP)) chunk_attn_simt_kernel(const ChunkAttnParams p) {
   constexpr int LD = DP + 4, RI = item_rows(DP);
   extern __shared__ float4 smem4[];
@@ -284,45 +302,45 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DP)) chunk_attn_simt_ker
   float* Ks = Qs + DP * (RI + 4);
   float* Vs = Ks + TK * LD;
   float* Ps = Vs + TK * LD;
-  __shared__ chunk::Start start;
+  __shared__ chunk::Start<TREE> start;
   // Cost units: an item 2, a tile 6, one of an item of few rows 3 (or 2). In a replayed graph, an item at 0,
   // 2, 4, 8: 6 prompts 135, 133, 132, 132 us, 32 blocks of 16 rows 227, 227, 228, 237. A tile of few rows
   // at 2, 3, 6 of 6: 14 tokens and 6 chunks 149, 145, 190, 6 prompts 146, 133, 140.
-  const chunk::Split<false> split = {p.cu_rows, p.kv_lens, p.batch, p.rows, p.n_kv, p.G, p.capacity,
-                              p.window, RI, 0, RI / (RI > 64 ? 2 : 4), 6, 2, 6, RI > 64 ? 3 : 2};
+  const chunk::Split<false, TREE> split = {p.cu_rows, p.kv_lens, p.batch, p.rows, p.n_kv, p.G, p.capacity,
+                              p.window, RI, 0, RI / (RI > 64 ? 2 : 4), 6, 2, 6, RI > 64 ? 3 : 2, p.tree.nodes, p.tree.max_nodes};
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be scheduled
   chunk::locate(split, smem4, &start, p.status);
-  chunk::Walker<false> walk;
+  chunk::Walker<false, TREE> walk;
   walk.init(split, start);
   __syncthreads();
   // columns beyond d_h stay zero
   for (int i = threadIdx.x; i < 2 * TK * LD; i += kThreads) Ks[i] = 0.f;
-  chunk::Piece w;
+  chunk::Piece<TREE> w;
   while (walk.next(&w)) {
     const int r0 = w.t * RI, rows = min(RI, w.n * p.G - r0);
     __syncthreads();
     if (rows <= 16)
-      piece<DP, 1>(p, w, r0, rows, Qs, Ks, Vs, Ps);
+      piece<DP, 1, TREE>(p, w, r0, rows, Qs, Ks, Vs, Ps);
     else if (RI == 64 || rows <= 64)
-      piece<DP, 4>(p, w, r0, rows, Qs, Ks, Vs, Ps);
+      piece<DP, 4, TREE>(p, w, r0, rows, Qs, Ks, Vs, Ps);
     else
-      piece<DP, RI / 16>(p, w, r0, rows, Qs, Ks, Vs, Ps);
+      piece<DP, RI / 16, TREE>(p, w, r0, rows, Qs, Ks, Vs, Ps);
   }
   if (threadIdx.x == 0) p.merge[blockIdx.x] = walk.merge;
 }
 
-template <int DP>
+template <int DP, bool TREE>
 cudaError_t launch(const ChunkAttnParams& p, cudaStream_t s) {
   constexpr int RI = item_rows(DP);
   const int tiles = (int)sizeof(float) * (DP * (RI + 4) + 2 * TK * (DP + 4) + RI * LP);
-  const int scratch = (int)(chunk::kLocateBytes * p.batch);
+  const int scratch = (int)(chunk::kLocateBytes<TREE> * p.batch);
   const int smem = tiles > scratch ? tiles : scratch;
-  const int most = (int)(chunk::kLocateBytes * kChunkMaxBatch);
+  const int most = (int)(chunk::kLocateBytes<TREE> * (TREE ? kTreeMaxBatch : kChunkMaxBatch));
   static SmemLimit limit;
-  cudaError_t e = limit.raise(chunk_attn_simt_kernel<DP>, tiles > most ? tiles : most);
+  cudaError_t e = limit.raise(chunk_attn_simt_kernel<DP, TREE>, tiles > most ? tiles : most);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_ATTN, s);
-  chunk_attn_simt_kernel<DP><<<chunk_attn_simt_ctas(p.d_h), kThreads, smem, s>>>(p);
+  chunk_attn_simt_kernel<DP, TREE><<<chunk_attn_simt_ctas(p.d_h), kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -332,9 +350,15 @@ int chunk_attn_simt_item_rows(int d_h) { return item_rows(d_h); }
 int chunk_attn_simt_ctas(int d_h) { return chunk_sms() * ctas_per_sm(d_h); }
 
 cudaError_t chunk_attn_simt(const ChunkAttnParams& p, cudaStream_t s) {
-  if (p.d_h <= 64) return launch<64>(p, s);
-  if (p.d_h <= 128) return launch<128>(p, s);
-  return launch<256>(p, s);
+  if (p.d_h <= 64) return launch<64, false>(p, s);
+  if (p.d_h <= 128) return launch<128, false>(p, s);
+  return launch<256, false>(p, s);
+}
+
+cudaError_t tree_attn_simt(const ChunkAttnParams& p, cudaStream_t s) {
+  if (p.d_h <= 64) return launch<64, true>(p, s);
+  if (p.d_h <= 128) return launch<128, true>(p, s);
+  return launch<256, true>(p, s);
 }
 
 }  // namespace dflash

@@ -22,11 +22,12 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdflash.so")
 
 DFLASH_F32, DFLASH_BF16 = 0, 1
-DEV_CAPACITY, DEV_ROPE, DEV_CROP, DEV_ROWS, DEV_TIMEOUT, DEV_PAGE = 1, 2, 4, 8, 16, 32
+DEV_CAPACITY, DEV_ROPE, DEV_CROP, DEV_ROWS, DEV_TIMEOUT, DEV_PAGE, DEV_TREE = 1, 2, 4, 8, 16, 32, 64
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE = range(6)
 KERNEL_NAMES = {1: "gemm", 2: "rmsnorm", 3: "head_epilogue", 4: "attention", 5: "combine",
                 6: "lens", 7: "crop", 8: "rope_table", 9: "schedule", 10: "accept",
-                11: "chunk_map", 12: "chunk_append", 13: "chunk_attn", 14: "chunk_merge"}
+                11: "chunk_map", 12: "chunk_append", 13: "chunk_attn", 14: "chunk_merge",
+                15: "tree_map", 16: "tree_accept", 17: "tree_commit", 18: "beam_scan", 19: "beam_merge"}
 KERNEL_IDS = {v: k for k, v in KERNEL_NAMES.items()}
 
 
@@ -62,6 +63,11 @@ class dflash_page_pool(ctypes.Structure):
                 ("taken_out", c_void_p)]
 
 
+class dflash_tree(ctypes.Structure):
+    _fields_ = [("nodes", c_void_p), ("depths", c_void_p), ("masks", c_void_p), ("batch", c_int),
+                ("max_nodes", c_int)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libdflash.so is not built ({LIB_PATH}); run "
@@ -89,6 +95,14 @@ def _load():
         "dflash_chunk_workspace_bytes": (c_size_t, [P]),
         "dflash_chunk_attn": (c_int, [P, P, c_int, P, P, c_longlong, c_int, c_float, P, P, c_size_t,
                                       P]),
+        "dflash_tree_map": (c_int, [P, P, P, P, P]),
+        "dflash_tree_attn": (c_int, [P, P, c_int, P, P, P, c_longlong, c_int, c_float, P, P, c_size_t,
+                                     P]),
+        "dflash_tree_accept": (c_int, [P, P, P, P, P, c_int, P, P, P, P, P, P]),
+        "dflash_tree_commit": (c_int, [P, P, P, P, P, c_int, P, P]),
+        "dflash_beam_workspace_bytes": (c_size_t, [c_int] * 4),
+        "dflash_beam_select": (c_int, [c_int, P, c_longlong, c_longlong, P, c_int, c_int, c_int, c_int,
+                                       c_int, P, P, P, c_longlong, P, c_size_t, P]),
         "dflash_status_get": (c_int, [POINTER(c_uint), P]),
         "dflash_status_string": (ctypes.c_char_p, [c_int]),
         "dflash_trace_start": (c_int, [c_uint, c_int]),
@@ -351,6 +365,33 @@ class PagePool:
                     taken=taken, taken_out=self.taken_out)
 
 
+class Tree:
+    """The trees of a batch (dflash_tree): nodes int32 [batch], depths int32 [batch][max_nodes] and
+    masks int32 [batch][max_nodes][max_nodes / 32] (bit u % 32 of word u / 32: the node sees node u).
+    Arrays that are not given are allocated on `device` (where they are, those that are given),
+    as zeros."""
+
+    def __init__(self, batch, max_nodes, device=None, nodes=None, depths=None, masks=None):
+        i32 = torch.int32
+        self.batch, self.max_nodes = int(batch), int(max_nodes)
+        if self.batch < 1 or self.max_nodes < 32 or self.max_nodes % 32:
+            raise ValueError(f"tree: {self.batch} sequences, max_nodes {self.max_nodes} (a multiple of 32)")
+        if device is None:
+            device = next((t.device for t in (nodes, depths, masks) if t is not None), "cuda")
+        new = lambda *shape: torch.zeros(shape, dtype=i32, device=device)  # noqa: E731
+        words = self.max_nodes // 32
+        self.nodes = new(self.batch) if nodes is None else nodes
+        self.depths = new(self.batch, self.max_nodes) if depths is None else depths
+        self.masks = new(self.batch, self.max_nodes, words) if masks is None else masks
+        self.device = self.nodes.get_device()
+        self.desc = dflash_tree(_ptr(self.nodes, "nodes", i32, self.batch),
+                                _ptr(self.depths, "depths", i32, self.batch * self.max_nodes),
+                                _ptr(self.masks, "masks", i32, self.batch * self.max_nodes * words),
+                                self.batch, self.max_nodes)
+        _one_device(self.device, depths=self.depths, masks=self.masks)
+        self.ref = ctypes.byref(self.desc)
+
+
 # ---------------------------------------------------------------------------
 # the C calls
 # ---------------------------------------------------------------------------
@@ -565,6 +606,111 @@ def dflash_chunk_attn(dims, cache, layer, plan, q, sliding_window, scaling, out,
                                   _chunk(plan, desc, cache), qp, ldq, int(sliding_window), float(scaling),
                                   _array(out, "out", et, plan.rows * qw, plan.device), *_ws(workspace),
                                   _stream(stream)), "dflash_chunk_attn")
+
+
+def _tree(tree, plan):
+    if tree.batch != plan.batch:
+        raise ValueError(f"tree: {tree.batch} sequences, the plan has {plan.batch}")
+    if tree.device != plan.device:
+        raise ValueError(f"tree: on device {tree.device}, the plan is on {plan.device}")
+    return tree.ref
+
+
+def _on_current(what, device):
+    if device != _current_device():
+        raise ValueError(f"{what}: on device {device}, the current one is {_current_device()}")
+
+
+def dflash_tree_map(plan, tree, parents, nodes_before=None, stream=None):
+    """Positions, depths and ancestor masks of a step's rows, after dflash_chunk_map."""
+    i32, dev = torch.int32, plan.device
+    _on_current("chunk plan", dev)
+    _check(_lib.dflash_tree_map(plan.ref, _tree(tree, plan), _array(parents, "parents", i32, plan.rows, dev),
+                                _array(nodes_before, "nodes_before", i32, plan.batch, dev), _stream(stream)),
+           "dflash_tree_map")
+
+
+def dflash_tree_attn(dims, cache, layer, plan, tree, q, sliding_window, scaling, out, workspace,
+                     stream=None):
+    """Attention of a step's rows over their committed rows and their trees' ancestors."""
+    desc, et = _desc(dims, cache), _et(dims)
+    qw = dims.n_h * dims.d_h
+    qp, ldq = _rows(q, "q", et, plan.rows, qw)
+    if isinstance(workspace, torch.Tensor) and workspace.get_device() != plan.device:
+        raise ValueError(f"workspace: on device {workspace.get_device()}, the plan is on {plan.device}")
+    _check(_lib.dflash_tree_attn(ctypes.byref(dims), ctypes.byref(desc), int(layer), _chunk(plan, desc, cache),
+                                 _tree(tree, plan), qp, ldq, int(sliding_window), float(scaling),
+                                 _array(out, "out", et, plan.rows * qw, plan.device), *_ws(workspace),
+                                 _stream(stream)), "dflash_tree_attn")
+
+
+def dflash_tree_accept(plan, parents, tokens, posterior, ctx_len, accept_len, path, next_cu_rows,
+                       ctx_next, next_anchor, stream=None):
+    """The accepted path of every sequence's tree; path is int32 [batch][max_path]."""
+    i32, dev, rows, batch = torch.int32, plan.device, plan.rows, plan.batch
+    _on_current("chunk plan", dev)
+    if path.dim() != 2 or path.shape[0] < batch:
+        raise ValueError(f"path: shape {tuple(path.shape)}, the call needs [{batch}][max_path]")
+    arr = lambda t, what, n: _array(t, what, i32, n, dev)  # noqa: E731
+    _check(_lib.dflash_tree_accept(plan.ref, arr(parents, "parents", rows), arr(tokens, "tokens", rows),
+                                   arr(posterior, "posterior", rows), arr(ctx_len, "ctx_len", batch),
+                                   int(path.shape[1]), arr(path, "path", 0), arr(accept_len, "accept_len", batch),
+                                   arr(next_cu_rows, "next_cu_rows", batch + 1), arr(ctx_next, "ctx_next", batch),
+                                   arr(next_anchor, "next_anchor", batch), _stream(stream)),
+           "dflash_tree_accept")
+
+
+def dflash_tree_commit(dims, cache, tree, ctx_len, path, accept_len, stream=None):
+    """Moves the accepted paths' rows behind the committed ones, in every layer, and sets lengths."""
+    i32, desc, dev = torch.int32, _desc(dims, cache), tree.device
+    _on_current("tree", dev)
+    if tree.batch != desc.batch:
+        raise ValueError(f"tree: {tree.batch} sequences, the cache has {desc.batch}")
+    if cache is not desc and cache.device != dev:
+        raise ValueError(f"cache: on device {cache.device}, the tree is on {dev}")
+    if path.dim() != 2 or path.shape[0] < tree.batch:
+        raise ValueError(f"path: shape {tuple(path.shape)}, the call needs [{tree.batch}][max_path]")
+    _check(_lib.dflash_tree_commit(ctypes.byref(dims), ctypes.byref(desc), tree.ref,
+                                   _array(ctx_len, "ctx_len", i32, tree.batch, dev), _array(path, "path", i32, 0, dev),
+                                   int(path.shape[1]), _array(accept_len, "accept_len", i32, tree.batch, dev),
+                                   _stream(stream)), "dflash_tree_commit")
+
+
+def dflash_beam_workspace_bytes(batch, beams, vocab, k):
+    return int(_lib.dflash_beam_workspace_bytes(int(batch), int(beams), int(vocab), int(k)))
+
+
+def _k_rows(t, what, dtype, batch, k, device):
+    """(address, elements between rows) of an output [batch][>= k] whose rows are dense."""
+    if t is None:
+        return None, None
+    if t.dtype is not dtype or t.get_device() != device or t.dim() != 2 or t.shape[0] < batch or t.shape[1] < k or \
+            (t.stride(1) != 1 and k > 1):
+        raise ValueError(f"{what}: {t.dtype} of shape {tuple(t.shape)}, strides {t.stride()} on device "
+                         f"{t.get_device()}; the call needs {dtype} [{batch}][{k}] on device {device}")
+    return t.data_ptr(), t.stride(0) if batch > 1 else k
+
+
+def dflash_beam_select(logits, scores, k, tokens, parents, scores_out, workspace, parent_base=0, stream=None):
+    """The k best of every sequence's beams x vocabulary; logits [batch][beams][vocab], float32 or
+    bfloat16, of any strides between rows (a row expanded over the beams is read once); scores
+    float32 [batch][beams] or None; tokens, parents and scores_out [batch][k], their rows alike far apart
+    (slices of node arrays are fine), the latter two may be None."""
+    if not logits.is_cuda or logits.dim() != 3 or (logits.shape[2] > 1 and logits.stride(2) != 1):
+        raise ValueError("logits: expected a CUDA tensor [batch][beams][vocab] with dense rows")
+    (batch, beams, vocab), dev, k = logits.shape, logits.get_device(), int(k)
+    _on_current("logits", dev)
+    tp, ld = _k_rows(tokens, "tokens", torch.int32, batch, k, dev)
+    pp, ldp = _k_rows(parents, "parents", torch.int32, batch, k, dev)
+    sp, lds = _k_rows(scores_out, "scores_out", torch.float32, batch, k, dev)
+    if ld is None or ldp not in (None, ld) or lds not in (None, ld):
+        raise ValueError(f"tokens, parents, scores_out: rows {ld}, {ldp}, {lds} elements apart, the call needs one distance")
+    if isinstance(workspace, torch.Tensor) and workspace.get_device() != dev:
+        raise ValueError(f"workspace: on device {workspace.get_device()}, the logits are on {dev}")
+    _check(_lib.dflash_beam_select(dtype_code(logits.dtype), logits.data_ptr(), logits.stride(0), logits.stride(1),
+                                   _array(scores, "scores", torch.float32, batch * beams, dev), batch, beams, vocab, k,
+                                   int(parent_base), tp, pp, sp, ld, *_ws(workspace), _stream(stream)),
+           "dflash_beam_select")
 
 
 def dflash_layer_out_workspace_bytes(dims, M, d_ff):
