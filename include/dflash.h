@@ -612,8 +612,8 @@ dflash_status dflash_tree_commit(const dflash_dims* dims, const dflash_kv_cache*
  *   workspace   dflash_beam_workspace_bytes of the same sizes, 256-byte aligned, of the calls that
  *               run one after another
  * The same inputs give the same bits. Host errors: sizes that are not positive, k above beams *
- * vocab, a negative stride or parent_base; unsupported: beams or k above 128, beams * vocab above
- * 2^31 - 1, batch * beams above 2^20.
+ * vocab, a negative stride or parent_base; unsupported: beams or k above 128, vocab above 2^28,
+ * beams * vocab above 2^31 - 1, batch * beams above 2^20.
  */
 size_t dflash_beam_workspace_bytes(int batch, int beams, int vocab, int k);
 dflash_status dflash_beam_select(int dtype, const void* logits, long long ld_seq, long long ld_beam,

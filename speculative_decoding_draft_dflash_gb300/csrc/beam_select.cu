@@ -8,24 +8,26 @@
 // own order needs no sum, and a candidate of the whole selection is among its row's k best.
 // The merge, a CTA per sequence, joins the pieces' sums, ranks the candidates in 64 bits and writes.
 //
-// The k largest. Every lane keeps the maximum of what it has seen; the q-th largest of a warp's lanes,
-// the lowest of the CTA's eight such values (8 q >= k), is reached by at least k elements, so that
-// nothing below it is a candidate. Warps publish theirs when they meet candidates and need not wait for
-// one another: an old value is only a lower one. A vector of eight logits that reaches the bound is
-// noted, by its maximum and number; the noted vectors are read again at the end, against the last
-// bound, and only then are elements looked at one by one (taken as they came, that cost twice the sum's
-// instructions). Notes that do not fit (rows of equal or of ascending logits) are cut to the k vectors
-// of the largest maxima: each of the others has k elements before all of its own.
+// The k largest. Every lane keeps the maximum of what it has seen. The q-th largest of a warp's lanes, of
+// the CTA's eight such values the s-th largest (q s >= k), is reached by at least k elements, so that
+// nothing below it is a candidate. (s = 6: random logits reach it 1.8 k times; s = 8, the lowest value,
+// 2.6 k times.) The first tile gives such a bound, more of them a better one (without waiting for
+// one another: a warp's old value is only a lower one). A lane whose 64 bytes of a tile reach it notes their
+// maximum and number, for itself; the elements of noted runs are looked at one by one at the end, against the
+// bound of all tiles, of a few runs of a warp. A lane whose notes are full has the bound looked at again, and
+// where that does not help (rows of equal or of ascending logits) the warp keeps the k runs of the largest
+// maxima: each of the others has k elements before all of its own. (Elements taken as they came, or a list of a
+// warp's, cost more than the sums: what a warp does beside them waits for votes, shuffles and instructions
+// that are not in the cache.)
 //
 // The sum. Which candidate of two beams is the better one is decided by the difference of two such
 // sums, so their errors must stay far below the gaps between scores (about 10^-2 among the best of a
-// vocabulary). d = x - ref is exact for bf16 within 16 binades; with t = fl(d log2 e) and
-// r = d log2 e - t (a fused multiply-add and the constant's second word), e^d = 2^t (1 + r ln 2): the terms
-// 2^t and 2^t r are added up apart. (t alone would be off by up to 10^-6.) Terms in fp32, a thread's
-// tiles added with their rounding errors kept, the rest in 64 bits. The few large terms of a row, where
-// 2^t's error of 2^-22 does not average out, are taken again by the merge. The order of the
-// additions depends on the vocabulary alone, so equal rows have equal sums and their candidates tie as
-// they should.
+// vocabulary): d = x - ref (exact for bf16 within 16 binades), e^d = 2^(d log2 e). The product's rounding
+// moves a term by up to 10^-6, but either way and by another amount for every value, so that 10^-8 is left
+// of it in a sum of a vocabulary (measured: 2 10^-8 at most); the few large terms of a row, where
+// it does not average out, are taken again by the merge. Terms in fp32, a thread's tiles added with their
+// rounding errors kept, the rest in 64 bits. The order of the additions depends on the
+// vocabulary alone, so equal rows have equal sums and their candidates tie as they should.
 #include <float.h>
 
 #include "tree.cuh"
@@ -35,7 +37,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kNotes = 192;    // noted vectors of a warp: kBeamMax and 32 at least
 constexpr int kMergeCap = 1024;  // entries of the merge's list
 constexpr float kFar = 40.f;   // how far above the reference a logit may lie
 
@@ -52,11 +53,6 @@ __device__ __forceinline__ float logit_of(u64 e) {
 }
 __device__ __forceinline__ uint32_t token_of(u64 e) { return 0xffffffffu - (uint32_t)e; }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -66,24 +62,17 @@ __device__ __forceinline__ float ex2(float x) {
 // log2 e and ln 2 as a float and what it leaves.
 constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f;
 constexpr float kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;
-constexpr float kDeep = -200.f;  // e^d is 0 from here on
-constexpr float kLowest = -3.38953139e38f;  // of bf16: below it a reference has no floor
 
-// The terms of e^d for kDeep <= d <= kFar: sum += 2^t, rest += 2^t r (twice).
-__device__ __forceinline__ void add_exp(float2 d, float2& sum, float2& rest) {
-  const float2 l = make_float2(kLog2e, kLog2e);
-  const float2 t = __fmul2_rn(d, l);
-  float2 r = __ffma2_rn(d, l, make_float2(-t.x, -t.y));
-  r = __ffma2_rn(d, make_float2(kLog2eLow, kLog2eLow), r);
-  const float2 e = make_float2(ex2(t.x), ex2(t.y));
-  sum = __fadd2_rn(sum, e);
-  rest = __ffma2_rn(e, r, rest);
+// The term of e^d: 0 for minus infinity.
+__device__ __forceinline__ float2 exp_of(float2 d) {
+  const float2 t = __fmul2_rn(d, make_float2(kLog2e, kLog2e));
+  return make_float2(ex2(t.x), ex2(t.y));
 }
 
 // e^d to 2^-27 as hi + lo, -80 <= d <= 80: e^d = 2^n 2^(f + g), f = fl(d log2 e) - n and g what the
 // product left, and 2^f = 1 + f ln 2 + f^2 P(f), the first product and sum with their rounding errors
 // (P: the Taylor terms up to f^8, 10^-9 at |f| = 1/2).
-__device__ __forceinline__ float2 exp_pair(float d) {
+__device__ __noinline__ float2 exp_pair(float d) {
   const float t = d * kLog2e, n = rintf(t), f = t - n;
   const float g = fmaf(d, kLog2eLow, fmaf(d, kLog2e, -t));
   float q = 1.32154868e-6f;
@@ -132,15 +121,9 @@ struct Bytes16 {
 template <typename T> struct Vec;
 template <> struct Vec<bf16> : Bytes16 {
   static constexpr int E = 8;
+  static __device__ __forceinline__ float read(const bf16* x) { return __bfloat162float(*x); }
   __device__ __forceinline__ float at(int i) const {
     return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-  }
-  // elements from e on, of which `end` exist; the others -inf
-  __device__ __forceinline__ void load(const bf16* row, int e, int end) {
-    const uint16_t* x = reinterpret_cast<const uint16_t*>(row);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = (e + 2 * i < end ? x[e + 2 * i] : 0xFF80u) | (e + 2 * i + 1 < end ? x[e + 2 * i + 1] : 0xFF80u) << 16;
   }
   __device__ __forceinline__ void keep(int n) {  // all but the first n become -inf
 #pragma unroll
@@ -149,43 +132,32 @@ template <> struct Vec<bf16> : Bytes16 {
       if (2 * i + 1 >= n) w[i] = (w[i] & 0xffffu) | 0xFF800000u;
     }
   }
-  __device__ __forceinline__ float most() const {  // (NaN only where all are)
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(w);
-    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
+  // Largest elements, in as many lots as is cheap: two halves of a word (NaN only where all are)
+  typedef uint32_t Most;
+  static __device__ __forceinline__ Most larger(Most a, Most b) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
   }
-  // x - ref of elements i and i + 1, where it matters: what is below the floor (a bf16 below
-  // ref + kDeep, so its weight is 0) is taken for it, as a product with -inf would be NaN
-  __device__ __forceinline__ float2 below(int i, float ref, uint32_t floor2) const {
-    const __nv_bfloat162 m = __hmax2_nan(reinterpret_cast<const __nv_bfloat162*>(w)[i >> 1],
-                                         *reinterpret_cast<const __nv_bfloat162*>(&floor2));
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
-    return __fadd2_rn(make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)), make_float2(-ref, -ref));
+  static __device__ __forceinline__ float value(Most a) {
+    return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
   }
-  static __device__ __forceinline__ uint32_t floor_of(float ref) {
-    const bf16 f = __float2bfloat16_rd(ref + 2 * kDeep);
-    uint32_t u = *reinterpret_cast<const uint16_t*>(&f);
-    if (__uint_as_float(u << 16) >= ref) u = u & 0x8000u ? u + 1 : u - 1;  // |ref| so large that 400 is lost
-    return u | u << 16;
-  }
+  __device__ __forceinline__ Most most() const { return larger(larger(w[0], w[1]), larger(w[2], w[3])); }
+  static constexpr Most kNone = 0xFF80FF80u;
 };
 template <> struct Vec<float> : Bytes16 {
   static constexpr int E = 4;
+  static __device__ __forceinline__ float read(const float* x) { return *x; }
   __device__ __forceinline__ float at(int i) const { return __uint_as_float(w[i]); }
-  __device__ __forceinline__ void load(const float* row, int e, int end) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = e + i < end ? __float_as_uint(row[e + i]) : 0xFF800000u;
-  }
   __device__ __forceinline__ void keep(int n) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i >= n) w[i] = 0xFF800000u;
   }
-  __device__ __forceinline__ float most() const { return fmaxf(fmaxf(at(0), at(1)), fmaxf(at(2), at(3))); }
-  __device__ __forceinline__ float2 below(int i, float ref, uint32_t) const {
-    return make_float2(max_nan(at(i) - ref, kDeep), max_nan(at(i + 1) - ref, kDeep));
-  }
-  static __device__ __forceinline__ uint32_t floor_of(float) { return 0; }
+  typedef float Most;
+  static __device__ __forceinline__ Most larger(Most a, Most b) { return fmaxf(a, b); }
+  static __device__ __forceinline__ float value(Most a) { return a; }
+  __device__ __forceinline__ Most most() const { return fmaxf(fmaxf(at(0), at(1)), fmaxf(at(2), at(3))); }
+  static constexpr Most kNone = -INFINITY;
 };
 
 struct Piece {  // of a row: the reference and the sum under it
@@ -199,38 +171,22 @@ struct Scan {
   long long ld_seq, ld_beam;
   u64* lists;     // [rows][splits][k], best first, 0 where there is none
   Piece* pieces;  // [rows][splits]
-  int vocab, rows_per_seq, splits, chunk, k;
+  int vocab, rows_per_seq, splits, chunk, k, pieces_n;
 };
 
-// Entry i's place among n: how many are before it.
+// (The code here is run once or twice a piece by warps that do different things. What does not fit the
+// instruction cache is fetched again and again, so it is kept small: few instances, few loops unrolled.)
+
+// An entry's place among those of a list, n of them padded with zeros to a multiple of four: how many
+// are before it.
 __device__ __forceinline__ int rank_of(const u64* e, int n, u64 mine) {
   int rank = 0;
-  int j = 0;
-  for (; j + 2 <= n; j += 2) {
-    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(e + j);
-    rank += (two.x > mine) + (two.y > mine);
+#pragma unroll 1
+  for (int j = 0; j < n; j += 4) {
+    const ulonglong2 a = reinterpret_cast<const ulonglong2*>(e + j)[0], b = reinterpret_cast<const ulonglong2*>(e + j)[1];
+    rank += (a.x > mine) + (a.y > mine) + (b.x > mine) + (b.y > mine);
   }
-  if (j < n) rank += e[j] > mine;
   return rank;
-}
-
-// Cuts a warp's list of n entries, k <= n <= N, to its k best, best first.
-template <int N>
-__device__ __forceinline__ void cut_warp_list(u64* e, int n, int k) {
-  const int lane = threadIdx.x & 31;
-  u64 mine[N / 32];
-  int rank[N / 32];
-#pragma unroll
-  for (int t = 0; t < N / 32; ++t) {
-    const int i = lane + 32 * t;
-    mine[t] = i < n ? e[i] : 0;
-    rank[t] = i < n ? rank_of(e, n, mine[t]) : k;
-  }
-  __syncwarp();
-#pragma unroll
-  for (int t = 0; t < N / 32; ++t)
-    if (rank[t] < k) e[rank[t]] = mine[t];
-  __syncwarp();
 }
 
 // A float's bits in order.
@@ -242,33 +198,100 @@ __device__ __forceinline__ float float_of(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// Reads a warp's noted vectors (numbers from element `begin` on) again and enters the elements that reach
-// the bound in its list, at most kEntries of which the k best are kept. Returns how many there are, at most k
-// or what was entered in a list that was never full.
-constexpr int kEntries = 256;
-template <typename T>
-__device__ __noinline__ int enter(const T* x, int begin, int end, const u64* notes, int n, u64* list, int k, float bound) {
-  constexpr int E = Vec<T>::E;
+constexpr int kSlots = 8;      // notes of a lane
+constexpr int kEntries = 160;  // of a warp's list: kBeamMax and 32 at least
+
+// Cuts a list of N entries (0: none), more than k of them, to the k best, best first, the others 0. Returns the
+// last one.
+template <int N>
+__device__ __forceinline__ u64 cut(u64* e, int k) {
+  const int lane = threadIdx.x & 31;
+  u64 mine[N / 32];
+  int rank[N / 32];
+#pragma unroll
+  for (int t = 0; t < N / 32; ++t) mine[t] = e[lane + 32 * t];
+#pragma unroll
+  for (int t = 0; t < N / 32; ++t) rank[t] = mine[t] != 0 ? rank_of(e, N, mine[t]) : N;
+  __syncwarp();
+#pragma unroll
+  for (int t = 0; t < N / 32; ++t) e[lane + 32 * t] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int t = 0; t < N / 32; ++t)
+    if (rank[t] < k) e[rank[t]] = mine[t];
+  __syncwarp();
+  return e[k - 1];
+}
+
+// A warp's notes, one lane's below one another: drops those below the bound and, if a lane is still full,
+// all but the k best, which it spreads over the lanes. Returns a bound for what comes later and the
+// lane's notes.
+struct Cleared {
+  float bound;
+  int of_lane;
+};
+__device__ __noinline__ Cleared clear_notes(u64* notes, int n, int k, float bound) {
   const int lane = threadIdx.x & 31;
   const uint32_t reach = order_of(bound + 0.f);
+  int kept = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const u64 note = notes[32 * i + lane];
+    if ((uint32_t)(note >> 32) >= reach) notes[32 * kept++ + lane] = note;
+  }
+  if (!__any_sync(0xffffffffu, kept == kSlots)) return {bound, kept};
+#pragma unroll 1
+  for (int i = kept; i < kSlots; ++i) notes[32 * i + lane] = 0;
+  const int all = __reduce_add_sync(0xffffffffu, kept);
+  __syncwarp();
+  float later = bound;
+  if (all > k) later = fmaxf(bound, float_of((uint32_t)(cut<32 * kSlots>(notes, k) >> 32) + 1));
+  else cut<32 * kSlots>(notes, all);  // (they are spread, but all of them stay)
+  const int left = min(all, k);
+  return {later, left > lane ? (left - lane + 31) / 32 : 0};
+}
+
+// Enters the elements of a warp's noted runs (L each, numbered from element `begin` on) that reach the
+// bound in its list, of which the k best are kept. Returns how many there are, at most k, padded with
+// zeros to a multiple of four.
+template <typename T, int L>
+__device__ __noinline__ int enter(const T* x, int begin, int end, u64* notes, int of_lane, u64* list, int k, float bound) {
+  constexpr int PER = 32 / L, AHEAD = 4;  // runs at a time, and of them in flight
+  const int lane = threadIdx.x & 31;
+  const uint32_t reach = order_of(bound + 0.f);
+  int kept = 0;  // notes that still reach the bound
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; __any_sync(0xffffffffu, i < of_lane); ++i) {
+    const u64 note = i < of_lane ? notes[32 * i + lane] : 0;
+    const bool is = note != 0 && (uint32_t)(note >> 32) >= reach;
+    const unsigned who = __ballot_sync(0xffffffffu, is);
+    if (is) notes[kept + __popc(who & ((1u << lane) - 1))] = note;
+    kept += __popc(who);
+    __syncwarp();
+  }
   u64 least = 0;
   int count = 0;
-  for (int g = 0; g < n; g += 32) {
-    const u64 note = g + lane < n ? notes[g + lane] : 0;
-    const bool is = note != 0 && (uint32_t)(note >> 32) >= reach;
-    if (!__any_sync(0xffffffffu, is)) continue;
-    const int e = is ? begin + (int)token_of(note) * E : end;
-    Vec<T> v;
-    v.load(x, e, end);
+#pragma unroll 1
+  for (int g = 0; g < kept; g += PER * AHEAD) {
+    float v[AHEAD];
+    int at[AHEAD];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const u64 entry = entry_of(v.at(i), e + i);
-      unsigned who = __ballot_sync(0xffffffffu, e + i < end && v.at(i) >= bound && entry > least);
+    for (int a = 0; a < AHEAD; ++a) {
+      const int i = g + a * PER + lane / L;
+      at[a] = i < kept ? begin + (int)token_of(notes[i]) * L + lane % L : end;
+      v[a] = at[a] < end ? Vec<T>::read(x + at[a]) : 0.f;
+    }
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      const u64 entry = entry_of(v[a], at[a]);
+      unsigned who = __ballot_sync(0xffffffffu, at[a] < end && v[a] >= bound && entry > least);
       if (who == 0) continue;
       if (count + __popc(who) > kEntries) {
-        cut_warp_list<kEntries>(list, count, k);
+        for (int i = count + lane; i < kEntries; i += 32) list[i] = 0;
+        __syncwarp();
+        least = cut<kEntries>(list, k);
         count = k;
-        least = list[k - 1];
         who = __ballot_sync(0xffffffffu, (who >> lane & 1) != 0 && entry > least);
       }
       if (who >> lane & 1) list[count + __popc(who & ((1u << lane) - 1))] = entry;
@@ -277,9 +300,12 @@ __device__ __noinline__ int enter(const T* x, int begin, int end, const u64* not
     }
   }
   if (count > k) {
-    cut_warp_list<kEntries>(list, count, k);
+    for (int i = count + lane; i < kEntries; i += 32) list[i] = 0;
+    __syncwarp();
+    cut<kEntries>(list, k);
     count = k;
   }
+  if (lane < 3 && count + lane < kEntries) list[count + lane] = 0;
   return count;
 }
 
@@ -298,10 +324,11 @@ __device__ __forceinline__ float sort_lanes(float v) {
   return v;
 }
 // The q-th largest of the lanes' values.
-__device__ __forceinline__ float nth_lane(float v, int q) {
+__device__ __noinline__ float nth_lane(float v, int q) {
   if (q > 8) return q > 32 ? -INFINITY : __shfl_sync(0xffffffffu, sort_lanes(v), q - 1);
   const int lane = threadIdx.x & 31;
   uint32_t k = order_of(v), m = __reduce_max_sync(0xffffffffu, k);
+#pragma unroll 1
   for (int i = 1; i < q; ++i) {
     if (lane == __ffs(__ballot_sync(0xffffffffu, k == m)) - 1) k = 0;
     m = __reduce_max_sync(0xffffffffu, k);
@@ -309,232 +336,247 @@ __device__ __forceinline__ float nth_lane(float v, int q) {
   return m == 0 ? -INFINITY : float_of(m);
 }
 
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-constexpr int kVecs = 4;     // of a thread and tile
-constexpr int kStages = 3;   // tiles of a warp on their way or in use
-constexpr int kSpan = 33;    // 16-byte blocks of a warp's vectors of one number, one more for rows that are not aligned
+// The nth largest of the first n <= 8 of the warps' values.
+__device__ __noinline__ float nth_of(const volatile float* value, int n, int nth) {
+  const int lane = threadIdx.x & 31;
+  const float mine = lane < n ? value[lane] : -INFINITY;
+  int before = lane < n ? 0 : 32;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float v = __shfl_sync(0xffffffffu, mine, w);
+    before += v > mine || (v == mine && w < lane);
+  }
+  const unsigned who = __ballot_sync(0xffffffffu, before == nth - 1);
+  return who ? __shfl_sync(0xffffffffu, mine, __ffs(who) - 1) : -INFINITY;
+}
 
+constexpr int kStages = 3;   // tiles of a warp on their way or in use
+
+// J: 16-byte blocks of a lane and tile.
+template <int J>
 struct ScanSmem {
-  uint4 ring[kWarps][kStages][kVecs][kSpan];
-  u64 notes[kWarps][kNotes];
+  uint4 ring[kWarps][kStages][32 * J + 1];  // (one block more for rows that are not aligned)
+  u64 notes[kWarps][32 * kSlots];
+  u64 entries[kWarps][kEntries];
   double wsum[kWarps];
   float wbound[kWarps], wmax[kWarps];
-  int count;
+  int wcount[kWarps];
 };
 
-// Vector j of a thread in the tile at `base`: elements base + (j * kThreads + thread) * E and on. Each warp
-// copies its own vectors ahead, so that warps need not wait for one another.
-template <typename T>
+// Persistent: CTA c takes the pieces c, c + CTAs, .., one after another. A tile is 4 J KB of the row, 512 J
+// bytes a warp, 16 J bytes in order a lane. Each warp copies its own blocks ahead, into the next piece
+// too, so that warps need not wait for one another within a piece and a piece's end hides behind the
+// loads of the next. A lane reads its blocks, eight lanes at a time: with J = 4, blocks are exchanged
+// within fours (by bits 3 and 4 of their number) to lie in different banks.
+template <typename T, int J>
 __global__ void __launch_bounds__(kThreads, 3) beam_scan_kernel(const Scan p) {
-  constexpr int J = kVecs, E = Vec<T>::E, STEP = kThreads * E, TILE = STEP * J;
+  constexpr int E = Vec<T>::E, L = J * E, TILE = kThreads * L, SPAN = 32 * J + 1;
   extern __shared__ __align__(16) unsigned char smem[];
-  ScanSmem& sh = *reinterpret_cast<ScanSmem*>(smem);
+  ScanSmem<J>& sh = *reinterpret_cast<ScanSmem<J>*>(smem);
   volatile float* wbound = sh.wbound;
   float* wmax = sh.wmax;
-  double* wsum = sh.wsum;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be scheduled
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int seq = blockIdx.x, beam = blockIdx.y, split = blockIdx.z;
-  const T* x = (const T*)p.logits + seq * p.ld_seq + beam * p.ld_beam;
-  const int shift = (int)((uintptr_t)x & 15);
-  const char* blocks = (const char*)x - shift;  // the row's 16-byte blocks
-  const int begin = min(p.vocab, split * p.chunk), end = min(p.vocab, begin + p.chunk);
-  const long long stop = shift + (long long)end * (int)sizeof(T);  // bytes of the blocks that matter
-  u64* notes = sh.notes[warp];
-  int noted = 0;
-  // warps that have a vector per lane in the first tile have a say in the bound
-  const int voters = min(kWarps, (end - begin) / (32 * E)), q = voters ? (p.k + voters - 1) / voters : 64;
-  auto copy = [&](int base, int stage) {
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const long long at = (long long)(base + j * STEP + warp * 32 * E) * (int)sizeof(T);
-      uint4* dst = sh.ring[warp][stage][j];
-      if (at + 16 * lane < stop) copy16(dst + lane, blocks + at + 16 * lane);
-      if (shift != 0 && lane == 0 && at + 512 < stop) copy16(dst + 32, blocks + at + 512);
-    }
+  // piece -> its row's first element; its elements [begin, end)
+  auto row_of = [&](int piece, int& begin, int& end) -> const T* {
+    const int row = piece / p.splits, split = piece - row * p.splits;
+    const int seq = row / p.rows_per_seq, beam = row - seq * p.rows_per_seq;
+    begin = split * p.chunk;
+    end = min(p.vocab, begin + p.chunk);
+    return (const T*)p.logits + seq * p.ld_seq + beam * p.ld_beam;
   };
+  // ---- copies ahead
+  constexpr int MIX = J == 4 ? 3 : 0;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sh.ring[warp]) + (lane ^ (lane >> 3 & MIX)) * 16;
+  uint32_t to = ring;
+  int next = blockIdx.x, tiles = 0, left = 0;  // the piece, tiles of it to copy, bytes from this lane's block on
+  bool tail = false;                           // a block more: the row is not aligned
+  const char* block = nullptr;
+  auto copy = [&]() {
+    if (tiles == 0 && next < p.pieces_n) {
+      int begin, end;
+      const T* x = row_of(next, begin, end);
+      const int shift = (int)((uintptr_t)x & 15), skip = (warp * 32 * J + lane) * 16;
+      tail = shift != 0 && lane == 0;
+      block = (const char*)(x + begin) - shift + skip;
+      left = shift + (end - begin) * (int)sizeof(T) - skip;
+      tiles = (end - begin + TILE - 1) / TILE;
+      next += gridDim.x;
+    }
+    if (tiles > 0) {
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    if (begin + s * TILE < end) copy(begin + s * TILE, s);
+      for (int j = 0; j < J; ++j)
+        if (j * 512 < left) copy16(to + j * 512, block + j * 512);
+      if (tail && J * 512 < left) copy16(to + J * 512, block + J * 512);
+      block += TILE * sizeof(T);
+      left -= TILE * (int)sizeof(T);
+      to = to == ring + (kStages - 1) * SPAN * 16 ? ring : to + SPAN * 16;
+      --tiles;
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  float best = -INFINITY;                    // this lane's largest so far
-  float ref = -INFINITY, far = 0.f;          // far: beyond it the reference has to move
-  float bound = 0.f;                         // what is below it is no candidate
-  uint32_t floor2 = 0;
-  float sum = 0.f, low = 0.f;                // sum + low
+  };
+#pragma unroll 1
+  for (int s = 0; s < kStages - 1; ++s) copy();
+  u64* notes = sh.notes[warp];
   int stage = 0;
-  for (int base = begin; base < end; base += TILE) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    __syncwarp();
-    Vec<T> now[J];
-    const int vecs = min(J, (end - base + STEP - 1) / STEP);  // of the tile
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint4* src = sh.ring[warp][stage][j] + lane;
-      const uint4 a = src[0];
-      if (shift == 0) {
-        now[j].w[0] = a.x; now[j].w[1] = a.y; now[j].w[2] = a.z; now[j].w[3] = a.w;
-      } else {
-        now[j].from(a, src[1], shift);
-      }
-    }
-    if (base + TILE > end) {
-#pragma unroll
-      for (int j = 0; j < J; ++j) now[j].keep(end - (base + (j * kThreads + (int)threadIdx.x) * E));
-    }
-    __syncwarp();  // the stage before this one has been read
-    if (base + (kStages - 1) * TILE < end) copy(base + (kStages - 1) * TILE, stage == 0 ? kStages - 1 : stage - 1);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (++stage == kStages) stage = 0;
-    float vmax[J], most = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      vmax[j] = now[j].most();
-      most = fmaxf(most, vmax[j]);
-    }
-    best = fmaxf(best, most);
-    auto publish = [&]() {  // the warp's share of the bound
-      const float v = warp < voters ? nth_lane(best, q) : INFINITY;
+#pragma unroll 1
+  for (int piece = blockIdx.x; piece < p.pieces_n; piece += gridDim.x) {
+    int begin, end;
+    const T* x = row_of(piece, begin, end);
+    const int shift = (int)((uintptr_t)x & 15);
+    // Warps whose lanes all have an element in the first tile have a say in the bound: the q-th largest of
+    // each one's lanes, and of these the s-th largest
+    const int voters = min(kWarps, (end - begin + L - 1) / (32 * L)), some = max(1, (3 * voters) / 4);
+    const int q = voters ? (p.k + some - 1) / some : 64, nth = (p.k + q - 1) / q;
+    int noted = 0;                               // by this lane
+    int seen = 0, due = 2;                       // tiles
+    typename Vec<T>::Most best = Vec<T>::kNone;  // this lane's largest so far
+    float ref = -INFINITY, far = 0.f;            // far: beyond it the reference has to move
+    float bound = 0.f;                           // what is below it is no candidate
+    float sum = 0.f, low = 0.f;                  // sum + low
+    auto publish = [&]() {
+      const float v = warp < voters ? nth_lane(Vec<T>::value(best), q) : -INFINITY;
       if (lane == 0) wbound[warp] = v;
     };
-    auto read_bound = [&]() {
-      float v = voters ? INFINITY : -INFINITY;
+#pragma unroll 1
+    for (int base = begin; base < end; base += TILE) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();
+      Vec<T> now[J];
+      const uint4* src = sh.ring[warp][stage] + lane * J;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v = fminf(v, wbound[w]);
-      return v;
-    };
-    if (base == begin) {
-      publish();
-      const float v = warp_max(best);
-      if (lane == 0) wmax[warp] = v;
-      __syncthreads();
-      bound = read_bound();
-      ref = wmax[0];
+      for (int j = 0; j < J; ++j) {
+        const uint4 a = src[j ^ (lane >> 1 & MIX)];
+        now[j].w[0] = a.x; now[j].w[1] = a.y; now[j].w[2] = a.z; now[j].w[3] = a.w;
+      }
+      if (shift != 0) {
+        const uint4 behind = src[J + (lane == 31 ? 0 : (lane + 1) >> 1 & MIX)];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) ref = fmaxf(ref, wmax[w]);
-      far = ref + kFar;  // (minus infinity: no finite logit yet)
-      floor2 = Vec<T>::floor_of(ref);
-    }
-    if (__any_sync(0xffffffffu, most >= bound || most > far || most == INFINITY)) {
-      if (base != begin && __popc(__ballot_sync(0xffffffffu, most >= bound)) >= 4) {
+        for (int j = 0; j < J; ++j) {
+          const Vec<T>& b = now[(j + 1) % J];
+          now[j].from(make_uint4(now[j].w[0], now[j].w[1], now[j].w[2], now[j].w[3]),
+                      j + 1 < J ? make_uint4(b.w[0], b.w[1], b.w[2], b.w[3]) : behind, shift);
+        }
+      }
+      const int run = end - (base + (int)threadIdx.x * L);  // elements of this lane's run
+      if (base + TILE > end) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) now[j].keep(run - j * E);
+      }
+      __syncwarp();  // the stage before this one has been read
+      copy();
+      if (++stage == kStages) stage = 0;
+      typename Vec<T>::Most lots = now[0].most();
+#pragma unroll
+      for (int j = 1; j < J; ++j) lots = Vec<T>::larger(lots, now[j].most());
+      best = Vec<T>::larger(best, lots);
+      const float most = Vec<T>::value(lots);
+      if (base == begin) {
+        publish();
+        const float v = warp_max(most);
+        if (lane == 0) wmax[warp] = v;
+        __syncthreads();
+        bound = nth_of(wbound, voters, nth);
+        ref = wmax[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) ref = fmaxf(ref, wmax[w]);
+        far = ref + kFar;  // (minus infinity: no finite logit yet)
+      }
+      if (seen == due) {  // after 2, 6, 14, .. tiles: a better bound
         publish();
         __syncwarp();
-        bound = fmaxf(bound, read_bound());
+        bound = fmaxf(bound, nth_of(wbound, voters, nth));
+        due = 2 * due + 2;
       }
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        unsigned who = __ballot_sync(0xffffffffu, j < vecs && vmax[j] >= bound);
-        if (who == 0) continue;
-        if (noted + __popc(who) > kNotes) {
-          cut_warp_list<kNotes>(notes, noted, p.k);
-          noted = p.k;
-          // later vectors have to be above the last one kept
-          bound = fmaxf(bound, float_of((uint32_t)(notes[p.k - 1] >> 32) + 1));
-          who = __ballot_sync(0xffffffffu, j < vecs && vmax[j] >= bound);
+      ++seen;
+      if (most >= bound && run > 0) notes[32 * noted++ + lane] = entry_of(most, (base - begin) / L + threadIdx.x);
+      if (__any_sync(0xffffffffu, noted == kSlots || most > far || most == INFINITY)) {
+        if (__any_sync(0xffffffffu, noted == kSlots)) {
+          publish();
+          __syncwarp();
+          const Cleared c = clear_notes(notes, noted, p.k, fmaxf(bound, nth_of(wbound, voters, nth)));
+          bound = c.bound;
+          noted = c.of_lane;
         }
-        if (who >> lane & 1)
-          notes[noted + __popc(who & ((1u << lane) - 1))] =
-              entry_of(vmax[j], (base - begin + j * STEP) / E + threadIdx.x);
-        noted += __popc(who);
-      }
-      // ---- the reference
-      if (__any_sync(0xffffffffu, most > far || most == INFINITY)) {
-        const float top = warp_max(most);
-        if (top == INFINITY) {
-          sum = NAN;
-        } else {
-          const float k = ref == -INFINITY ? 1.f : expf(ref - top);
-          sum *= k;
-          low *= k;
-          floor2 = Vec<T>::floor_of(top);
-        }
-        ref = top;
-        far = ref + kFar;
-      }
-    }
-    // ---- the sum
-    float2 acc = make_float2(0.f, 0.f), acc2 = acc, rest = acc;
-    if (ref > kLowest && ref != INFINITY) {
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        if (j >= vecs) continue;
-#pragma unroll
-        for (int i = 0; i < E; i += 4) {
-          add_exp(now[j].below(i, ref, floor2), acc, rest);
-          add_exp(now[j].below(i + 2, ref, floor2), acc2, rest);
+        // ---- the reference
+        if (__any_sync(0xffffffffu, most > far || most == INFINITY)) {
+          const float top = warp_max(most);
+          if (top == INFINITY) {
+            sum = NAN;
+          } else if (ref != -INFINITY) {
+            const float k = expf(ref - top);
+            sum *= k;
+            low *= k;
+          }
+          ref = top;
+          far = ref + kFar;
         }
       }
-    } else {  // nothing yet, or nothing but the lowest value (and a row with infinity has its NaN)
+      // ---- the sum (no finite logit yet: of zeros)
+      const float from = ref == -INFINITY ? 0.f : ref;
+      const float2 minus = make_float2(-from, -from);
+      float2 acc = make_float2(0.f, 0.f), acc2 = acc;
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const float v = now[j].at(i);
-          if (j < vecs) acc.x += v == ref && ref != -INFINITY ? 1.f : isnan(v) ? v : 0.f;
+        for (int i = 0; i < E; i += 4) {
+          acc = __fadd2_rn(acc, exp_of(__fadd2_rn(make_float2(now[j].at(i), now[j].at(i + 1)), minus)));
+          acc2 = __fadd2_rn(acc2, exp_of(__fadd2_rn(make_float2(now[j].at(i + 2), now[j].at(i + 3)), minus)));
         }
+      const float tile = (acc.x + acc.y) + (acc2.x + acc2.y);
+      const float s = sum + tile, t = s - sum;  // and the rounding error of s
+      low += (sum - (s - t)) + (tile - t);
+      sum = s;
     }
-    const float tile = fmaf(rest.x + rest.y, kLn2, (acc.x + acc.y) + (acc2.x + acc2.y));
-    const float s = sum + tile, t = s - sum;  // and the rounding error of s
-    low += (sum - (s - t)) + (tile - t);
-    sum = s;
-  }
-  // ---- elements of the noted vectors, against the last bound; the warps' lists become one
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  if (begin < end) {
-    const float v = warp < voters ? nth_lane(best, q) : INFINITY;
+    // ---- elements of the noted runs, against the last bound; the warps' lists become one
+    publish();
+    if (lane == 0) wmax[warp] = ref;
+    __syncthreads();
+    bound = fmaxf(bound, nth_of(wbound, voters, nth));
+    float top = wmax[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, wmax[w]);
+    const int count = enter<T, L>(x, begin, end, notes, noted, sh.entries[warp], p.k, bound);
+    double d = (double)sum + (double)low;
+    if (ref != top && ref != -INFINITY) {  // (d is below e^-40 of the whole where that is the limit)
+      const float2 w = exp_pair(fmaxf(ref - top, -80.f));
+      d *= (double)w.x + (double)w.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     if (lane == 0) {
-      wbound[warp] = v;
-      wmax[warp] = ref;
+      sh.wsum[warp] = d;
+      sh.wcount[warp] = count;
     }
-  } else if (lane == 0) {
-    wbound[warp] = wmax[warp] = -INFINITY;
-  }
-  if (threadIdx.x == 0) sh.count = 0;
-  __syncthreads();  // (and the ring is free)
-  float top = wmax[0], last = voters ? INFINITY : -INFINITY;
+    __syncthreads();
+    // ---- ranks among all warps' entries
+    int n = 0, in = 0, of = 0;  // all; this thread's place in warp `of`'s list
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    top = fmaxf(top, wmax[w]);
-    last = fminf(last, wbound[w]);
-  }
-  u64* mine = reinterpret_cast<u64*>(sh.ring[warp]);  // kEntries of them, then all warps' k each
-  static_assert(sizeof(sh.ring[0]) >= kEntries * sizeof(u64) && sizeof(sh.ring) >= kWarps * kBeamMax * sizeof(u64), "ring");
-  const int count = enter<T>(x, begin, end, notes, noted, mine, p.k, last);
-  u64 held[kBeamMax / 32];
-#pragma unroll
-  for (int t = 0; t < kBeamMax / 32; ++t) held[t] = lane + 32 * t < count ? mine[lane + 32 * t] : 0;
-  int place = 0;
-  if (lane == 0 && count) place = atomicAdd(&sh.count, count);
-  place = __shfl_sync(0xffffffffu, place, 0);
-  __syncthreads();
-  u64* list = reinterpret_cast<u64*>(sh.ring);
-#pragma unroll
-  for (int t = 0; t < kBeamMax / 32; ++t)
-    if (lane + 32 * t < count) list[place + lane + 32 * t] = held[t];
-  double d = (double)sum + (double)low;
-  if (ref != top && ref != -INFINITY) d *= exp((double)ref - (double)top);  // (far apart: rare)
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  if (lane == 0) wsum[warp] = d;
-  __syncthreads();
-  const int n = sh.count;
-  const size_t piece = ((size_t)seq * p.rows_per_seq + beam) * p.splits + split;
-  u64* out = p.lists + piece * p.k;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const u64 e = list[i];
-    const int r = rank_of(list, n, e);
-    if (r < p.k) out[r] = e;
-  }
-  for (int i = n + threadIdx.x; i < p.k; i += kThreads) out[i] = 0;
-  if (threadIdx.x == 0) {
-    d = wsum[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) d += wsum[w];
-    p.pieces[piece] = {d, top, 0};
+    for (int w = 0; w < kWarps; ++w) {
+      if ((int)threadIdx.x >= n) in = threadIdx.x - n, of = w;
+      n += sh.wcount[w];
+    }
+    u64* out = p.lists + (size_t)piece * p.k;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      while (in >= sh.wcount[of]) in -= sh.wcount[of++];
+      const u64 e = sh.entries[of][in];
+      int r = 0;
+#pragma unroll 1
+      for (int w = 0; w < kWarps; ++w) r += rank_of(sh.entries[w], sh.wcount[w], e);
+      if (r < p.k) out[r] = e;
+      in += kThreads;
+    }
+    for (int i = n + threadIdx.x; i < p.k; i += kThreads) out[i] = 0;
+    if (threadIdx.x == 0) {
+      d = sh.wsum[0];
+#pragma unroll 1
+      for (int w = 1; w < kWarps; ++w) d += sh.wsum[w];
+      p.pieces[piece] = {d, top, 0};
+    }
   }
 }
 
@@ -568,7 +610,7 @@ struct Ranked {
 constexpr int kMergeThreads = 512;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMostRough = 16384;  // candidates of a sequence (kBeamMax beams of as many)
-constexpr int kCounts = 64;
+constexpr int kBins = 256, kFirstBin = 117 << 3;  // distances from 2^-10 to 2^22
 
 // Entry i's place among n by `parts` neighbouring lanes (a power of two), all of which get it.
 __device__ __forceinline__ int rank_of(const Ranked& l, int n, u64 score, uint32_t place, int parts) {
@@ -606,19 +648,19 @@ __device__ __noinline__ void cut_ranked(Ranked& l, int k) {
 }
 
 // A CTA per sequence. Few thousand candidates at most, so that latencies count: scores in 32 bits lie in
-// shared memory, a handful of counts finds a threshold that between k and about 2 k of them reach, and
-// these alone are scored in 64 bits and ranked, by counting those before each.
+// shared memory, a histogram gives a threshold that between k and about 2 k of them reach, and these
+// alone are scored in 64 bits and ranked, by counting those before each.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p) {
   extern __shared__ float rough[];  // [beams * splits * k]
   __shared__ Ranked list;
   __shared__ double lse[kBeamMax], shift[kBeamMax];  // log of the row's sum under m; m
   __shared__ float4 beam_s[kBeamMax];                // score, log sum and m in 32 bits, or NaN
   __shared__ int spread_s;                           // largest |score| + |log sum| of a beam, as bits
-  __shared__ int counts[kCounts];
+  __shared__ int bins[kBins], bin_s;
   __shared__ float top_s[kMergeWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
   if (threadIdx.x == 0) list.count = spread_s = 0;
-  if (threadIdx.x < kCounts) counts[threadIdx.x] = 0;
+  if (threadIdx.x < kBins) bins[threadIdx.x] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the scan's lists
   const int per = p.splits * p.k;
   const u64* lists = p.lists + (size_t)b * p.rows_per_seq * per;
@@ -640,11 +682,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p
       double part = j == 0 ? c.sum : 0.0;
       if (e != 0) {
         const float d = logit_of(e) - c.ref;
-        float2 a = make_float2(0.f, 0.f), b2 = a;
-        add_exp(make_float2(max_nan(d, kDeep), kDeep), a, b2);
-        if ((double)a.x * 16.0 > c.sum) {
+        const float a = exp_of(make_float2(d, d)).x;
+        if ((double)a * 16.0 > c.sum) {
           const float2 t = exp_pair(d);
-          part += ((double)t.x - (double)a.x) + (double)(t.y - b2.x * kLn2);
+          part += ((double)t.x - (double)a) + (double)t.y;
         }
       }
       if (c.ref != -INFINITY && under != 0.f) {
@@ -691,39 +732,35 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, top_s[w]);
-  // ---- the threshold
-  int tries = 0;
-  auto count = [&](float t) -> int {  // (at most kCounts times)
-    int n = 0;
-#pragma unroll 4
-    for (int c = threadIdx.x; c < total; c += kMergeThreads) n += rough[c] >= t;
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0 && n) atomicAdd(&counts[tries], n);
-    __syncthreads();
-    return counts[tries++];
-  };
-  float high = INFINITY, bound = -INFINITY;  // fewer than k reach `high`, k or more the bound
+  // ---- the threshold, from the numbers of candidates by their distance from the best, eight bins an
+  // octave: the end of the bin that holds the k-th
+  float bound = -INFINITY;
   if (top != -INFINITY) {
-    float d = 0.5f;
-    for (; d < 1e30f; d *= 4.f) {  // 51 counts at most, and 8
-      const float t = top - d;
-      const int n = count(t);
-      if (n >= p.k) {
-        bound = t;
-        for (int i = 0, have = n; i < 8 && have > 2 * p.k + 16; ++i) {
-          const float mid = high == INFINITY ? 0.5f * (top + bound) : 0.5f * (high + bound);
-          const int c = count(mid);
-          if (c >= p.k) {
-            bound = mid;
-            have = c;
-          } else {
-            high = mid;
-          }
-        }
-        break;
-      }
-      high = t;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < total; c += kMergeThreads) {
+      const float v = rough[c];
+      if (v == v) atomicAdd(&bins[min(max((int)(__float_as_uint(top - v) >> 20) - kFirstBin, 0), kBins - 1)], 1);
     }
+    __syncthreads();
+    if (warp == 0) {
+      int n[kBins / 32], mine = 0;
+#pragma unroll
+      for (int i = 0; i < kBins / 32; ++i) mine += n[i] = bins[lane * (kBins / 32) + i];
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      const int l = __ffs(__ballot_sync(0xffffffffu, upto >= p.k)) - 1;  // (there are k candidates)
+      if (lane == l) {
+        int have = upto - mine, i = 0;
+        while (i < kBins / 32 - 1 && have + n[i] < p.k) have += n[i++];
+        bin_s = lane * (kBins / 32) + i;
+      }
+    }
+    __syncthreads();
+    if (bin_s < kBins - 1) bound = top - __uint_as_float((uint32_t)(bin_s + 1 + kFirstBin) << 20);
   }
   // a rough score is off by eight roundings of |score|, |logit - m| and |log sum| at most
   const float slack = (2.f * __int_as_float(spread_s) + fabsf(bound) + fabsf(top)) * 9.6e-7f;
@@ -783,27 +820,39 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p
   }
 }
 
-// Pieces of a row: enough CTAs to fill the GPU four times over, none below 2048 logits, and no more
-// candidates of a sequence than the merge holds.
-int splits_of(int rows, int beams, int vocab, int k) {
-  const int most = (vocab + 2047) / 2048, fit = kMostRough / 2 / (beams * k);
-  const long long want = (4LL * chunk_sms() + rows - 1) / rows;
-  const int s = (int)(want > most ? most : want), t = s > fit ? fit : s;
-  return t < 1 ? 1 : t;
+constexpr int kCtas = 3;  // of the scan, per SM
+
+// How rows are cut. A piece costs the loads of its elements and about as much again as 8 K of them
+// for its start and end; CTAs take pieces in turns. More pieces are more candidates for the merge, which
+// holds kMostRough of a sequence.
+struct Cut {
+  int splits, chunk;  // pieces of a row, and elements of a piece (whole runs of every thread)
+};
+Cut cut_of(int rows, int beams, int vocab, int k) {
+  constexpr int UNIT = kThreads * 8;
+  const int slots = kCtas * chunk_sms(), units = (vocab + UNIT - 1) / UNIT, fit = kMostRough / 2 / (beams * k);
+  Cut best = {1, units * UNIT};
+  double least = 1e300;
+  for (int s = 1; s <= units && (s == 1 || s <= fit) && (long long)rows * (s - 1) < 8LL * slots; ++s) {
+    const int per = (units + s - 1) / s, n = (units + per - 1) / per;
+    const long long turns = ((long long)rows * n + slots - 1) / slots;
+    const double cost = (double)turns * (per + 4) + (double)beams * n * k / 512.;
+    if (cost < least) {
+      least = cost;
+      best = {n, per * UNIT};
+    }
+  }
+  return best;
 }
 
-// Whole vectors of every thread (of either type), where the row has that many.
-int chunk_of(int splits, int vocab) {
-  const int per = (vocab + splits - 1) / splits;
-  return (per + kThreads * 8 - 1) / (kThreads * 8) * (kThreads * 8);
-}
-
-template <typename T>
-cudaError_t scan_rows(const Scan& p, dim3 grid, cudaStream_t s) {
+template <typename T, int J>
+cudaError_t scan_rows(const Scan& p, cudaStream_t s) {
   static SmemLimit limit;
-  cudaError_t e = limit.raise(beam_scan_kernel<T>, (int)sizeof(ScanSmem));
+  cudaError_t e = limit.raise(beam_scan_kernel<T, J>, (int)sizeof(ScanSmem<J>));
   if (e != cudaSuccess) return e;
-  beam_scan_kernel<T><<<grid, kThreads, sizeof(ScanSmem), s>>>(p);
+  LaunchScope ls_(DFLASH_KERNEL_BEAM_SCAN, s);
+  const int slots = kCtas * chunk_sms();
+  beam_scan_kernel<T, J><<<p.pieces_n < slots ? p.pieces_n : slots, kThreads, sizeof(ScanSmem<J>), s>>>(p);
   return cudaGetLastError();
 }
 
@@ -815,7 +864,7 @@ struct Carved {
 Carved carve(Carver& cv, int batch, int beams, int vocab, int k) {
   size_t pieces = 0;
   for (int rows : {batch, batch * beams}) {  // a shared row per sequence, or one per beam
-    const size_t n = (size_t)rows * splits_of(rows, beams, vocab, k);
+    const size_t n = (size_t)rows * cut_of(rows, beams, vocab, k).splits;
     pieces = n > pieces ? n : pieces;
   }
   Carved c;
@@ -836,23 +885,19 @@ cudaError_t beam_select(int dtype, const BeamParams& a, cudaStream_t s) {
   Carver cv(a.workspace, ~size_t(0));
   const Carved c = carve(cv, a.batch, a.beams, a.vocab, a.k);
   const int per_seq = a.ld_beam == 0 ? 1 : a.beams, rows = a.batch * per_seq;
-  const int splits = splits_of(rows, a.beams, a.vocab, a.k);
-  const Scan scan = {a.logits, a.ld_seq, a.ld_beam, c.lists, c.pieces, a.vocab, per_seq, splits, chunk_of(splits, a.vocab), a.k};
-  {
-    LaunchScope ls_(DFLASH_KERNEL_BEAM_SCAN, s);
-    const dim3 grid(a.batch, per_seq, splits);
-    cudaError_t e;
-    if (dtype == DFLASH_F32)
-      e = scan_rows<float>(scan, grid, s);
-    else
-      e = scan_rows<bf16>(scan, grid, s);
-    if (e != cudaSuccess) return e;
-  }
+  const Cut cut = cut_of(rows, a.beams, a.vocab, a.k);
+  const int splits = cut.splits;
+  const Scan scan = {a.logits, a.ld_seq, a.ld_beam, c.lists, c.pieces, a.vocab, per_seq, splits, cut.chunk, a.k, rows * splits};
+  // short pieces: 16 bytes a lane and tile, so that more lanes have some
+  const bool fine = cut.chunk <= kThreads * 16;
+  cudaError_t e = dtype == DFLASH_F32 ? (fine ? scan_rows<float, 1>(scan, s) : scan_rows<float, 4>(scan, s))
+                        : (fine ? scan_rows<bf16, 1>(scan, s) : scan_rows<bf16, 4>(scan, s));
+  if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_BEAM_MERGE, s);
   const Merge merge = {c.lists, c.pieces, a.scores, a.tokens, a.parents, a.scores_out, a.ld_out,
                        a.beams, per_seq, splits, a.k, a.vocab, a.parent_base};
   static SmemLimit limit;
-  cudaError_t e = limit.raise(beam_merge_kernel, (int)sizeof(float) * kMostRough);
+  e = limit.raise(beam_merge_kernel, (int)sizeof(float) * kMostRough);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.batch);

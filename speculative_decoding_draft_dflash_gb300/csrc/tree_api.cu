@@ -132,7 +132,7 @@ namespace {
 dflash_status check_beams(int batch, int beams, int vocab, int k) {
   if (batch <= 0 || beams <= 0 || vocab <= 0 || k <= 0) return DFLASH_ERR_INVALID_ARG;
   if ((long long)beams * vocab < k) return DFLASH_ERR_INVALID_ARG;
-  if (beams > kBeamMax || k > kBeamMax || (long long)beams * vocab > 0x7fffffffll ||
+  if (beams > kBeamMax || k > kBeamMax || (long long)beams * vocab > 0x7fffffffll || vocab > (1 << 28) ||
       (long long)batch * beams > (1 << 20))
     return DFLASH_ERR_UNSUPPORTED;
   return DFLASH_OK;
