@@ -354,6 +354,18 @@ __device__ __noinline__ float nth_of(const volatile float* value, int n, int nth
   return who ? __shfl_sync(0xffffffffu, mine, __ffs(who) - 1) : -INFINITY;
 }
 
+// Sums of (hi, lo) pairs, with the roundings of hi kept in lo.
+__device__ __forceinline__ float2 add_pairs(float2 a, float2 b) {
+  const float s = a.x + b.x, t = s - a.x;
+  return make_float2(s, (a.y + b.y) + ((a.x - (s - t)) + (b.x - t)));
+}
+__device__ __forceinline__ float2 sum_lanes(float2 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = add_pairs(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+  return v;
+}
+
 constexpr int kStages = 3;   // tiles of a warp on their way or in use
 
 // J: 16-byte blocks of a lane and tile.
@@ -362,8 +374,8 @@ struct ScanSmem {
   uint4 ring[kWarps][kStages][32 * J + 1];  // (one block more for rows that are not aligned)
   u64 notes[kWarps][32 * kSlots];
   u64 entries[kWarps][kEntries];
-  double wsum[kWarps];
-  float wbound[kWarps], wmax[kWarps];
+  float2 wsum[kWarps];
+  float wbound[kWarps], wmax[kWarps], wref[kWarps];
   int wcount[kWarps];
 };
 
@@ -532,24 +544,17 @@ __global__ void __launch_bounds__(kThreads, 3) beam_scan_kernel(const Scan p) {
       low += (sum - (s - t)) + (tile - t);
       sum = s;
     }
-    // ---- elements of the noted runs, against the last bound; the warps' lists become one
-    publish();
-    if (lane == 0) wmax[warp] = ref;
-    __syncthreads();
-    bound = fmaxf(bound, nth_of(wbound, voters, nth));
-    float top = wmax[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, wmax[w]);
-    const int count = enter<T, L>(x, begin, end, notes, noted, sh.entries[warp], p.k, bound);
-    double d = (double)sum + (double)low;
-    if (ref != top && ref != -INFINITY) {  // (d is below e^-40 of the whole where that is the limit)
-      const float2 w = exp_pair(fmaxf(ref - top, -80.f));
-      d *= (double)w.x + (double)w.y;
+    if (seen > 1) {  // (one tile: it is the bound of all)
+      publish();
+      __syncwarp();
+      bound = fmaxf(bound, nth_of(wbound, voters, nth));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    // ---- elements of the noted runs that reach the bound
+    const int count = enter<T, L>(x, begin, end, notes, noted, sh.entries[warp], p.k, bound);
+    const float2 part = sum_lanes(make_float2(sum, low));
     if (lane == 0) {
-      sh.wsum[warp] = d;
+      sh.wsum[warp] = part;
+      sh.wref[warp] = ref;
       sh.wcount[warp] = count;
     }
     __syncthreads();
@@ -571,11 +576,16 @@ __global__ void __launch_bounds__(kThreads, 3) beam_scan_kernel(const Scan p) {
       in += kThreads;
     }
     for (int i = n + threadIdx.x; i < p.k; i += kThreads) out[i] = 0;
-    if (threadIdx.x == 0) {
-      d = sh.wsum[0];
-#pragma unroll 1
-      for (int w = 1; w < kWarps; ++w) d += sh.wsum[w];
-      p.pieces[piece] = {d, top, 0};
+    if (warp == kWarps - 1) {  // the warps' sums (the first ones are busy with ranks)
+      const float mine = lane < kWarps ? sh.wref[lane] : -INFINITY, top = warp_max(mine);
+      float2 v = lane < kWarps ? sh.wsum[lane] : make_float2(0.f, 0.f);
+      if (mine != top && mine != -INFINITY) {
+        const float2 w = exp_pair(fmaxf(mine - top, -80.f));
+        const float q = v.x * w.x;
+        v = mine - top < -80.f ? make_float2(0.f, 0.f) : make_float2(q, fmaf(v.x, w.x, -q) + (v.x * w.y + v.y * w.x));
+      }
+      v = sum_lanes(v);
+      if (lane == 0) p.pieces[piece] = {(double)v.x + (double)v.y, top, 0};
     }
   }
 }
@@ -607,8 +617,6 @@ struct Ranked {
   int count;
 };
 
-constexpr int kMergeThreads = 512;
-constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMostRough = 16384;  // candidates of a sequence (kBeamMax beams of as many)
 constexpr int kBins = 256, kFirstBin = 117 << 3;  // distances from 2^-10 to 2^22
 
@@ -623,14 +631,15 @@ __device__ __forceinline__ int rank_of(const Ranked& l, int n, u64 score, uint32
 }
 
 // Cuts the list to its k best, best first.
+template <int THREADS>
 __device__ __noinline__ void cut_ranked(Ranked& l, int k) {
   const int n = min(l.count, kMergeCap);
-  u64 mine[kMergeCap / kMergeThreads];
-  uint32_t at[kMergeCap / kMergeThreads];
-  int rank[kMergeCap / kMergeThreads];
+  u64 mine[kMergeCap / THREADS];
+  uint32_t at[kMergeCap / THREADS];
+  int rank[kMergeCap / THREADS];
 #pragma unroll
-  for (int t = 0; t < kMergeCap / kMergeThreads; ++t) {
-    const int i = threadIdx.x + t * kMergeThreads;
+  for (int t = 0; t < kMergeCap / THREADS; ++t) {
+    const int i = threadIdx.x + t * THREADS;
     mine[t] = i < n ? l.score[i] : 0;
     at[t] = i < n ? l.place[i] : 0;
     rank[t] = rank_of(l, n, mine[t], at[t], 1);
@@ -638,7 +647,7 @@ __device__ __noinline__ void cut_ranked(Ranked& l, int k) {
   }
   __syncthreads();
 #pragma unroll
-  for (int t = 0; t < kMergeCap / kMergeThreads; ++t)
+  for (int t = 0; t < kMergeCap / THREADS; ++t)
     if (rank[t] < k) {
       l.score[rank[t]] = mine[t];
       l.place[rank[t]] = at[t];
@@ -650,17 +659,19 @@ __device__ __noinline__ void cut_ranked(Ranked& l, int k) {
 // A CTA per sequence. Few thousand candidates at most, so that latencies count: scores in 32 bits lie in
 // shared memory, a histogram gives a threshold that between k and about 2 k of them reach, and these
 // alone are scored in 64 bits and ranked, by counting those before each.
-__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) beam_merge_kernel(const Merge p) {
+  constexpr int WARPS = THREADS / 32;
   extern __shared__ float rough[];  // [beams * splits * k]
   __shared__ Ranked list;
   __shared__ double lse[kBeamMax], shift[kBeamMax];  // log of the row's sum under m; m
   __shared__ float4 beam_s[kBeamMax];                // score, log sum and m in 32 bits, or NaN
   __shared__ int spread_s;                           // largest |score| + |log sum| of a beam, as bits
   __shared__ int bins[kBins], bin_s;
-  __shared__ float top_s[kMergeWarps];
+  __shared__ float top_s[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
   if (threadIdx.x == 0) list.count = spread_s = 0;
-  if (threadIdx.x < kBins) bins[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < kBins; i += THREADS) bins[i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the scan's lists
   const int per = p.splits * p.k;
   const u64* lists = p.lists + (size_t)b * p.rows_per_seq * per;
@@ -668,7 +679,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p
   // ---- a row's sum, a warp per row. Terms above 1/16 of it among the pieces' first are taken again: the
   // scan's are off by up to 2^-22
   const int first = p.splits < 32 ? min(p.k, 32 / p.splits) : 1;  // looked at, of each piece
-  for (int r = warp; r < p.rows_per_seq; r += kMergeWarps) {
+  for (int r = warp; r < p.rows_per_seq; r += WARPS) {
     const Piece* pc = pieces + r * p.splits;
     float m = -INFINITY;
     for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, pc[s].ref);
@@ -703,7 +714,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < p.beams; i += kMergeThreads) {
+  for (int i = threadIdx.x; i < p.beams; i += THREADS) {
     const int r = p.rows_per_seq == 1 ? 0 : i;
     const float s = p.scores ? p.scores[(size_t)b * p.beams + i] : 0.f, z = (float)lse[r];
     const bool alive = isfinite(s) && !isnan(z);
@@ -718,7 +729,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p
   auto beam_of = [&](int c) { return (int)(((float)c + 0.5f) * inv); };  // (c < 2^14: exact)
   float top = -INFINITY;
 #pragma unroll 4
-  for (int c = threadIdx.x; c < total; c += kMergeThreads) {
+  for (int c = threadIdx.x; c < total; c += THREADS) {
     const int beam = beam_of(c), i = c - beam * per;
     const u64 x = lists[p.rows_per_seq == 1 ? i : c];
     const float4 of = beam_s[beam];
@@ -731,13 +742,13 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p
   if (lane == 0) top_s[warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, top_s[w]);
+  for (int w = 0; w < WARPS; ++w) top = fmaxf(top, top_s[w]);
   // ---- the threshold, from the numbers of candidates by their distance from the best, eight bins an
   // octave: the end of the bin that holds the k-th
   float bound = -INFINITY;
   if (top != -INFINITY) {
 #pragma unroll 4
-    for (int c = threadIdx.x; c < total; c += kMergeThreads) {
+    for (int c = threadIdx.x; c < total; c += THREADS) {
       const float v = rough[c];
       if (v == v) atomicAdd(&bins[min(max((int)(__float_as_uint(top - v) >> 20) - kFirstBin, 0), kBins - 1)], 1);
     }
@@ -768,7 +779,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p
   // ---- exact scores of what reaches it
   u64 least = 0;
   uint32_t least_place = 0xffffffffu;
-  for (int base = 0; base < total; base += kMergeThreads) {
+  for (int base = 0; base < total; base += THREADS) {
     const int c = base + threadIdx.x;
     bool todo = c < total && rough[c] >= bound;
     u64 key = 0;
@@ -799,15 +810,17 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p
       }
       more = __syncthreads_or(todo);
       if (more) {
-        cut_ranked(list, p.k);
+        cut_ranked<THREADS>(list, p.k);
         least = list.score[p.k - 1];  // (a full list has k entries)
         least_place = list.place[p.k - 1];
       }
     } while (more);
   }
   // ---- ranks
-  const int n = min(list.count, kMergeCap), parts = n <= 64 ? 8 : n <= 128 ? 4 : n <= 256 ? 2 : 1;
-  for (int i = threadIdx.x / parts; i < (n + 31) / 32 * 32; i += kMergeThreads / parts) {
+  const int n = min(list.count, kMergeCap);
+  int parts = 1;
+  while (2 * parts * n <= THREADS && parts < 8) parts *= 2;
+  for (int i = threadIdx.x / parts; i < (n + 31) / 32 * 32; i += THREADS / parts) {
     const u64 score = i < n ? list.score[i] : 0;
     const uint32_t place = i < n ? list.place[i] : 0;
     const int r = rank_of(list, n, score, place, parts);
@@ -822,9 +835,12 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const Merge p
 
 constexpr int kCtas = 3;  // of the scan, per SM
 
-// How rows are cut. A piece costs the loads of its elements and about as much again as 8 K of them
-// for its start and end; CTAs take pieces in turns. More pieces are more candidates for the merge, which
-// holds kMostRough of a sequence.
+// How rows are cut. CTAs take pieces in turns; a piece costs the loads of its elements and about as much
+// again as 54 K of them for its start and end (6 us), and more candidates for the merge, which holds kMostRough
+// of a sequence. Measured, us (pieces a row):
+//   256 rows of 131072, k 16       1: 26.9   2: 32.5   4: 37.8   8: 48.2
+//   16 rows of 131072, k 16        1: 20.8   4: 15.3   8: 14.0  16: 15.2
+//   4 rows of 131072, k 8          1: 19.4   4: 13.6  16: 12.1  32: 12.1
 struct Cut {
   int splits, chunk;  // pieces of a row, and elements of a piece (whole runs of every thread)
 };
@@ -836,7 +852,7 @@ Cut cut_of(int rows, int beams, int vocab, int k) {
   for (int s = 1; s <= units && (s == 1 || s <= fit) && (long long)rows * (s - 1) < 8LL * slots; ++s) {
     const int per = (units + s - 1) / s, n = (units + per - 1) / per;
     const long long turns = ((long long)rows * n + slots - 1) / slots;
-    const double cost = (double)turns * (per + 4) + (double)beams * n * k / 512.;
+    const double cost = (double)turns * (per + 27) + (double)beams * n * k / 128.;
     if (cost < least) {
       least = cost;
       best = {n, per * UNIT};
@@ -854,6 +870,25 @@ cudaError_t scan_rows(const Scan& p, cudaStream_t s) {
   const int slots = kCtas * chunk_sms();
   beam_scan_kernel<T, J><<<p.pieces_n < slots ? p.pieces_n : slots, kThreads, sizeof(ScanSmem<J>), s>>>(p);
   return cudaGetLastError();
+}
+
+template <int THREADS>
+cudaError_t merge_rows(const Merge& p, int batch, cudaStream_t s) {
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(beam_merge_kernel<THREADS>, (int)sizeof(float) * kMostRough);
+  if (e != cudaSuccess) return e;
+  LaunchScope ls_(DFLASH_KERNEL_BEAM_MERGE, s);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(batch);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = sizeof(float) * (size_t)p.beams * p.splits * p.k;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // scheduled as SMs fall free
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, beam_merge_kernel<THREADS>, p);
 }
 
 struct Carved {
@@ -893,23 +928,11 @@ cudaError_t beam_select(int dtype, const BeamParams& a, cudaStream_t s) {
   cudaError_t e = dtype == DFLASH_F32 ? (fine ? scan_rows<float, 1>(scan, s) : scan_rows<float, 4>(scan, s))
                         : (fine ? scan_rows<bf16, 1>(scan, s) : scan_rows<bf16, 4>(scan, s));
   if (e != cudaSuccess) return e;
-  LaunchScope ls_(DFLASH_KERNEL_BEAM_MERGE, s);
   const Merge merge = {c.lists, c.pieces, a.scores, a.tokens, a.parents, a.scores_out, a.ld_out,
                        a.beams, per_seq, splits, a.k, a.vocab, a.parent_base};
-  static SmemLimit limit;
-  e = limit.raise(beam_merge_kernel, (int)sizeof(float) * kMostRough);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.batch);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.dynamicSmemBytes = sizeof(float) * (size_t)a.beams * splits * a.k;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // scheduled as SMs fall free
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, beam_merge_kernel, merge);
+  // Four warps for few candidates of few rows: such sequences are many, and share an SM (2048 rows, greedy: 57 us
+  // with 128 threads, 72 with 512; 64 sequences of 8 beams, k 8: 34 and 31)
+  return per_seq * splits <= 4 && (long long)a.beams * splits * a.k <= 128 ? merge_rows<128>(merge, a.batch, s) : merge_rows<512>(merge, a.batch, s);
 }
 
 }  // namespace dflash
