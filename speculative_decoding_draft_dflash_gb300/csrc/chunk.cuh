@@ -423,34 +423,47 @@ struct Walker {
   }
 };
 
-// Which of the keys k .. k + 31 the node `node` (none: -1) of sequence b's tree sees, as bits.
-// Committed keys by the window alone; keys of the tree by the node's mask, up to its own, and
+// Which of the keys k .. k + 127 the node `node` (none: -1) of sequence b's tree sees, as bits of four
+// words. Committed keys by the window alone; keys of the tree by the node's mask, up to its own, and
 // by the window: a node's position is the committed rows plus its depth. (A window as deep as
-// the node cuts nothing from its tree, so depths are compared where it is not.)
-static __device__ __noinline__ uint32_t tree_bits(const TreeRows& t, int b, int node, int ctx, int k, int window) {
-  if (node < 0) return 0;
-  const int u0 = k - ctx;  // node of bit 0
-  const size_t row = (size_t)b * t.max_nodes;
-  const int depth = window > 0 ? t.depths[row + node] : 0;
-  uint32_t committed = u0 >= 0 ? 0u : u0 <= -32 ? 0xffffffffu : (1u << -u0) - 1u;
-  if (window > 0) {
-    const int l0 = ctx + depth - window + 1 - k;  // the first bit that the window leaves
-    committed &= l0 <= 0 ? 0xffffffffu : l0 > 31 ? 0u : 0xffffffffu << l0;
-  }
-  if (u0 <= -32 || u0 > node) return committed;
-  const int words = t.max_nodes >> 5, i = u0 >> 5;  // (u0 >> 5 is -1 for -31 .. -1)
-  const uint32_t* m = t.masks + (row + node) * words;
-  const uint32_t lo = i >= 0 ? m[i] : 0u, hi = i + 1 < words ? m[i + 1] : 0u;
-  uint32_t bits = __funnelshift_r(lo, hi, u0 & 31);
-  const int last = node - u0;  // >= 0
-  bits &= last >= 31 ? 0xffffffffu : (2u << last) - 1u;
-  if (window > 0 && depth >= window) {
-    for (uint32_t left = bits; left; left &= left - 1) {
-      const int e = __ffs(left) - 1;
-      if (depth - t.depths[row + u0 + e] >= window) bits &= ~(1u << e);
+// the node cuts nothing from its tree, so depths are compared where it is not.) One call for a tile, so
+// that the five words a tile can straddle are loaded at once; not inlined, as the kernels have little
+// room for code.
+static __device__ __noinline__ uint4 tree_bits(const TreeRows& t, int b, int node, int ctx, int k, int window) {
+  uint32_t m[4] = {0, 0, 0, 0};
+  if (node >= 0) {
+    const size_t row = (size_t)b * t.max_nodes;
+    const int u0 = k - ctx, i0 = u0 >> 5;  // node of bit 0; the word it is in (below 0: committed keys)
+    const uint32_t* mask = t.masks + (row + node) * (t.max_nodes >> 5);
+    const int depth = window > 0 ? t.depths[row + node] : 0;
+    uint32_t w[5];
+#pragma unroll
+    for (int c = 0; c < 5; ++c) w[c] = i0 + c >= 0 && 32 * (i0 + c) <= node ? mask[i0 + c] : 0u;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int last = node - u0 - 32 * c;  // bit of the own node
+      m[c] = __funnelshift_r(w[c], w[c + 1], u0 & 31) & (last < 0 ? 0u : last >= 31 ? 0xffffffffu : (2u << last) - 1u);
+    }
+    if (window > 0 && depth >= window) {
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t bits = c == 0 ? m[0] : c == 1 ? m[1] : c == 2 ? m[2] : m[3], keep = bits;
+#pragma unroll 1
+        for (; bits; bits &= bits - 1) {
+          const int e = __ffs(bits) - 1;
+          if (depth - t.depths[row + u0 + 32 * c + e] >= window) keep &= ~(1u << e);
+        }
+        (c == 0 ? m[0] : c == 1 ? m[1] : c == 2 ? m[2] : m[3]) = keep;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int n = -u0 - 32 * c;                                                 // committed keys
+      const int l0 = window > 0 ? ctx + depth - window + 1 - k - 32 * c : 0;      // the first the window leaves
+      m[c] |= (n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u) & (l0 <= 0 ? 0xffffffffu : l0 > 31 ? 0u : 0xffffffffu << l0);
     }
   }
-  return committed | bits;
+  return make_uint4(m[0], m[1], m[2], m[3]);
 }
 
 }  // namespace chunk

@@ -186,8 +186,8 @@ __device__ __forceinline__ void piece(const ChunkAttnParams& p, const chunk::Pie
         }
         if constexpr (TREE) {
           const int node = pos < 0 ? -1 : pos - w.ctx;
-          const uint32_t b0 = chunk::tree_bits(p.tree, w.b, node, w.ctx, k0, p.window);
-          const uint32_t b1 = chunk::tree_bits(p.tree, w.b, node, w.ctx, k0 + 32, p.window);
+          const uint4 bits = chunk::tree_bits(p.tree, w.b, node, w.ctx, k0, p.window);
+          const uint32_t b0 = bits.x, b1 = bits.y;  // (a tile is 64 keys here)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (((k < 2 ? b0 : b1) >> (tx + 16 * (k & 1)) & 1) == 0) s[i][k] = -INFINITY;

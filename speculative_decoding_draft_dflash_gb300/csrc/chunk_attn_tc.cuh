@@ -451,8 +451,8 @@ __device__ __noinline__ void repair(const Params<TREE>& p, const Item<TREE>& it,
 #pragma unroll 1
     for (int e = 0; e < TK; ++e) {
       if constexpr (TREE) {
-        const uint32_t m = chunk::tree_bits(p.tree, it.w.b, pos - it.w.ctx, it.w.ctx, k + (e & ~31), p.split.window);
-        if ((m >> (e & 31) & 1) == 0) continue;
+        const uint4 m = chunk::tree_bits(p.tree, it.w.b, pos - it.w.ctx, it.w.ctx, k, p.split.window);
+        if (((e < 32 ? m.x : e < 64 ? m.y : e < 96 ? m.z : m.w) >> (e & 31) & 1) == 0) continue;
       } else {
         if (k + e > pos || (p.split.window > 0 && pos - (k + e) >= p.split.window)) continue;
       }
@@ -590,14 +590,12 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
       const int hand_in = (warp & 3) == 0 ? 5 - ((rows + 31) >> 5) : 1;
       if (!any) ns += g.dual ? g.T : (g.T + 1 - X) >> 1;
       for (int j = !any ? g.T : g.dual ? 0 : X; j < g.T; j += step, ++done) {
-        [[maybe_unused]] uint32_t tm[4];  // TREE: keys that this row sees; looked up while S is computed
+        [[maybe_unused]] uint4 tm;  // TREE: keys that this row sees; looked up while S is computed
         if constexpr (TREE) {
           const int k = g.key0 + j * TK;
           if (k + TK > g.closed || (p.split.window > 0 && wlast - k >= p.split.window)) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              tm[c] = chunk::tree_bits(p.tree, it.w.b, valid ? pos - it.w.ctx : -1, it.w.ctx, k + 32 * c, p.split.window);
-            seen = seen || (tm[0] | tm[1] | tm[2] | tm[3]) != 0;
+            tm = chunk::tree_bits(p.tree, it.w.b, valid ? pos - it.w.ctx : -1, it.w.ctx, k, p.split.window);
+            seen = seen || (tm.x | tm.y | tm.z | tm.w) != 0;
           } else {
             seen = true;
           }
@@ -627,7 +625,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
               const int h = hi - 32 * c, l0 = lo - 32 * c;
               uint32_t m = h < 0 ? 0u : h >= 31 ? 0xffffffffu : (2u << h) - 1u;
               m &= l0 <= 0 ? 0xffffffffu : l0 > 31 ? 0u : 0xffffffffu << l0;
-              if constexpr (TREE) m = tm[c];
+              if constexpr (TREE) m = c == 0 ? tm.x : c == 1 ? tm.y : c == 2 ? tm.z : tm.w;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 s[32 * c + e] = m & (1u << e) ? s[32 * c + e] : -INFINITY;
