@@ -544,6 +544,18 @@ def _array(t, what, dtype, numel, device):
     raise ValueError(f"{what}: on device {t.get_device()}, the plan is on {device}")
 
 
+def _int_arrays(device, names, tensors, sizes):
+    """_array of several int32 tensors: one loop instead of as many calls (0.2 us of host time each)."""
+    i32, out = torch.int32, []
+    for what, t, n in zip(names, tensors, sizes):
+        if isinstance(t, torch.Tensor) and t.dtype is i32 and t.get_device() == device and t.numel() >= n and \
+                t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            out.append(_array(t, what, i32, n, device))
+    return out
+
+
 def _chunk(plan, desc, cache):
     """C descriptor of a plan, checked against the cache and the current device."""
     if plan.batch != desc.batch:
@@ -647,22 +659,24 @@ def dflash_tree_attn(dims, cache, layer, plan, tree, q, sliding_window, scaling,
 def dflash_tree_accept(plan, parents, tokens, posterior, ctx_len, accept_len, path, next_cu_rows,
                        ctx_next, next_anchor, stream=None):
     """The accepted path of every sequence's tree; path is int32 [batch][max_path]."""
-    i32, dev, rows, batch = torch.int32, plan.device, plan.rows, plan.batch
+    dev, rows, batch = plan.device, plan.rows, plan.batch
     _on_current("chunk plan", dev)
-    if path.dim() != 2 or path.shape[0] < batch:
-        raise ValueError(f"path: shape {tuple(path.shape)}, the call needs [{batch}][max_path]")
-    arr = lambda t, what, n: _array(t, what, i32, n, dev)  # noqa: E731
-    _check(_lib.dflash_tree_accept(plan.ref, arr(parents, "parents", rows), arr(tokens, "tokens", rows),
-                                   arr(posterior, "posterior", rows), arr(ctx_len, "ctx_len", batch),
-                                   int(path.shape[1]), arr(path, "path", 0), arr(accept_len, "accept_len", batch),
-                                   arr(next_cu_rows, "next_cu_rows", batch + 1), arr(ctx_next, "ctx_next", batch),
-                                   arr(next_anchor, "next_anchor", batch), _stream(stream)),
+    shape = path.shape
+    if len(shape) != 2 or shape[0] < batch:
+        raise ValueError(f"path: shape {tuple(shape)}, the call needs [{batch}][max_path]")
+    par, tok, post, ctx, pth, acc, cu, nxt, anchor = _int_arrays(
+        dev, _ACCEPT, (parents, tokens, posterior, ctx_len, path, accept_len, next_cu_rows, ctx_next, next_anchor),
+        (rows, rows, rows, batch, 0, batch, batch + 1, batch, batch))
+    _check(_lib.dflash_tree_accept(plan.ref, par, tok, post, ctx, shape[1], pth, acc, cu, nxt, anchor, _stream(stream)),
            "dflash_tree_accept")
+
+
+_ACCEPT = ("parents", "tokens", "posterior", "ctx_len", "path", "accept_len", "next_cu_rows", "ctx_next", "next_anchor")
 
 
 def dflash_tree_commit(dims, cache, tree, ctx_len, path, accept_len, stream=None):
     """Moves the accepted paths' rows behind the committed ones, in every layer, and sets lengths."""
-    i32, desc, dev = torch.int32, _desc(dims, cache), tree.device
+    desc, dev = _desc(dims, cache), tree.device
     _on_current("tree", dev)
     if tree.batch != desc.batch:
         raise ValueError(f"tree: {tree.batch} sequences, the cache has {desc.batch}")
@@ -670,9 +684,9 @@ def dflash_tree_commit(dims, cache, tree, ctx_len, path, accept_len, stream=None
         raise ValueError(f"cache: on device {cache.device}, the tree is on {dev}")
     if path.dim() != 2 or path.shape[0] < tree.batch:
         raise ValueError(f"path: shape {tuple(path.shape)}, the call needs [{tree.batch}][max_path]")
-    _check(_lib.dflash_tree_commit(ctypes.byref(dims), ctypes.byref(desc), tree.ref,
-                                   _array(ctx_len, "ctx_len", i32, tree.batch, dev), _array(path, "path", i32, 0, dev),
-                                   int(path.shape[1]), _array(accept_len, "accept_len", i32, tree.batch, dev),
+    ctx, pth, acc = _int_arrays(dev, ("ctx_len", "path", "accept_len"), (ctx_len, path, accept_len),
+                                (tree.batch, 0, tree.batch))
+    _check(_lib.dflash_tree_commit(ctypes.byref(dims), ctypes.byref(desc), tree.ref, ctx, pth, int(path.shape[1]), acc,
                                    _stream(stream)), "dflash_tree_commit")
 
 
