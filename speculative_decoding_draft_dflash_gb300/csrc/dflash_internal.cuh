@@ -57,15 +57,17 @@ struct Carver {
 // test lowered it with dflash_test_wait_limit; dflash_api.cu).
 unsigned long long wait_limit_ns();
 
-// Raises a kernel's dynamic shared-memory limit once per device.
+// Raises a kernel's dynamic shared-memory limit once per device (and allows clusters of more than eight CTAs).
 struct SmemLimit {
   unsigned char done[128] = {};
-  template <typename F> cudaError_t raise(F* kernel, int bytes) {
+  template <typename F> cudaError_t raise(F* kernel, int bytes, bool wide_clusters = false) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128 && __atomic_load_n(&done[dev], __ATOMIC_ACQUIRE)) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && wide_clusters)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess && dev >= 0 && dev < 128) __atomic_store_n(&done[dev], 1, __ATOMIC_RELEASE);
     return e;
   }

@@ -4,7 +4,7 @@
 //
 // next(p) = min {i > p : parent(i) = p, token(i) = posterior(p)} is found for all nodes at once,
 // a lane per row with a minimum in shared memory; the path is then one load a step. A warp per
-// sequence; the CTAs are one cluster of at most eight, which the prefix sum of the accepted
+// sequence; the CTAs are one cluster of at most sixteen, which the prefix sum of the accepted
 // rows needs (totals exchanged through distributed shared memory).
 #include <cooperative_groups.h>
 #include <limits.h>
@@ -19,7 +19,8 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kNext = 512;  // rows of a tree whose successors fit a warp's share of shared memory
-constexpr int kPer = kChunkMaxBatch / 8;  // sequences of a CTA, at most
+constexpr int kCtas = 16;                     // more than eight is not portable, but fits a GPC here
+constexpr int kPer = kChunkMaxBatch / kCtas;  // sequences of a CTA, at most
 
 struct Smem {
   int next[kWarps][kNext];
@@ -123,10 +124,10 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeAcceptP
 
 cudaError_t tree_accept(const TreeAcceptParams& p, cudaStream_t s) {
   static SmemLimit limit;
-  cudaError_t e = limit.raise(tree_accept_kernel, (int)sizeof(Smem));
+  cudaError_t e = limit.raise(tree_accept_kernel, (int)sizeof(Smem), true);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_TREE_ACCEPT, s);
-  const int want = (p.batch + kWarps - 1) / kWarps, ctas = want > 8 ? 8 : want;
+  const int want = (p.batch + kWarps - 1) / kWarps, ctas = want > kCtas ? kCtas : want;
   const int per = (p.batch + ctas - 1) / ctas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);

@@ -186,3 +186,34 @@ def test_select_optional_outputs_and_launches(D):
         D.dflash_beam_select(x, s, 6, tok[:, ::2], None, None, ws)
     with pytest.raises(D.DFlashError):
         D.dflash_beam_select(x, s, 6, tok, None, None, ws[:100].clone())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_select_rows_beyond_32_bit_offsets(D, dtype):
+    far = 2 ** 31 + 8
+    t = torch.zeros(far + 4096, dtype=TORCH[dtype], device=DEV)
+    x, s = random(dtype, 2, 1, 4001, seed=11)
+    t[:4001], t[far:far + 4001] = x[0, 0], x[1, 0]
+    check(D, t.as_strided((2, 1, 4001), (far, 4001, 1)), s, 20)
+    check(D, t.as_strided((1, 2, 4001), (far, far, 1)), s.t().contiguous(), 20)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_select_clustered_maxima(D, dtype):
+    """The best logits side by side in one run, in one lane's runs of every tile, and in the last elements."""
+    V = 70001
+    for place in ("run", "lane", "end"):
+        x, s = random(dtype, 2, 2, V, seed=12)
+        at = {"run": torch.arange(33000, 33100), "lane": torch.arange(0, V - 32, 8192)[:, None] + torch.arange(12),
+              "end": torch.arange(V - 90, V)}[place].flatten()
+        x[..., at] = (30 + torch.arange(at.numel()).float() * 0.125).to(DEV, TORCH[dtype])
+        for k in (3, 40, 128):
+            check(D, x, s, k)
+
+
+def test_select_many_rows_and_beams(D):
+    x, s = random("bf16", 3000, 1, 100, seed=13)
+    check(D, x, s, 1)
+    x, s = random("f32", 2, 128, 5000, seed=14)
+    check(D, x, s, 128)
+    check(D, x[:, :1].expand(2, 128, 5000), s, 128)

@@ -517,3 +517,324 @@ def test_commit_bad_page(D):
             old.view(c.k.shape[:-1] + (-1,))[:, int(c.block_table[0, 0]), :, 123]
         assert torch.equal(now, old)
     assert c.lens.tolist() == [[124], [124]]
+
+
+# ---------------------------------------------------------------------------
+# together: rounds of drafted trees, a beam search
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv,paged", [("bf16", True), ("bf16", False), ("fp8", True), ("f32", False)])
+@pytest.mark.parametrize("graph", [False, True])
+def test_rounds_of_trees_leave_the_accepted_rows_in_the_cache(D, kv, paged, graph):
+    """Map, tree map, append, attention, greedy posterior, acceptance and commit, round after round on
+    the device (captured: one graph, replayed): what each round decides, then the cache against rows made from
+    the accepted nodes' projections."""
+    B, layers, n, width = 3, 2, 24, 8
+    n_h, n_kv, d = (8, 2, 128) if kv != "f32" else (4, 2, 64)
+    dt = torch.float32 if kv == "f32" else torch.bfloat16
+    cap, V = 384, 40
+    r = rng_of(17)
+    c = D.KVCache(layers, B, n_kv, cap, d, dt, DEV, paged=paged, kv="fp8" if kv == "fp8" else "bf16",
+                  kv_scales=[[0.05, 0.02]] * layers if kv == "fp8" else None)
+    dims = D.make_dims(64, n_h, n_kv, d, 1, 1, 1e-6, dt)
+    pool = D.PagePool(i32([0] * B), c.block_table.flatten().clone(), i32([0])) if paged else None
+    M = B * n
+    cu = [b * n for b in range(B + 1)]
+    plan, tree = D.ChunkPlan(i32(cu), M), D.Tree(B, 32, DEV)
+    widths = (n_h * d, n_kv * d, n_kv * d)
+    x = torch.zeros((layers, M, sum(widths)), dtype=dt, device=DEV)
+    parents, tokens = i32([0] * M), i32([0] * M)
+    logits = torch.zeros((M, 1, V), dtype=torch.float32, device=DEV)
+    posterior = torch.zeros((M, 1), dtype=torch.int32, device=DEV)
+    ctx, acc, path = i32([0] * B), i32([0] * B), i32(np.zeros((B, 8)))
+    ncu, nxt, anchor = i32([0] * (B + 1)), i32([0] * B), i32([0] * B)
+    table = torch.empty((cap, d // 2, 2), dtype=torch.float32, device=DEV)
+    D.dflash_rope_table_build(1e6, d, cap, table)
+    gk = (1 + 0.1 * torch.randn(d, generator=torch.Generator().manual_seed(1))).to(DEV, dt)
+    q = [torch.zeros((M, n_h * d), dtype=dt, device=DEV) for _ in range(layers)]
+    out = [torch.zeros_like(t) for t in q]
+    ws = torch.empty(D.dflash_chunk_workspace_bytes(dims), dtype=torch.uint8, device=DEV)
+    bws = torch.empty(D.dflash_beam_workspace_bytes(M, 1, V, 1), dtype=torch.uint8, device=DEV)
+
+    def round_():
+        D.dflash_chunk_map(c, 0, plan, pool)
+        D.dflash_tree_map(plan, tree, parents)
+        for l in range(layers):
+            a, b, v = x[l].split(widths, dim=1)
+            D.dflash_chunk_append(dims, c, l, plan, a, b, v, gk, gk, table, cap, q[l])
+            D.dflash_tree_attn(dims, c, l, plan, tree, q[l], 0, 0.0, out[l], ws)
+        D.dflash_beam_select(logits, None, 1, posterior, None, None, bws)
+        D.dflash_tree_accept(plan, parents, tokens, posterior, ctx, acc, path, ncu, nxt, anchor)
+        D.dflash_tree_commit(dims, c, tree, ctx, path, acc)
+        ctx.copy_(nxt)
+
+    g = None
+    if graph:                                        # capture (nothing runs)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            round_()
+    kept = [[[] for _ in range(B)] for _ in range(layers)]      # (k, v) projections of the accepted rows
+    moved = 0
+    for step in range(5):
+        host = r.standard_normal((layers, M, sum(widths))).astype(np.float32)
+        x.copy_(torch.from_numpy(host).to(dt))
+        par, tok, post = [], [], []
+        for b in range(B):
+            p = T.random_tree(r, n, width // 2)
+            t = r.integers(0, V, size=n).tolist()
+            kids = [[i for i in range(n) if p[i] == u] for u in range(n)]
+            par, tok = par + p, tok + t
+            post += [t[int(r.choice(k))] if k and r.random() < 0.85 else int(r.integers(0, V)) for k in kids]
+        parents.copy_(i32(par)), tokens.copy_(i32(tok))
+        lg = torch.randn((M, 1, V), generator=torch.Generator().manual_seed(step))
+        lg[torch.arange(M), 0, torch.tensor(post)] = 9.0
+        logits.copy_(lg)
+        before = ctx.tolist()
+        g.replay() if graph else round_()
+        assert D.dflash_status_get() == 0
+        assert posterior[:, 0].tolist() == post
+        xn = np64(x.reshape(layers * M, -1)).reshape(layers, M, -1)
+        for b in range(B):
+            lo = b * n
+            want, last = T.accept(par[lo:lo + n], tok[lo:lo + n], post[lo:lo + n], 8)
+            assert path[b].tolist() == want + [-1] * (8 - len(want)) and int(anchor[b]) == last
+            assert int(ctx[b]) == before[b] + len(want) and c.lens[:, b].tolist() == [int(ctx[b])] * layers
+            moved += sum(i != u for i, u in enumerate(want))
+            for l in range(layers):
+                kept[l][b] += [xn[l, lo + u, n_h * d:] for u in want]
+    assert moved > 10
+    scales = c.scales
+    for l in range(layers):
+        for b in range(B):
+            m = int(ctx[b])
+            assert m == len(kept[l][b])
+            got = [np64(c.rows(w, l, b, 0, m, codes=True)).transpose(1, 0, 2) for w in "kv"]
+            for i in range(m):
+                k, v = kept[l][b][i][:n_kv * d].reshape(n_kv, d), kept[l][b][i][n_kv * d:].reshape(n_kv, d)
+                y, mag = R.norm_rope(k, np64(gk), i)
+                how = {"f32": "f32", "bf16": "bf16", "fp8": "e4m3"}[kv]
+                sk, sv = (scales[l] if kv == "fp8" else (1.0, 1.0))
+                assert (np.abs(got[0][i] - np.clip(y / sk, -448, 448)) <= R.append_bound(y / sk, mag / sk, d, how)).all(), (l, b, i)
+                assert (np.abs(got[1][i] - np.clip(v / sv, -448, 448)) <= R.append_bound(v / sv, np.abs(v / sv), d, how)).all()
+
+
+def test_beam_search_over_one_cache(D):
+    """A beam search on a small random model: hypotheses are paths of one tree behind the prompt, and
+    nothing of the cache moves. Tokens, parents and scores against the same search with every hypothesis
+    recomputed from its start in float64."""
+    n_h, n_kv, d, V, beams, steps, B = 4, 2, 32, 60, 3, 7, 2
+    g = torch.Generator().manual_seed(31)
+    emb = torch.randn((V, 48), generator=g, dtype=torch.float64)
+    Wq, Wk, Wv = (torch.randn((48, h * d), generator=g, dtype=torch.float64) * 0.3 for h in (n_h, n_kv, n_kv))
+    Wo = torch.randn((n_h * d, V), generator=g, dtype=torch.float64) * 0.4
+    emb, Wq, Wk, Wv, Wo = (t.float() for t in (emb, Wq, Wk, Wv, Wo))
+    prompts = [[3, 17, 41, 8], [55, 2, 9, 30]]
+    P = len(prompts[0])
+    cap = 128
+    c = D.KVCache(1, B, n_kv, cap, d, "f32", DEV)
+    dims = D.make_dims(64, n_h, n_kv, d, 1, 1, 1e-6, "f32")
+    table = torch.empty((cap, d // 2, 2), dtype=torch.float32, device=DEV)
+    D.dflash_rope_table_build(1e6, d, cap, table)
+    ws = torch.empty(D.dflash_chunk_workspace_bytes(dims), dtype=torch.uint8, device=DEV)
+    dev = [t.to(DEV) for t in (emb, Wq, Wk, Wv, Wo)]
+
+    def step(plan, tree, tokens):
+        h = dev[0][tokens.long()]
+        q, k, v = h @ dev[1], h @ dev[2], h @ dev[3]
+        qo, out = torch.empty_like(q), torch.empty_like(q)
+        D.dflash_chunk_append(dims, c, 0, plan, q, k, v, None, None, table, cap, qo)
+        if tree is None:
+            D.dflash_chunk_attn(dims, c, 0, plan, qo, 0, 0.0, out, ws)
+        else:
+            D.dflash_tree_attn(dims, c, 0, plan, tree, qo, 0, 0.0, out, ws)
+        return out @ dev[4]
+
+    def exact(seq):
+        """Next-token logits of a whole sequence in float64."""
+        e = emb.double().numpy()[seq]
+        q, k, v = ((e @ w.double().numpy()).reshape(len(seq), -1, d) for w in (Wq, Wk, Wv))
+        k = np.stack([R.norm_rope(k[i], None, i)[0] for i in range(len(seq))])
+        q1 = R.norm_rope(q[-1], None, len(seq) - 1)[0][None]
+        o, _, _, _ = R.attention(q1, k, v, len(seq), 1, n_h // n_kv, 0, d ** -0.5)
+        return o.reshape(-1) @ Wo.double().numpy()
+
+    torch.backends.cuda.matmul.allow_tf32 = False
+    plan = D.ChunkPlan(i32([0, P, 2 * P]), 2 * P)
+    D.dflash_chunk_map(c, 0, plan)
+    logits = step(plan, None, i32(sum(prompts, [])))
+    ref = [[(p, 0.0)] for p in prompts]
+    tree = D.Tree(B, 64, DEV)
+    nodes = 0
+    scores = None
+    last = logits.view(B, P, V)[:, -1:, :]                     # one beam: the prompt
+    for s in range(steps):
+        n_in = last.shape[1]
+        tok, par = (torch.zeros((B, beams), dtype=torch.int32, device=DEV) for _ in range(2))
+        new = torch.zeros((B, beams), dtype=torch.float32, device=DEV)
+        bws = torch.empty(D.dflash_beam_workspace_bytes(B, n_in, V, beams), dtype=torch.uint8, device=DEV)
+        base = max(0, nodes - n_in) if s else 0
+        D.dflash_beam_select(last.contiguous(), scores, beams, tok, par, new, bws, parent_base=base)
+        scores = new
+        for b in range(B):
+            x = np.stack([exact(h) for h, _ in ref[b]])
+            t, i, v = T.beam_select(x, np.array([w for _, w in ref[b]]), beams)
+            assert tok[b].tolist() == t.tolist() and (par[b] - base).tolist() == i.tolist(), (s, b)
+            # scores: fp32 projections, attention and sums of up to 48, 64 and 128 terms, a step's error adding
+            # to the last's
+            assert np.abs(np64(new[b]) - v).max() <= (s + 1) * 2e-4
+            ref[b] = [(ref[b][j][0] + [int(u)], float(w)) for j, u, w in zip(i, t, v)]
+        parents = par if s else torch.full_like(par, -1)       # the first hypotheses follow the prompt
+        plan = D.ChunkPlan(i32([0, beams, 2 * beams]), 2 * beams)
+        D.dflash_chunk_map(c, 0, plan)
+        D.dflash_tree_map(plan, tree, parents.contiguous(), tree.nodes)
+        nodes += beams
+        assert plan.positions.tolist() == [P + s] * (2 * beams) and tree.nodes.tolist() == [nodes] * B
+        last = step(plan, tree, tok.flatten()).view(B, beams, V)
+    assert D.dflash_status_get() == 0
+    # keep the best hypothesis: its path becomes the cache's rows
+    paths = []
+    for b in range(B):
+        masks = tree.masks[b].cpu().numpy().astype(np.uint32)
+        m = int(masks[nodes - beams, 0]) | int(masks[nodes - beams, 1]) << 32
+        paths.append([u for u in range(nodes) if m >> u & 1])
+    assert all(len(p) == steps for p in paths)
+    D.dflash_tree_commit(dims, c, tree, i32([P] * B), i32(paths), i32([steps - 1] * B))
+    assert c.lens.tolist() == [[P + steps] * B] and D.dflash_status_get() == 0
+    for b in range(B):
+        seq = ref[b][0][0]
+        k = (emb.double().numpy()[seq] @ Wk.double().numpy()).reshape(len(seq), n_kv, d)
+        got = np64(c.rows("k", 0, b, 0, P + steps)).transpose(1, 0, 2)
+        for i in range(P + steps):
+            y, mag = R.norm_rope(k[i], None, i)
+            assert (np.abs(got[i] - y) <= 48 * 2.0 ** -22 * (np.abs(emb.numpy()[seq[i]])[:, None] * np.abs(Wk.numpy())).sum(0).max()
+                    + R.append_bound(y, mag, d, "f32")).all()
+
+
+# ---------------------------------------------------------------------------
+# sizes
+# ---------------------------------------------------------------------------
+
+def test_steps_without_rows(D):
+    plan = D.ChunkPlan(i32([0, 0, 0]), 3, kv_lens=i32([5, 0]), slots=i32([-1] * 3), positions=i32([-7] * 3))
+    tree = D.Tree(2, 32, DEV)
+    tree.nodes.fill_(9)
+    D.dflash_tree_map(plan, tree, i32([7] * 3), i32([2, 3]))
+    assert tree.nodes.tolist() == [2, 3] and plan.positions.tolist() == [-7] * 3 and plan.kv_lens.tolist() == [5, 0]
+    got, ctx = _accept(D, [0, 0], [], [], [], 3, pad=3, kv=[5, 5])
+    _check_accept(got, ctx, [0, 0], [], [], [], 3)
+    s = TreeStep(D, "bf16", (4, 2, 128), [10], [0], [4], seed=1)
+    s.map(), s.tree_map()
+    plan = D.ChunkPlan(i32([0, 0]), 0, kv_lens=i32([10]))
+    out = torch.full((1, 512), 3.0, dtype=torch.bfloat16, device=DEV)
+    D.dflash_tree_attn(s.dims, s.cache, 0, plan, s.tree, out, 0, 0.0, out, s.ws)
+    assert (out == 3.0).all() and D.dflash_status_get() == 0
+
+
+def test_map_beyond_32_bit_offsets(D):
+    """Masks of 1100 sequences of 4096 nodes: 2.3 GB."""
+    B, N = 1100, 4096
+    tree = D.Tree(B, N, DEV)
+    n = 5
+    plan = D.ChunkPlan(i32([n * b for b in range(B + 1)]), n * B, kv_lens=i32([n + 4000 + b for b in range(B)]), slots=i32([1] * n * B))
+    par = [-1, 0, 0, 2, 1]
+    D.dflash_tree_map(plan, tree, i32(par * B))
+    D.dflash_tree_map(plan, tree, i32([4, 5, 5, 7, 8] * B), tree.nodes)
+    assert D.dflash_status_get() == 0 and tree.nodes.unique().tolist() == [10]
+    for b in (0, 1023, 1024, 1099):
+        want = T.tree_map([0, 5], [10 ** 6], par, [0], [[]], [[]], N)
+        want = T.tree_map([0, 5], [10 ** 6], [4, 5, 5, 7, 8], want[1], want[2], want[3], N)
+        got = tree.masks[b, :10].cpu().numpy()
+        assert all((got[t] == T.words(want[3][0][t], N)).all() for t in range(10))
+        assert tree.depths[b, :10].tolist() == want[2][0]
+
+
+def test_attn_and_commit_beyond_32_bit_offsets(D):
+    """The second layer of a pool of 9000 pages begins 2.4 GB on."""
+    n_h, n_kv, d, pages = 16, 8, 128, 9000
+    table = torch.tensor([[8999, 4500, 17]], dtype=torch.int32)
+    c = D.KVCache(2, 1, n_kv, 384, d, "bf16", DEV, page_table=table, n_pages=pages)
+    dims = D.make_dims(64, n_h, n_kv, d, 1, 1, 1e-6, "bf16")
+    g = torch.Generator().manual_seed(2)
+    ctx, n = 120, 40
+    K, V = (torch.randn((n_kv, ctx + n, d), generator=g).to(DEV, torch.bfloat16) for _ in range(2))
+    c.set_rows(1, 0, K, V)
+    plan = D.ChunkPlan(i32([0, n]), n, kv_lens=i32([ctx + n]), slots=i32([0] * n))
+    tree = D.Tree(1, 64, DEV)
+    par = T.random_tree(rng_of(3), n)
+    D.dflash_tree_map(plan, tree, i32(par))
+    q = torch.randn((n, n_h * d), generator=g).to(DEV, torch.bfloat16)
+    out = torch.zeros_like(q)
+    ws = torch.empty(D.dflash_chunk_workspace_bytes(dims), dtype=torch.uint8, device=DEV)
+    D.dflash_tree_attn(dims, c, 1, plan, tree, q, 0, 0.0, out, ws)
+    _, nodes, depths, masks, _ = T.tree_map([0, n], [10 ** 6], par, [0], [[]], [[]], 64)
+    keys = [T.visible(ctx + n, n, t, depths[0], masks[0][t], 0) for t in range(n)]
+    kn, vn = np64(K).transpose(1, 0, 2), np64(V).transpose(1, 0, 2)
+    ref, mag, big, most = T.attention(np64(q).reshape(n, n_h, d), kn, vn, keys, 2, d ** -0.5)
+    assert (np.abs(np64(out).reshape(n, n_h, d) - ref) <= T.attention_bound(ref, mag, big, most, d, "bf16")).all()
+    D.dflash_tree_commit(dims, c, tree, i32([ctx]), i32([[0, 5, 20, 39]]), i32([3]))
+    for i, u in enumerate((0, 5, 20, 39)):
+        assert torch.equal(c.rows("k", 1, 0, ctx + i, ctx + i + 1)[:, 0], K[:, ctx + u])
+        assert torch.equal(c.rows("v", 1, 0, ctx + i, ctx + i + 1)[:, 0], V[:, ctx + u])
+    assert D.dflash_status_get() == 0 and c.lens.tolist() == [[ctx + 4]] * 2
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "f32"])
+def test_attn_many_sequences(D, kv):
+    """4096 sequences of a node or two."""
+    B = 4096
+    n_h, n_kv, d = (2, 1, 128) if kv != "f32" else (2, 1, 32)
+    r = rng_of(5)
+    ctx, rows = r.integers(0, 4, size=B).tolist(), r.integers(0, 3, size=B).tolist()
+    s = TreeStep(D, kv, (n_h, n_kv, d), ctx, [0] * B, rows, max_nodes=32, paged=False, seed=5)
+    s.map(), s.tree_map()
+    q = torch.empty((s.M, n_h * d), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    out = torch.empty_like(q)
+    s.tree_attn(q, out)
+    assert D.dflash_status_get() == 0
+    s.check_tree(q, out, skip=set(range(B)) - set(range(0, B, 41)) - {B - 1})
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_attn_that_gives_up_leaves_a_working_gpu(D, kv):
+    """With a limit of 1 ns the roles of the kernel stop at their first longer wait; the next call is
+    right. (The warp that checks the tiles of the tree first waits for tens of microseconds.)"""
+    s = TreeStep(D, kv, (32, 8, 128), [100_000], [0], [64], seed=9)
+    s.map(), s.tree_map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    s.tree_attn(q, want)
+    assert D.dflash_status_get() == 0
+    st = 0
+    try:
+        D.dflash_test_wait_limit(1)
+        for _ in range(3):
+            s.tree_attn(q, out)
+            st |= D.dflash_status_get()
+            if st & D.DEV_TIMEOUT:
+                break
+    finally:
+        D.dflash_test_wait_limit(0)
+    assert st == D.DEV_TIMEOUT
+    out.fill_(float("nan"))
+    s.tree_attn(q, out)
+    assert D.dflash_status_get() == 0
+    assert torch.equal(out, want)
+
+
+def test_launches_and_trace_kinds(D):
+    s = TreeStep(D, "bf16", (8, 2, 128), [300], [0], [20], seed=10)
+    s.map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    out = torch.empty_like(q)
+    kinds = ["tree_map", "chunk_append", "chunk_attn", "chunk_merge", "tree_accept", "tree_commit"]
+    n = D.dflash_launch_count()
+    D.dflash_trace_start(kinds, 16)
+    s.tree_map(), s.append(q), s.tree_attn(q, out)
+    o = [i32([0]), i32([[0] * 4]), i32([0, 0]), i32([0]), i32([0])]
+    D.dflash_tree_accept(s.plan, s.parents, s.parents, s.parents, i32([300]), *o)
+    D.dflash_tree_commit(s.dims, s.cache, s.tree, i32([300]), o[1], o[0])
+    assert [k for k, _ in D.dflash_trace_stop()] == kinds
+    assert D.dflash_launch_count() == n + len(kinds) and D.dflash_status_get() == 0
