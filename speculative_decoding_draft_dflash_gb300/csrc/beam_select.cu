@@ -391,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 3) beam_scan_kernel(const Scan p) {
   ScanSmem<J>& sh = *reinterpret_cast<ScanSmem<J>*>(smem);
   volatile float* wbound = sh.wbound;
   float* wmax = sh.wmax;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be scheduled
+  grid_wait();
+  grid_trigger();  // the merge may be scheduled
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // piece -> its row's first element; its elements [begin, end)
   auto row_of = [&](int piece, int& begin, int& end) -> const T* {
@@ -672,7 +673,8 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(const Merge p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
   if (threadIdx.x == 0) list.count = spread_s = 0;
   for (int i = threadIdx.x; i < kBins; i += THREADS) bins[i] = 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the scan's lists
+  grid_wait();  // the scan's lists
+  grid_trigger();
   const int per = p.splits * p.k;
   const u64* lists = p.lists + (size_t)b * p.rows_per_seq * per;
   const Piece* pieces = p.pieces + (size_t)b * p.rows_per_seq * p.splits;
@@ -868,8 +870,8 @@ cudaError_t scan_rows(const Scan& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_BEAM_SCAN, s);
   const int slots = kCtas * chunk_sms();
-  beam_scan_kernel<T, J><<<p.pieces_n < slots ? p.pieces_n : slots, kThreads, sizeof(ScanSmem<J>), s>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(beam_scan_kernel<T, J>, dim3(p.pieces_n < slots ? p.pieces_n : slots), kThreads,
+                           sizeof(ScanSmem<J>), s, p);
 }
 
 template <int THREADS>
@@ -878,17 +880,8 @@ cudaError_t merge_rows(const Merge& p, int batch, cudaStream_t s) {
   const cudaError_t e = limit.raise(beam_merge_kernel<THREADS>, (int)sizeof(float) * kMostRough);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_BEAM_MERGE, s);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(batch);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = sizeof(float) * (size_t)p.beams * p.splits * p.k;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // scheduled as SMs fall free
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, beam_merge_kernel<THREADS>, p);
+  return launch_overlapped(beam_merge_kernel<THREADS>, dim3(batch), THREADS, sizeof(float) * (size_t)p.beams * p.splits * p.k,
+                           s, p);
 }
 
 struct Carved {

@@ -20,7 +20,8 @@ __device__ __forceinline__ float piece_weight(float mx, float M, bool natural) {
 
 // f32: a warp per query row; partials row by row.
 __global__ void __launch_bounds__(256) chunk_merge_f32_kernel(const ChunkAttnParams p, int rows_max) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's partials
+  grid_wait();  // the attention kernel's partials
+  grid_trigger();
   const int4 m = p.merge[blockIdx.x];
   if (m.w == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -71,7 +72,8 @@ __global__ void __launch_bounds__(256) chunk_merge_f32_kernel(const ChunkAttnPar
 // bf16, d_h = 128: partials are [column / 8][row][8]. A warp takes 8 rows x 32 columns: lane
 // = (row, group of 8 columns); eight lanes of a column group read 256 bytes in a row.
 __global__ void __launch_bounds__(256) chunk_merge_bf16_kernel(const ChunkAttnParams p, int rows_max) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's partials
+  grid_wait();  // the attention kernel's partials
+  grid_trigger();
   const int4 m = p.merge[blockIdx.x];
   if (m.w == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -157,18 +159,9 @@ cudaError_t chunk_attn(int dtype, const ChunkAttnParams& p, cudaStream_t s) {
                                : (f32 ? chunk_attn_simt(p, s) : chunk_attn_tc(p, s));
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_MERGE, s);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(attn_ctas(dtype, p.d_h), 16);  // every row at once
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // scheduled as SMs fall free
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return dtype == DFLASH_F32
-             ? cudaLaunchKernelEx(&cfg, chunk_merge_f32_kernel, p, chunk_attn_simt_item_rows(p.d_h))
-             : cudaLaunchKernelEx(&cfg, chunk_merge_bf16_kernel, p, chunk_attn_tc_item_rows(p.G));
+  const dim3 grid(attn_ctas(dtype, p.d_h), 16);  // every row at once
+  return f32 ? launch_overlapped(chunk_merge_f32_kernel, grid, 256, 0, s, p, chunk_attn_simt_item_rows(p.d_h))
+             : launch_overlapped(chunk_merge_bf16_kernel, grid, 256, 0, s, p, chunk_attn_tc_item_rows(p.G));
 }
 
 }  // namespace dflash

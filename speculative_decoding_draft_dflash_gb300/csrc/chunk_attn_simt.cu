@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DP)) chunk_attn_simt_ker
   // at 2, 3, 6 of 6: 14 tokens and 6 chunks 149, 145, 190, 6 prompts 146, 133, 140.
   const chunk::Split<false, TREE> split = {p.cu_rows, p.kv_lens, p.batch, p.rows, p.n_kv, p.G, p.capacity,
                               p.window, RI, 0, RI / (RI > 64 ? 2 : 4), 6, 2, 6, RI > 64 ? 3 : 2, p.tree.nodes, p.tree.max_nodes};
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be scheduled
+  grid_wait();
+  grid_trigger();  // the merge may be scheduled
   chunk::locate(split, smem4, &start, p.status);
   chunk::Walker<false, TREE> walk;
   walk.init(split, start);
@@ -340,8 +341,7 @@ cudaError_t launch(const ChunkAttnParams& p, cudaStream_t s) {
   cudaError_t e = limit.raise(chunk_attn_simt_kernel<DP, TREE>, tiles > most ? tiles : most);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_ATTN, s);
-  chunk_attn_simt_kernel<DP, TREE><<<chunk_attn_simt_ctas(p.d_h), kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(chunk_attn_simt_kernel<DP, TREE>, dim3(chunk_attn_simt_ctas(p.d_h)), kThreads, smem, s, p);
 }
 
 }  // namespace

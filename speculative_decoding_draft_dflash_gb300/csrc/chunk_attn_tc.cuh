@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = ptx::smem_u32(smem);
   if (sbase & 1023) {  // the swizzled tiles would be misplaced
+    grid_wait();
     if (threadIdx.x == 0) {
       atomicOr(p.status, DFLASH_DEV_TIMEOUT);
       p.merge[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -538,7 +539,8 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     ptx::prefetch_tmap(&p.k);
     ptx::prefetch_tmap(&p.v);
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be scheduled
+  grid_wait();     // nothing of the caller's has been read or written yet
+  grid_trigger();  // the merge may be scheduled
   // the work split, in what becomes the K / V ring
   static_assert(5 * TILE >= chunk::kLocateBytes<TREE> * (TREE ? kTreeMaxBatch : kChunkMaxBatch), "scratch of the work split");
   chunk::locate(p.split, smem + PL::OFF_KV, &sh.start, p.status);
@@ -1157,8 +1159,7 @@ cudaError_t launch(const Params<TREE>& p, cudaStream_t s) {
   cudaError_t e = limit.raise(chunk_attn_tc_kernel<FP8, TREE>, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_CHUNK_ATTN, s);
-  chunk_attn_tc_kernel<FP8, TREE><<<chunk_sms(), Plan<FP8>::THREADS, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(chunk_attn_tc_kernel<FP8, TREE>, dim3(chunk_sms()), Plan<FP8>::THREADS, smem, s, p);
 }
 
 }  // namespace

@@ -73,6 +73,27 @@ struct SmemLimit {
   }
 };
 
+// Programmatic dependent launch: a kernel launched with launch_overlapped may be scheduled once every CTA of
+// the kernel before it in the stream has called grid_trigger or ended. It calls grid_wait, in all threads and
+// before anything is read or written, which returns when that kernel has completed (and, as every
+// such kernel waits itself, all before it). So only its launch and its start overlap with the other's end.
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // per-device sticky status word (defined in dflash_api.cu)
 unsigned* status_word();
 

@@ -32,6 +32,8 @@ struct Smem {
 __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeAcceptParams p, int per) {
   extern __shared__ int4 smem4[];
   Smem& sh = *reinterpret_cast<Smem*>(smem4);
+  grid_wait();
+  grid_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int s0 = (int)blockIdx.x * per, s1 = min(p.batch, s0 + per);
   int* next = sh.next[warp];
@@ -134,12 +136,14 @@ cudaError_t tree_accept(const TreeAcceptParams& p, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Smem);
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ctas;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, tree_accept_kernel, p, per);
 }
 

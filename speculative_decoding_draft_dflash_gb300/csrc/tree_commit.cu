@@ -16,6 +16,8 @@ constexpr int kAhead = 8;  // rows in flight per thread
 template <typename T>
 __global__ void __launch_bounds__(256) tree_commit_kernel(const TreeCommitParams p) {
   __shared__ long long src[kRows], dst[kRows];  // row of KV head 0 in the layer, -1: not moved
+  grid_wait();
+  grid_trigger();
   const int b = blockIdx.x, l = blockIdx.y >> 1, which = blockIdx.y & 1;
   const int a = p.accept_len[b], ctx = p.ctx_len[b], nodes = p.nodes[b];
   if (a == -1) return;
@@ -77,11 +79,7 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(const TreeCommitParams
 cudaError_t tree_commit(const TreeCommitParams& p, cudaStream_t s) {
   LaunchScope ls_(DFLASH_KERNEL_TREE_COMMIT, s);
   const dim3 grid(p.batch, 2 * p.n_layers);
-  if (p.row_bytes % 16 == 0)
-    tree_commit_kernel<uint4><<<grid, 128, 0, s>>>(p);
-  else
-    tree_commit_kernel<uint2><<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(p.row_bytes % 16 == 0 ? tree_commit_kernel<uint4> : tree_commit_kernel<uint2>, grid, 128, 0, s, p);
 }
 
 }  // namespace dflash

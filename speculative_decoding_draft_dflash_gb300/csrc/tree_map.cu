@@ -19,6 +19,8 @@ constexpr int kBlock = 128;  // rows between two barriers
 template <int NW>
 __global__ void __launch_bounds__(1024) tree_map_kernel(const TreeMapParams p) {
   __shared__ int up[kTreeMaxNodes];
+  grid_wait();
+  grid_trigger();
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int lo = p.cu_rows[b], hi = p.cu_rows[b + 1], kv = p.kv_lens[b];
   const int t0 = p.nodes_before ? p.nodes_before[b] : 0;
@@ -95,13 +97,8 @@ cudaError_t tree_map(const TreeMapParams& p, cudaStream_t s) {
   // a warp for each of a sequence's rows, on average
   const int per = p.rows / p.batch + 1, warps = per < 4 ? 4 : per > 32 ? 32 : per;
   const int words = p.max_nodes / 32;
-  if (words <= 32)
-    tree_map_kernel<1><<<p.batch, 32 * warps, 0, s>>>(p);
-  else if (words <= 64)
-    tree_map_kernel<2><<<p.batch, 32 * warps, 0, s>>>(p);
-  else
-    tree_map_kernel<4><<<p.batch, 32 * warps, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(words <= 32 ? tree_map_kernel<1> : words <= 64 ? tree_map_kernel<2> : tree_map_kernel<4>,
+                           dim3(p.batch), 32 * warps, 0, s, p);
 }
 
 }  // namespace dflash

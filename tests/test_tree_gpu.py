@@ -838,3 +838,65 @@ def test_launches_and_trace_kinds(D):
     D.dflash_tree_commit(s.dims, s.cache, s.tree, i32([300]), o[1], o[0])
     assert [k for k, _ in D.dflash_trace_stop()] == kinds
     assert D.dflash_launch_count() == n + len(kinds) and D.dflash_status_get() == 0
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_wait_for_a_stream_that_was_joined(D, graph):
+    """Inputs that another stream writes late, after long products; the calling stream waits for its event only.
+    What the calls read before that would be other inputs, whose results differ."""
+    r = rng_of(21)
+    n, B, path = 64, 30, 12
+    parents = [u for _ in range(B) for u in T.random_tree(r, n, 5)]
+    tokens, posterior = ([int(x) for x in r.integers(0, 3, size=n * B)] for _ in range(2))
+    right = [i32(parents), i32(tokens), i32(posterior)]
+    wrong = [i32([i - 1 for _ in range(B) for i in range(n)]), torch.zeros_like(right[1]), torch.ones_like(right[2])]
+    logits = torch.randn(4, 2, 40000, device=DEV)
+    ins = [w.clone() for w in wrong] + [torch.zeros_like(logits)]
+    cu, kv = i32(np.arange(B + 1) * n), [n] * B
+    plan = D.ChunkPlan(cu, n * B, kv_lens=i32(kv))
+    tree = D.Tree(B, n, DEV)
+    ctx = i32(range(B))
+    o = [i32([0] * B), i32([[0] * path] * B), i32([0] * (B + 1)), i32([0] * B), i32([0] * B)]
+    sel = [torch.zeros((4, 3), dtype=t, device=DEV) for t in (torch.int32, torch.int32, torch.float32)]
+    ws = torch.empty(D.dflash_beam_workspace_bytes(4, 2, 40000, 3), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    big = torch.randn(4096, 4096, device=DEV)
+    out = torch.empty_like(big)
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                torch.mm(big, big, out=out)
+            for i, t in zip(ins, right + [logits]):
+                i.copy_(t)
+        D.dflash_beam_select(ins[3], None, 2, sel[0][:, :2], sel[1][:, :2], sel[2][:, :2], ws)   # of the zeros, or of both
+        main.wait_stream(side)
+        D.dflash_tree_accept(plan, *ins[:3], ctx, *o)
+        D.dflash_beam_select(ins[3], None, 3, *sel, ws)
+        D.dflash_tree_map(plan, tree, ins[0])
+
+    torch.mm(big, big, out=out)
+    if graph:
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+    for _ in range(3):
+        for i, t in zip(ins, wrong):
+            i.copy_(t)
+        ins[3].zero_()
+        [t.fill_(-3) for t in o + sel]
+        g.replay() if graph else step()
+        torch.cuda.synchronize()
+        got = dict(zip(("a", "path", "cu", "ctx", "anchor"), (t.tolist() for t in o)))
+        _check_accept(got, list(range(B)), [n] * B, parents, tokens, posterior, path)
+        for b in range(4):
+            t, i, _ = T.beam_select(np64(logits)[b], np.zeros(2), 3)
+            assert sel[0][b].tolist() == t.tolist() and sel[1][b].tolist() == i.tolist()
+        _, _, depths, masks, _ = T.tree_map(np.arange(B + 1) * n, kv, parents, [0] * B, [[]] * B, [[]] * B, n)
+        assert tree.depths.tolist() == [list(d) for d in depths]
+        got = tree.masks.cpu().numpy()
+        assert all((got[b, t] == T.words(masks[b][t], n)).all() for b in range(B) for t in range(n))
+    assert D.dflash_status_get() == 0
