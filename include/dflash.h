@@ -597,9 +597,10 @@ dflash_status dflash_tree_commit(const dflash_dims* dims, const dflash_kv_cache*
  * best first, equal scores by the lowest i * vocab + v:
  *   tokens[b][j] = v, parents[b][j] = parent_base + i, scores_out[b][j] = score
  * With beams 1 and k 1 that is the greedy token of each row; with parent_base the number of the
- * level's first node, parents are those of dflash_tree_map. Scores are compared in 64 bits, in which the
- * log-sum is within about 10^-8 (scores nearer than that to one another may change places), and
- * rounded to f32 once. A beam whose score is not finite, or whose row holds NaN, plus infinity or no
+ * level's first node, parents are those of dflash_tree_map. Scores are compared in 64 bits and
+ * rounded to f32 once. The log-sum in them is within 2 10^-6, and of rows in no special order within
+ * about 10^-8: scores of two beams that are nearer than that to one another may change places, those
+ * of one beam never do. A beam whose score is not finite, or whose row holds NaN, plus infinity or no
  * finite logit, has no probability: all its scores are minus infinity. So is that of a logit of
  * minus infinity.
  *   dtype       DFLASH_F32 or DFLASH_BF16, of the logits

@@ -45,7 +45,9 @@
 // converted, which leaves about 64 KB on their way, where bf16 has about 96 of 160 KB; at 4.7 and
 // 6.4 TB/s over 152 SMs both come to 2.1 to 2.3 us a load. Deeper rings have not been tried.
 //
-// Tried and slower. P as three E5M2 terms and V as stored, with no conversion (20 MMAs a tile
+// Tried and slower. Tiles fetched into L2 one to ten ahead of their loads, into the next item too (64
+// tokens 147 -> 167 us on E4M3; bf16, 32 blocks 69 -> 72 at one ahead, 100 at six): the loads pass the
+// same queue twice. P as three E5M2 terms and V as stored, with no conversion (20 MMAs a tile
 // for 16, and the terms cost the softmax 420 instructions: 64 tokens 150 -> 200 us). Keys x rows
 // for few rows, a key per thread and P through shared memory (64 rows 70 -> 132 us: at 10
 // cycles an instruction the four warps wait for tensor memory and for one another). Q repeated

@@ -8,6 +8,11 @@
 // a bit per step, each lane holding words of the mask, up to the first node whose mask is complete
 // (one of an earlier step, or of an earlier block of kBlock rows), which it takes over. So a row
 // costs its depth in shared-memory latencies, and a chain of thousands of rows stays linear.
+//
+// Bound by latency: 58 to 220 KB of masks are a few hundredths of a microsecond at the copy rate. 32 trees of
+// 64 nodes 3.0 us in a replayed graph, 16 new rows behind 200 to 900 nodes of 64 sequences 2.6 (5.3 and 4.7
+// call by call, which is the host's time): the launch, then three dependent loads (lengths, parents, the
+// masks taken over) and the walk.
 #include "tree.cuh"
 
 namespace dflash {
@@ -38,7 +43,7 @@ __global__ void __launch_bounds__(1024) tree_map_kernel(const TreeMapParams p) {
     return;
   }
   // kv 0: the step refused the sequence already
-  bool bad = kv != 0 && (t0 < 0 || n > p.max_nodes - t0 || kv - n < t0);
+  bool bad = kv != 0 && (t0 < 0 || n > p.max_nodes - t0 || kv < t0 + n);
   if (!bad && kv != 0) {
     bool mine = false;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {

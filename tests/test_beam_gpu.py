@@ -217,3 +217,18 @@ def test_select_many_rows_and_beams(D):
     x, s = random("f32", 2, 128, 5000, seed=14)
     check(D, x, s, 128)
     check(D, x[:, :1].expand(2, 128, 5000), s, 128)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("high", [11.9, 12.5, 39.0, 90.0])
+def test_select_sums_whose_terms_err_one_way(D, dtype, high):
+    """A few low logits, then one value over and over, so that no term's error makes up for another's. Of the
+    values near `high` the one whose product with log2 e rounds the furthest."""
+    v = torch.linspace(high - 0.5, high, 4001).to(TORCH[dtype])
+    t = v.float() * np.float32(np.log2(np.e))
+    err = (np64(t) - np64(v) * np.log2(np.e)) * (np64(v) < high)
+    x = torch.zeros((2, 2, 60000), dtype=TORCH[dtype])
+    for b, worst in enumerate((v[int(err.argmax())], v[int(err.argmin())])):
+        x[b, :, 9000:] = worst
+        x[b, 1, 9000:20000] -= 3
+    check(D, x.to(DEV), torch.tensor([[-1.0, -1.125], [0.0, 0.0]], device=DEV), 5)

@@ -109,6 +109,18 @@ def test_map_refuses(D):
     assert plan.kv_lens.tolist() == [0, 0, 9] and tr.tree.nodes.tolist() == [-1, 0, 4]
 
 
+@pytest.mark.parametrize("kv", [-2 ** 31, -2 ** 31 + 1, -1, 2, 2 ** 31 - 1])
+def test_map_of_any_length(D, kv):
+    """Three new rows: fewer rows held, also so few that the difference wraps, are refused."""
+    tr = Trees(D, [0], 32)
+    plan = D.ChunkPlan(i32([0, 3]), 3, kv_lens=i32([kv]), slots=i32([3] * 3))
+    D.dflash_tree_map(plan, tr.tree, i32([-1, 0, 0]))
+    good = kv >= 3
+    assert D.dflash_status_get() == (0 if good else D.DEV_TREE)
+    assert plan.positions.tolist() == ([kv - 3, kv - 2, kv - 2] if good else [-1] * 3)
+    assert plan.kv_lens.tolist() == [kv if good else 0] and tr.tree.nodes.tolist() == [3 if good else 0]
+
+
 def test_map_in_place_over_three_steps(D):
     tr = Trees(D, [0, 0], 64)
     tr.tree.nodes.zero_()
