@@ -7,8 +7,10 @@
 // so nothing has to be waited for. A CTA per sequence, layer and K or V.
 //
 // Bound by loads in flight. 16 layers of 64 sequences, paths of 4 to 16 nodes, 8 heads of 128 in bf16:
-// 64 MB read and written, 15.1 us in a replayed graph (4.2 TB/s; the copy rate allows 9.4 us): each CTA moves
-// a few KB behind three dependent loads (lengths, path, pages). Two layers of 32 sequences, 1.3 MB: 3.2 us.
+// 64 MB read and written, 14.5 us in a replayed graph (4.4 TB/s; the copy rate allows 9.4 us): each CTA moves
+// a few KB in runs of 256 bytes, behind three dependent loads (lengths, path, pages). Eight CTAs on an SM, by 64
+// registers: 16.0 us with as many registers as the loads would like, 14.7 with nine, 15.9 and 18.1 with ten and
+// twelve, which spill; four rows in flight instead of eight 15.5. Two layers of 32 sequences, 1.3 MB: 3.2 us.
 #include "tree.cuh"
 
 namespace dflash {
@@ -18,7 +20,7 @@ constexpr int kRows = 64;  // rows whose addresses are in shared memory at a tim
 constexpr int kAhead = 8;  // rows in flight per thread
 
 template <typename T>
-__global__ void __launch_bounds__(128) tree_commit_kernel(const TreeCommitParams p) {
+__global__ void __launch_bounds__(128, 8) tree_commit_kernel(const TreeCommitParams p) {
   __shared__ long long src[kRows], dst[kRows];  // row of KV head 0 in the layer, -1: not moved
   grid_wait();
   grid_trigger();
