@@ -209,26 +209,74 @@ __device__ __forceinline__ float float_of(uint32_t k) {
 constexpr int kSlots = 8;      // notes of a lane
 constexpr int kEntries = 160;  // of a warp's list: kBeamMax and 32 at least
 
-// Cuts a list of N entries (0: none), more than k of them, to the k best, best first, the others 0. Returns the
-// last one.
-template <int N>
-__device__ __forceinline__ u64 cut(u64* e, int k) {
+// Cuts a list of n entries in `slots` places (a multiple of 32; 0: none) to the k best, the others 0. Returns a
+// value that these reach and the others do not: the k-th largest logit's bits one by one, of those in which the
+// entries differ, then, among equal ones, the token's. FEW: with few registers, for calls out of the loop that reads
+// the logits: what a call may use, its caller cannot keep over it (256 rows of 131072 25.9 us, and 28.1 with the
+// halves of the entries in registers; 2 against 5 us a call). Counting those before each entry, and so sorting
+// them, took 5 us a call.
+static_assert(kEntries <= 32 * kSlots, "places of a list");
+template <bool FEW>
+__device__ __noinline__ u64 cut(u64* e, int slots, int n, int k) {
+  constexpr int UNROLL = FEW ? 1 : kSlots;
   const int lane = threadIdx.x & 31;
-  u64 mine[N / 32];
-  int rank[N / 32];
-#pragma unroll
-  for (int t = 0; t < N / 32; ++t) mine[t] = e[lane + 32 * t];
-#pragma unroll
-  for (int t = 0; t < N / 32; ++t) rank[t] = mine[t] != 0 ? rank_of(e, N, mine[t]) : N;
+  const uint32_t* half = reinterpret_cast<const uint32_t*>(e);  // of an entry: the token's, the logit's
+  uint32_t limit[2] = {0, 1};
+  if (n > k) {
+#pragma unroll 1
+    for (int word = 1; word >= 0; --word) {
+      uint32_t kept[UNROLL];
+      auto load = [&](int t) -> uint32_t {  // 0: not in question
+        const int i = lane + 32 * t;
+        const uint32_t hi = i < slots ? half[2 * i + 1] : 0;
+        return hi != 0 && (word == 1 || hi == limit[1]) ? half[2 * i + word] : 0;
+      };
+      auto key = [&](int t) -> uint32_t { return FEW ? load(t) : kept[t % UNROLL]; };
+      uint32_t any = 0, all = 0xffffffffu;
+#pragma unroll UNROLL
+      for (int t = 0; t < kSlots; ++t) {
+        const uint32_t x = kept[t % UNROLL] = load(t);
+        if (x != 0) any |= x, all &= x;
+      }
+      all = __reduce_and_sync(0xffffffffu, all);
+      const uint32_t differ = __reduce_or_sync(0xffffffffu, any) & ~all;
+      uint32_t least = 0;
+#pragma unroll 1
+      for (uint32_t left = differ; left != 0 && n != k;) {
+        const uint32_t bit = 0x80000000u >> __clz(left), trial = least | bit;
+        left ^= bit;
+        int c = 0;
+#pragma unroll UNROLL
+        for (int t = 0; t < kSlots; ++t) c += (key(t) & differ) >= trial;
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (c >= k) least = trial, n = c;
+      }
+      least |= all;
+      (word == 1 ? limit[1] : limit[0]) = least;
+      if (n == k) break;
+      int sure = 0;  // (of the logits: what is above the k-th stays, and the rest are alike)
+#pragma unroll UNROLL
+      for (int t = 0; t < kSlots; ++t) sure += key(t) > least;
+      sure = __reduce_add_sync(0xffffffffu, sure);
+      n -= sure, k -= sure;
+    }
+  }
+  const u64 last = (u64)limit[1] << 32 | limit[0];
+  int at = 0;
+#pragma unroll 1
+  for (int i = lane; i < slots; i += 32) {
+    const u64 v = e[i];
+    const bool in = v >= last;
+    const unsigned who = __ballot_sync(0xffffffffu, in);
+    __syncwarp();
+    if (in) e[at + __popc(who & ((1u << lane) - 1))] = v;
+    at += __popc(who);
+    __syncwarp();
+  }
+#pragma unroll 1
+  for (int i = at + lane; i < slots; i += 32) e[i] = 0;
   __syncwarp();
-#pragma unroll
-  for (int t = 0; t < N / 32; ++t) e[lane + 32 * t] = 0;
-  __syncwarp();
-#pragma unroll
-  for (int t = 0; t < N / 32; ++t)
-    if (rank[t] < k) e[rank[t]] = mine[t];
-  __syncwarp();
-  return e[k - 1];
+  return last;
 }
 
 // A warp's notes, one lane's below one another: drops those below the bound and, if a lane is still full,
@@ -253,9 +301,9 @@ __device__ __noinline__ Cleared clear_notes(u64* notes, int n, int k, float boun
   const int all = __reduce_add_sync(0xffffffffu, kept);
   __syncwarp();
   float later = bound;
-  if (all > k) later = fmaxf(bound, float_of((uint32_t)(cut<32 * kSlots>(notes, k) >> 32) + 1));
-  else cut<32 * kSlots>(notes, all);  // (they are spread, but all of them stay)
   const int left = min(all, k);
+  const u64 least = cut<true>(notes, 32 * kSlots, all, left);  // (spread over the lanes, even if all of them stay)
+  if (all > k) later = fmaxf(bound, float_of((uint32_t)(least >> 32) + 1));
   return {later, left > lane ? (left - lane + 31) / 32 : 0};
 }
 
@@ -298,7 +346,7 @@ __device__ __noinline__ int enter(const T* x, int begin, int end, u64* notes, in
       if (count + __popc(who) > kEntries) {
         for (int i = count + lane; i < kEntries; i += 32) list[i] = 0;
         __syncwarp();
-        least = cut<kEntries>(list, k);
+        least = cut<false>(list, kEntries, count, k);
         count = k;
         who = __ballot_sync(0xffffffffu, (who >> lane & 1) != 0 && entry > least);
       }
@@ -310,7 +358,7 @@ __device__ __noinline__ int enter(const T* x, int begin, int end, u64* notes, in
   if (count > k) {
     for (int i = count + lane; i < kEntries; i += 32) list[i] = 0;
     __syncwarp();
-    cut<kEntries>(list, k);
+    cut<false>(list, kEntries, count, k);
     count = k;
   }
   if (lane < 3 && count + lane < kEntries) list[count + lane] = 0;
@@ -449,10 +497,10 @@ __global__ void __launch_bounds__(kThreads, 3) beam_scan_kernel(const Scan p) {
     int begin, end;
     const T* x = row_of(piece, begin, end);
     const int shift = (int)((uintptr_t)x & 15);
-    // Warps whose lanes all have an element in the first tile have a say in the bound: the q-th largest of
-    // each one's lanes, and of these the s-th largest
-    const int voters = min(kWarps, (end - begin + L - 1) / (32 * L)), some = max(1, (3 * voters) / 4);
-    const int q = voters ? (p.k + some - 1) / some : 64, nth = (p.k + q - 1) / q;
+    // Warps whose lanes all have an element in the first tile (or the first one) have a say in the bound: the
+    // q-th largest of each one's lanes, and of these the s-th largest
+    const int voters = min(kWarps, max(1, (end - begin + L - 1) / (32 * L))), some = max(1, (3 * voters) / 4);
+    const int q = (p.k + some - 1) / some, nth = (p.k + q - 1) / q;
     int noted = 0;                               // by this lane
     int seen = 0, due = 2;                       // tiles
     typename Vec<T>::Most best = Vec<T>::kNone;  // this lane's largest so far
