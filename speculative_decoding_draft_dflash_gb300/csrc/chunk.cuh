@@ -168,6 +168,7 @@ __device__ __forceinline__ Seq<TREE> load_seq(const Split<TOKENS, TREE>& p, int 
 // (rows * G fits 31 bits)
 template <bool TOKENS, bool TREE>
 __device__ __forceinline__ int n_items(const Split<TOKENS, TREE>& p, const Seq<TREE>& s) {
+  if (TOKENS ? s.n <= p.item_tokens : s.n * p.G <= p.item_rows) return s.n > 0;
   if (TOKENS) return (int)((unsigned)(s.n + p.item_tokens - 1) / (unsigned)p.item_tokens);
   return (int)((unsigned)(s.n * p.G + p.item_rows - 1) / (unsigned)p.item_rows);
 }
@@ -203,31 +204,143 @@ __device__ __forceinline__ int item_units(const Split<TOKENS, TREE>& p, const Se
   return p.item_cost + tile_units(p, s, t) * item_keys(p, s, t).y;
 }
 
+// a / b for a >= 0, b > 0.
+static __device__ __noinline__ long long divide64(long long a, int b) { return a / b; }
+__device__ __forceinline__ long long divide(long long a, int b) {
+  return a >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : divide64(a, b);
+}
+
+// The cost line's shares: CTA c has [from(c), from(c + 1)), none but the first ctas. A share is large
+// enough for a key tile, so that every CTA inside a cut item has at least one.
+struct Shares {
+  long long each;   // units of a share; the first `more` have one more
+  int more, ctas;
+  template <bool TOKENS, bool TREE>
+  __device__ __forceinline__ void init(const Split<TOKENS, TREE>& p, long long total) {
+    const int least = max(p.tile_cost, p.half_cost);
+    ctas = (int)gridDim.x;
+    if (total < (long long)ctas * least) ctas = max(1, (int)total / least);
+    each = divide(total, ctas);
+    more = (int)(total - each * ctas);
+  }
+  __device__ __forceinline__ long long from(int c) const { return c < ctas ? c * each + min(c, more) : ctas * each + more; }
+};
+
 // A CTA's share and where it starts.
 template <bool TREE>
 struct Start {
   long long begin, end;  // on the cost line
-  long long total;
-  int ctas;              // CTAs with a share
+  Shares shares;
   int b, kvh, t;         // the item that holds `begin`
   int off;               // cost units of it before `begin`
   Seq<TREE> s;           // its sequence
 };
 
-// CTAs that get a share: large enough for a key tile, so that every CTA inside a cut item has
-// at least one.
-template <bool TOKENS, bool TREE>
-__device__ __forceinline__ int active_ctas(const Split<TOKENS, TREE>& p, long long total, int ctas) {
-  const int least = max(p.tile_cost, p.half_cost);
-  return total >= (long long)ctas * least ? ctas : max(1, (int)(total / least));
-}
-static __device__ __noinline__ long long bound(long long total, int active, int c) {
-  return total * c / active;
-}
-
 // Shared scratch of locate: every sequence and its cost.
 template <bool TREE>
 constexpr size_t kLocateBytes = sizeof(Seq<TREE>) + sizeof(long long);  // per sequence
+
+// The KV head and the item of a sequence that hold cost unit `rest` of it; per_head: of one of its heads. By a
+// whole warp.
+template <bool TOKENS, bool TREE>
+__device__ __noinline__ void locate_item(const Split<TOKENS, TREE>& p, const Seq<TREE>& s, long long rest, long long per_head,
+                                            Start<TREE>* st) {
+  const int lane = threadIdx.x & 31;
+  int kvh = 0;
+  while (rest >= per_head) {  // (n_kv steps at most)
+    rest -= per_head;
+    ++kvh;
+  }
+  // the item: scan their costs 32 at a time (their sum fits 31 bits: the capacity does)
+  const int items = n_items(p, s);
+  int t = 0;
+#pragma unroll 1
+  for (int base = 0; base < items; base += 32) {
+    const int u = base + lane;
+    const int w = u < items ? item_units(p, s, u) : 0;
+    int v = w;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, v > rest);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      t = base + l;
+      rest -= __shfl_sync(0xffffffffu, v - w, l);
+      break;
+    }
+    rest -= __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (lane == 0) {
+    st->kvh = kvh;
+    st->t = t;
+    st->off = (int)rest;
+    st->s = s;
+  }
+}
+
+// locate for at most 32 sequences by one warp, in registers: 32, 16, .. lanes share a sequence. All of this comes
+// before the first load, and is run once: an instruction costs about 40 cycles then, as none is in the cache, so
+// what counts is how few there are, and that parameters are operands, not loads (16 rows behind 1023 of one
+// sequence: 15.8 us with locate, 13.7; 32 blocks of 16 rows 69.4 and 66.8; one token in f32 19.2 and 16.8).
+template <bool TOKENS, bool TREE>
+__device__ __forceinline__ void locate_by_warp(const Split<TOKENS, TREE>& p, Start<TREE>* st, unsigned* status) {
+  const int lane = threadIdx.x & 31;
+  const int shift = __clz(p.batch - 1) - 27;  // log2 of a sequence's lanes (one sequence: 32 - 27)
+  const int b = lane >> shift, lanes = 1 << shift;
+  Seq<TREE> s = {};
+  unsigned bad = 0;
+  int items = 0;
+  if (b < p.batch) {
+    s = load_seq(p, b, &bad);
+    items = n_items(p, s);
+  }
+  if (bad && blockIdx.x == 0) atomicOr(status, bad);
+  long long sum = 0;
+#pragma unroll 1
+  for (int t = lane & (lanes - 1); t < items; t += lanes) sum += item_units(p, s, t);
+#pragma unroll 1
+  for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const long long cost = sum * p.n_kv;
+  long long upto = (lane & (lanes - 1)) == 0 ? cost : 0;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
+  }
+  const long long total = __shfl_sync(0xffffffffu, upto, 31);
+  Shares shares;
+  shares.init(p, total);
+  const long long begin = shares.from(blockIdx.x), end = shares.from(blockIdx.x + 1);
+  int l = 0;
+  if (begin < end) {  // the first sequence whose prefix exceeds begin
+    l = __ffs(__ballot_sync(0xffffffffu, upto > begin)) - 1;
+    long long rest = begin - (upto - cost);
+    if (__any_sync(0xffffffffu, lane == l && items > 1)) {
+      s.row0 = __shfl_sync(0xffffffffu, s.row0, l);
+      s.n = __shfl_sync(0xffffffffu, s.n, l);
+      s.kv = __shfl_sync(0xffffffffu, s.kv, l);
+      if constexpr (TREE) s.ctx = __shfl_sync(0xffffffffu, s.ctx, l);
+      locate_item(p, s, __shfl_sync(0xffffffffu, rest, l), __shfl_sync(0xffffffffu, sum, l), st);
+    } else if (lane == l) {  // one item a head
+      int kvh = 0;
+      for (; rest >= sum; rest -= sum) ++kvh;
+      st->kvh = kvh;
+      st->t = 0;
+      st->off = (int)rest;
+      st->s = s;
+    }
+  }
+  if (lane == 0) {
+    st->begin = begin;
+    st->end = end;
+    st->shares = shares;
+    st->b = l >> shift;
+  }
+  __syncwarp();
+}
 
 // Run by all threads of the CTA; `scratch` is 16-byte aligned shared memory of kLocateBytes per
 // sequence (free again after the call and a __syncthreads), `st` shared. A thread per sequence
@@ -272,10 +385,9 @@ __device__ __noinline__ void locate(const Split<TOKENS, TREE>& p, void* scratch,
       carry = __shfl_sync(0xffffffffu, v, 31);
     }
     __syncwarp();
-    const int active = active_ctas(p, carry, (int)gridDim.x);
-    const int c = (int)blockIdx.x;
-    const long long begin = c < active ? bound(carry, active, c) : carry;
-    const long long end = c < active ? bound(carry, active, c + 1) : carry;
+    Shares shares;
+    shares.init(p, carry);
+    const long long begin = shares.from(blockIdx.x), end = shares.from(blockIdx.x + 1);
     int b = 0;
     if (begin < end) {  // the first sequence whose prefix exceeds begin
       int lo = 0, hi = p.batch - 1;
@@ -286,47 +398,12 @@ __device__ __noinline__ void locate(const Split<TOKENS, TREE>& p, void* scratch,
       b = lo;
       const Seq<TREE> s = seq[b];
       const long long before = b > 0 ? cost[b - 1] : 0;
-      const long long per_head = bound(cost[b] - before, p.n_kv, 1);
-      int kvh = 0;
-      long long rest = begin - before;
-      while (rest >= per_head) {  // (n_kv steps at most)
-        rest -= per_head;
-        ++kvh;
-      }
-      // the item: scan their costs 32 at a time (their sum fits 31 bits: the capacity does)
-      const int items = n_items(p, s);
-      int t = 0;
-#pragma unroll 1
-      for (int base = 0; base < items; base += 32) {
-        const int u = base + lane;
-        const int w = u < items ? item_units(p, s, u) : 0;
-        int v = w;
-#pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v += x;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, v > rest);
-        if (past) {
-          const int l = __ffs(past) - 1;
-          t = base + l;
-          rest -= __shfl_sync(0xffffffffu, v - w, l);
-          break;
-        }
-        rest -= __shfl_sync(0xffffffffu, v, 31);
-      }
-      if (lane == 0) {
-        st->kvh = kvh;
-        st->t = t;
-        st->off = (int)rest;
-        st->s = s;
-      }
+      locate_item(p, s, begin - before, divide(cost[b] - before, p.n_kv), st);
     }
     if (lane == 0) {
       st->begin = begin;
       st->end = end;
-      st->total = carry;
-      st->ctas = active;
+      st->shares = shares;
       st->b = b;
     }
   }
@@ -351,18 +428,17 @@ struct Piece<true> : PieceOf {
 // Walks a CTA's share piece by piece (one thread, or all threads of a warp alike).
 template <bool TOKENS, bool TREE>
 struct Walker {
-  Split<TOKENS, TREE> p;
+  const Split<TOKENS, TREE>& p;
   Seq<TREE> s;
-  long long at, end, total;
-  int ctas, b, kvh, t, off;
+  long long at, end;
+  Shares shares;
+  int b, kvh, t, off;
   int4 merge;  // what to merge: {b, kvh, t, pieces}, pieces 0 when nothing was cut here
 
-  __device__ __forceinline__ void init(const Split<TOKENS, TREE>& split, const Start<TREE>& st) {
-    p = split;
+  __device__ __forceinline__ Walker(const Split<TOKENS, TREE>& split, const Start<TREE>& st) : p(split) {
     at = st.begin;
     end = st.end;
-    total = st.total;
-    ctas = st.ctas;
+    shares = st.shares;
     b = st.b;
     kvh = st.kvh;
     t = st.t;
@@ -407,7 +483,7 @@ struct Walker {
         // the start of an item that goes on: how many CTAs finish it
         const long long item_end = at + (whole - off);
         int c = (int)blockIdx.x + 1, n = 1;
-        while (bound(total, ctas, c) < item_end) {
+        while (shares.from(c) < item_end) {
           ++c;
           ++n;
         }

@@ -317,10 +317,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DP)) chunk_attn_simt_ker
                               p.window, RI, 0, RI / (RI > 64 ? 2 : 4), 6, 2, 6, RI > 64 ? 3 : 2, p.tree.nodes, p.tree.max_nodes};
   grid_wait();
   grid_trigger();  // the merge may be scheduled
-  chunk::locate(split, smem4, &start, p.status);
-  chunk::Walker<false, TREE> walk;
-  walk.init(split, start);
+  if (p.batch > 32)
+    chunk::locate(split, smem4, &start, p.status);
+  else if (threadIdx.x < 32)
+    chunk::locate_by_warp(split, &start, p.status);
   __syncthreads();
+  chunk::Walker<false, TREE> walk(split, start);
   // columns beyond d_h stay zero
   for (int i = threadIdx.x; i < 2 * TK * LD; i += kThreads) Ks[i] = 0.f;
   chunk::Piece<TREE> w;

@@ -45,7 +45,11 @@
 // converted, which leaves about 64 KB on their way, where bf16 has about 96 of 160 KB; at 4.7 and
 // 6.4 TB/s over 152 SMs both come to 2.1 to 2.3 us a load. Deeper rings have not been tried.
 //
-// Tried and slower. Tiles fetched into L2 one to ten ahead of their loads, into the next item too (64
+// The start: about 5 us from the launch to the first load, of lengths, split and page look-up one after another,
+// run by the loading warp alone where there are at most 32 sequences.
+//
+// Tried and slower. The softmax run once on nothing while the work is looked for, so that its code is in the
+// instruction cache (16 rows behind 1023 13.7 -> 14.1 us: it takes the fetches from the loading warp). Tiles fetched into L2 one to ten ahead of their loads, into the next item too (64
 // tokens 147 -> 167 us on E4M3; bf16, 32 blocks 69 -> 72 at one ahead, 100 at six): the loads pass the
 // same queue twice. P as three E5M2 terms and V as stored, with no conversion (20 MMAs a tile
 // for 16, and the terms cost the softmax 420 instructions: 64 tokens 150 -> 200 us). Keys x rows
@@ -545,8 +549,11 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
   grid_trigger();  // the merge may be scheduled
   // the work split, in what becomes the K / V ring
   static_assert(5 * TILE >= chunk::kLocateBytes<TREE> * (TREE ? kTreeMaxBatch : kChunkMaxBatch), "scratch of the work split");
-  chunk::locate(p.split, smem + PL::OFF_KV, &sh.start, p.status);
-  ptx::fence_proxy_async_smem();  // TMA overwrites them
+  const bool few = p.split.batch <= 32;  // sequences: the loading warp finds the share by itself
+  if (!few) {
+    chunk::locate(p.split, smem + PL::OFF_KV, &sh.start, p.status);
+    ptx::fence_proxy_async_smem();  // TMA overwrites them
+  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -798,15 +805,15 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
     reg_dec<PL::REG_REST>();
     if (warp == 8) {
       // ------------------------------------------------------------------ work list, TMA
+      if (few) chunk::locate_by_warp(p.split, &sh.start, p.status);
       if (lane == 0) {
-        chunk::Walker<true, TREE> walk;
-        walk.init(p.split, sh.start);
+        chunk::Walker<true, TREE> walk(p.split, sh.start);
         chunk::Piece<TREE> w;
         int count[2] = {0, 0}, nq[2] = {0, 0};  // tiles (bf16: of both kinds), Q tiles
-        chunk::Piece<TREE> cur;
+        chunk::Piece<TREE> cur = {};  // (before the first: no tiles)
         bool more = true;
 #pragma unroll 1
-        for (int n = -1;; ++n) {  // item n's tiles are issued once item n + 1 is known
+        for (int n = -1;; ++n) {  // item n + 1 is looked for once item n's first loads are on their way
           if (n >= 0) {
             const int slot = n % kRing;
             if (n >= kRing && !wait(sh.ite[slot], n / kRing - 1)) break;
@@ -817,13 +824,12 @@ __global__ void __launch_bounds__(Plan<FP8>::THREADS, 1) chunk_attn_tc_kernel(co
             if (!more) break;
             cur = w;
           }
+          const Geometry<TREE> g(p, cur);
           more = walk.next(&w);
           if (n < 0) continue;
-          const Geometry<TREE> g(p, cur);
-          if (g.T == 0) continue;
           const int32_t* table = p.table ? p.table + (size_t)cur.b * p.pps + (g.key0 >> 7) : nullptr;
           bool stop = false;
-          int page = table ? table[0] : 0;
+          int page = table && g.T > 0 ? table[0] : 0;
 #pragma unroll 1
           for (int i = 0, jk = 0, jv = 0; i <= 2 * g.T; ++i) {
             // after the first K tile: Q, unless nothing is left to load
