@@ -216,8 +216,8 @@ struct Shares {
   long long each;   // units of a share; the first `more` have one more
   int more, ctas;
   template <bool TOKENS, bool TREE>
-  __device__ __forceinline__ void init(const Split<TOKENS, TREE>& p, long long total) {
-    const int least = max(p.tile_cost, p.half_cost);
+  __device__ __forceinline__ void init(const Split<TOKENS, TREE>& p, long long total, int tiles = 1) {
+    const int least = tiles * max(p.tile_cost, p.half_cost);
     ctas = (int)gridDim.x;
     if (total < (long long)ctas * least) ctas = max(1, (int)total / least);
     each = divide(total, ctas);
@@ -311,8 +311,17 @@ __device__ __forceinline__ void locate_by_warp(const Split<TOKENS, TREE>& p, Sta
     if (lane >= o) upto += u;
   }
   const long long total = __shfl_sync(0xffffffffu, upto, 31);
+  // Fewer heads than eight: an item may be cut into as many pieces as there are CTAs, which the merge adds up one
+  // after another (0.33 us each, a tile of a share about 1.1): s tiles a share and T / s pieces of T tiles are
+  // the quickest around s = sqrt(0.3 T). 16 rows behind 32767 of one KV head, by s: 1: 56.4 us, 2: 44.8, 4: 30.0,
+  // 6: 25.8, the rule's 8 28.5; eight heads and 9 tiles: 13.6, 13.8, 17.2, 18.9.
+  int tiles = 1;
+  if (TOKENS && p.batch * p.n_kv < 8) {
+    const int item = __reduce_max_sync(0xffffffffu, items > 0 ? (int)__fdividef((float)sum, (float)items) : 1);
+    tiles = max(1, (int)__fdividef(1.f, rsqrtf((float)(item / (4 * p.tile_cost)))));  // (0: 1 / infinity)
+  }
   Shares shares;
-  shares.init(p, total);
+  shares.init(p, total, tiles);
   const long long begin = shares.from(blockIdx.x), end = shares.from(blockIdx.x + 1);
   int l = 0;
   if (begin < end) {  // the first sequence whose prefix exceeds begin

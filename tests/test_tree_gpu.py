@@ -912,3 +912,42 @@ def test_calls_wait_for_a_stream_that_was_joined(D, graph):
         got = tree.masks.cpu().numpy()
         assert all((got[b, t] == T.words(masks[b][t], n)).all() for b in range(B) for t in range(n))
     assert D.dflash_status_get() == 0
+
+
+@pytest.mark.parametrize("kv,heads,paged", [("bf16", (8, 1, 128), True), ("fp8", (8, 2, 128), True), ("f32", (2, 1, 64), False)])
+@pytest.mark.parametrize("ctx,before,rows", [([30000], [0], [1]), ([20001], [100], [16]), ([9000], [0], [130]),
+                                             ([5000, 0, 300], [7, 0, 0], [3, 40, 1])])
+def test_attn_few_heads_over_long_contexts(D, kv, heads, paged, ctx, before, rows):
+    """One item cut into many pieces, of more than a tile each."""
+    s = TreeStep(D, kv, heads, ctx, before, rows, paged=paged, pad=1, seed=31)
+    s.map(), s.tree_map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    out = torch.empty_like(q)
+    s.append(q)
+    for window in (0, 4000):
+        s.tree_attn(q, out, window)
+        s.check_tree(q, out, window)
+    assert D.dflash_status_get() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("batch", [1, 2, 3, 4, 5, 8, 9, 16, 17, 31, 32, 33, 64])
+def test_attn_any_number_of_sequences(D, kv, batch):
+    """Both ways of finding a share of the work; empty sequences, one of several items, refused ones between."""
+    r = rng_of(batch)
+    rows = [int(n) for n in r.integers(0, 20, size=batch)]
+    rows[batch // 2] = 150
+    ctx = [int(c) for c in r.integers(0, 500, size=batch)]
+    s = TreeStep(D, kv, (4, 2, 64 if kv == "f32" else 128), ctx, [0] * batch, rows, paged=kv != "f32", seed=batch)
+    s.map(), s.tree_map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    out = torch.full_like(q, float("nan"))
+    s.append(q)
+    refused = [b for b in range(batch) if rows[b] and b % 5 == 4 and b != batch // 2]
+    for b in refused:
+        s.plan.kv_lens[b] = 0
+    s.tree_attn(q, out)
+    s.check_tree(q, out, skip=refused)
+    for b in refused:
+        assert (out[int(s.cu[b]):int(s.cu[b + 1])] == 0).all()
+    assert D.dflash_status_get() == 0
