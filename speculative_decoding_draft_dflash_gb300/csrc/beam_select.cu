@@ -940,20 +940,27 @@ cudaError_t merge_rows(const Merge& p, int batch, cudaStream_t s) {
                            s, p);
 }
 
+// Both ways to cut a call's rows (one per beam, or one shared by them) and the workspace, which holds either.
+struct Sizes {
+  Cut each, shared;
+  size_t pieces;
+};
+Sizes sizes_of(int batch, int beams, int vocab, int k) {
+  Sizes z;
+  z.each = z.shared = cut_of(batch * beams, beams, vocab, k);
+  if (beams > 1) z.shared = cut_of(batch, beams, vocab, k);
+  const size_t e = (size_t)batch * beams * z.each.splits, s = (size_t)batch * z.shared.splits;
+  z.pieces = e > s ? e : s;
+  return z;
+}
 struct Carved {
   u64* lists;
   Piece* pieces;
 };
-// (rows: of the call with a row per beam, which needs the most)
-Carved carve(Carver& cv, int batch, int beams, int vocab, int k) {
-  size_t pieces = 0;
-  for (int rows : {batch, batch * beams}) {  // a shared row per sequence, or one per beam
-    const size_t n = (size_t)rows * cut_of(rows, beams, vocab, k).splits;
-    pieces = n > pieces ? n : pieces;
-  }
+Carved carve(Carver& cv, const Sizes& z, int k) {
   Carved c;
-  c.lists = cv.take<u64>(pieces * k);
-  c.pieces = cv.take<Piece>(pieces);
+  c.lists = cv.take<u64>(z.pieces * k);
+  c.pieces = cv.take<Piece>(z.pieces);
   return c;
 }
 
@@ -961,27 +968,30 @@ Carved carve(Carver& cv, int batch, int beams, int vocab, int k) {
 
 size_t beam_workspace(int batch, int beams, int vocab, int k) {
   Carver cv(nullptr, ~size_t(0));
-  carve(cv, batch, beams, vocab, k);
+  carve(cv, sizes_of(batch, beams, vocab, k), k);
   return cv.off;
 }
 
-cudaError_t beam_select(int dtype, const BeamParams& a, cudaStream_t s) {
-  Carver cv(a.workspace, ~size_t(0));
-  const Carved c = carve(cv, a.batch, a.beams, a.vocab, a.k);
+dflash_status beam_select(int dtype, const BeamParams& a, size_t ws_bytes, cudaStream_t s) {
+  const Sizes sizes = sizes_of(a.batch, a.beams, a.vocab, a.k);
+  Carver cv(a.workspace, ws_bytes);
+  const Carved c = carve(cv, sizes, a.k);
+  if (!cv.ok) return DFLASH_ERR_WORKSPACE;
   const int per_seq = a.ld_beam == 0 ? 1 : a.beams, rows = a.batch * per_seq;
-  const Cut cut = cut_of(rows, a.beams, a.vocab, a.k);
+  const Cut cut = per_seq == 1 ? sizes.shared : sizes.each;
   const int splits = cut.splits;
   const Scan scan = {a.logits, a.ld_seq, a.ld_beam, c.lists, c.pieces, a.vocab, per_seq, splits, cut.chunk, a.k, rows * splits};
   // short pieces: 16 bytes a lane and tile, so that more lanes have some
   const bool fine = cut.chunk <= kThreads * 16;
   cudaError_t e = dtype == DFLASH_F32 ? (fine ? scan_rows<float, 1>(scan, s) : scan_rows<float, 4>(scan, s))
                         : (fine ? scan_rows<bf16, 1>(scan, s) : scan_rows<bf16, 4>(scan, s));
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess) return cuda_status(e);
   const Merge merge = {c.lists, c.pieces, a.scores, a.tokens, a.parents, a.scores_out, a.ld_out,
                        a.beams, per_seq, splits, a.k, a.vocab, a.parent_base};
   // Four warps for few candidates of few rows: such sequences are many, and share an SM (2048 rows, greedy: 57 us
   // with 128 threads, 72 with 512; 64 sequences of 8 beams, k 8: 34 and 31)
-  return per_seq * splits <= 4 && (long long)a.beams * splits * a.k <= 128 ? merge_rows<128>(merge, a.batch, s) : merge_rows<512>(merge, a.batch, s);
+  const bool small = per_seq * splits <= 4 && (long long)a.beams * splits * a.k <= 128;
+  return cuda_status(small ? merge_rows<128>(merge, a.batch, s) : merge_rows<512>(merge, a.batch, s));
 }
 
 }  // namespace dflash

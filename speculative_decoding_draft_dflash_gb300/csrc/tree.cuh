@@ -66,6 +66,6 @@ struct BeamParams {
   int batch, beams, vocab, k, parent_base;
 };
 size_t beam_workspace(int batch, int beams, int vocab, int k);
-cudaError_t beam_select(int dtype, const BeamParams& p, cudaStream_t s);
+dflash_status beam_select(int dtype, const BeamParams& p, size_t ws_bytes, cudaStream_t s);  // or DFLASH_ERR_WORKSPACE
 
 }  // namespace dflash

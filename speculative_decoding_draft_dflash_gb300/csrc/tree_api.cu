@@ -157,7 +157,6 @@ DFLASH_API dflash_status dflash_beam_select(int dtype, const void* logits, long 
   if (!aligned4(tokens) || (parents && !aligned4(parents)) || (scores_out && !aligned4(scores_out)) ||
       (scores && !aligned4(scores)) || !workspace || ((uintptr_t)workspace & 255))
     return DFLASH_ERR_INVALID_ARG;
-  if (ws_bytes < beam_workspace(batch, beams, vocab, k)) return DFLASH_ERR_WORKSPACE;
   BeamParams p;
   memset(&p, 0, sizeof(p));
   p.logits = logits;
@@ -174,5 +173,5 @@ DFLASH_API dflash_status dflash_beam_select(int dtype, const void* logits, long 
   p.vocab = vocab;
   p.k = k;
   p.parent_base = parent_base;
-  return cuda_status(beam_select(dtype, p, stream));
+  return beam_select(dtype, p, ws_bytes, stream);
 }

@@ -546,14 +546,16 @@ def _array(t, what, dtype, numel, device):
 
 def _int_arrays(device, names, tensors, sizes):
     """_array of several int32 tensors: one loop instead of as many calls (0.2 us of host time each)."""
-    i32, out = torch.int32, []
-    for what, t, n in zip(names, tensors, sizes):
-        if isinstance(t, torch.Tensor) and t.dtype is i32 and t.get_device() == device and t.numel() >= n and \
-                t.is_contiguous():
-            out.append(t.data_ptr())
+    i32 = torch.int32
+    try:
+        for t, n in zip(tensors, sizes):
+            if t.dtype is not i32 or t.get_device() != device or t.numel() < n or not t.is_contiguous():
+                break
         else:
-            out.append(_array(t, what, i32, n, device))
-    return out
+            return [t.data_ptr() for t in tensors]
+    except AttributeError:  # None, or an address
+        pass
+    return [_array(t, what, i32, n, device) for what, t, n in zip(names, tensors, sizes)]
 
 
 def _chunk(plan, desc, cache):
@@ -698,11 +700,12 @@ def _k_rows(t, what, dtype, batch, k, device):
     """(address, elements between rows) of an output [batch][>= k] whose rows are dense."""
     if t is None:
         return None, None
-    if t.dtype is not dtype or t.get_device() != device or t.dim() != 2 or t.shape[0] < batch or t.shape[1] < k or \
-            (t.stride(1) != 1 and k > 1):
-        raise ValueError(f"{what}: {t.dtype} of shape {tuple(t.shape)}, strides {t.stride()} on device "
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not dtype or t.get_device() != device or len(shape) != 2 or shape[0] < batch or shape[1] < k or \
+            (stride[1] != 1 and k > 1):
+        raise ValueError(f"{what}: {t.dtype} of shape {tuple(shape)}, strides {stride} on device "
                          f"{t.get_device()}; the call needs {dtype} [{batch}][{k}] on device {device}")
-    return t.data_ptr(), t.stride(0) if batch > 1 else k
+    return t.data_ptr(), stride[0] if batch > 1 else k
 
 
 def dflash_beam_select(logits, scores, k, tokens, parents, scores_out, workspace, parent_base=0, stream=None):
@@ -710,9 +713,10 @@ def dflash_beam_select(logits, scores, k, tokens, parents, scores_out, workspace
     bfloat16, of any strides between rows (a row expanded over the beams is read once); scores
     float32 [batch][beams] or None; tokens, parents and scores_out [batch][k], their rows alike far apart
     (slices of node arrays are fine), the latter two may be None."""
-    if not logits.is_cuda or logits.dim() != 3 or (logits.shape[2] > 1 and logits.stride(2) != 1):
+    shape, stride, dev, k = logits.shape, logits.stride(), logits.get_device(), int(k)
+    if dev < 0 or len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
         raise ValueError("logits: expected a CUDA tensor [batch][beams][vocab] with dense rows")
-    (batch, beams, vocab), dev, k = logits.shape, logits.get_device(), int(k)
+    batch, beams, vocab = shape
     _on_current("logits", dev)
     tp, ld = _k_rows(tokens, "tokens", torch.int32, batch, k, dev)
     pp, ldp = _k_rows(parents, "parents", torch.int32, batch, k, dev)
@@ -721,7 +725,9 @@ def dflash_beam_select(logits, scores, k, tokens, parents, scores_out, workspace
         raise ValueError(f"tokens, parents, scores_out: rows {ld}, {ldp}, {lds} elements apart, the call needs one distance")
     if isinstance(workspace, torch.Tensor) and workspace.get_device() != dev:
         raise ValueError(f"workspace: on device {workspace.get_device()}, the logits are on {dev}")
-    _check(_lib.dflash_beam_select(dtype_code(logits.dtype), logits.data_ptr(), logits.stride(0), logits.stride(1),
+    dtype = logits.dtype
+    code = DFLASH_BF16 if dtype is torch.bfloat16 else dtype_code(dtype)
+    _check(_lib.dflash_beam_select(code, logits.data_ptr(), stride[0], stride[1],
                                    _array(scores, "scores", torch.float32, batch * beams, dev), batch, beams, vocab, k,
                                    int(parent_base), tp, pp, sp, ld, *_ws(workspace), _stream(stream)),
            "dflash_beam_select")
