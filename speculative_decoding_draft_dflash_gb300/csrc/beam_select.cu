@@ -31,11 +31,11 @@
 // one way, as where a row repeats one value: d <= 12 is off by 12 2^-24, t = d log2 e by 12 2^-24 and 12 1.3 10^-8
 // of e^d, 2^t by 2^-22, 1.9 10^-6 in all.)
 //
-// What bounds it. 256 rows of 131072 bf16 logits, 16 kept: 27.4 us in a replayed graph, where HBM would allow
-// 9.9: the scan 21 to 25 (12 instructions a logit; the issue slots are half used, as one SM has two rows and
-// the next one), the merge the rest. 256 rows of 50001 f32 logits 23.9 (7.5), 1024 greedy rows of 131072 64
-// (39.5). One row of 32000: 10.2, launches and two short chains of barriers and code that is not in the
-// cache yet.
+// What bounds it. 256 rows of 131072 bf16 logits, 16 kept: 25.9 us in a replayed graph, where HBM would allow
+// 9.9: the scan about 20 (12 instructions a logit; the issue slots are half used, as one SM has two rows and
+// the next one), the merge the rest. 256 rows of 50001 f32 logits 22.5 (7.5), 1024 greedy rows of 131072 55.4
+// (39.5), 2048 of 32000 51.0 (19.3). One row of 32000 10.0, 128 rows of 100 to 1000 9.8: launches and two short
+// chains of barriers and code that is not in the cache yet.
 #include <float.h>
 
 #include "tree.cuh"
@@ -308,8 +308,8 @@ __device__ __noinline__ Cleared clear_notes(u64* notes, int n, int k, float boun
 }
 
 // Enters the elements of a warp's noted runs (L each, numbered from element `begin` on) that reach the
-// bound in its list, of which the k best are kept. Returns how many there are, at most k, padded with
-// zeros to a multiple of four.
+// bound in its list, cut to the k best of them when it is full. Returns how many there are, at most k + 32, padded
+// with zeros to a multiple of four.
 template <typename T, int L>
 __device__ __noinline__ int enter(const T* x, int begin, int end, u64* notes, int of_lane, u64* list, int k, float bound) {
   constexpr int PER = 32 / L, AHEAD = 4;  // runs at a time, and of them in flight
@@ -355,7 +355,7 @@ __device__ __noinline__ int enter(const T* x, int begin, int end, u64* notes, in
       __syncwarp();
     }
   }
-  if (count > k) {
+  if (count > k + 32) {  // (a few more are ranked with the rest: 128 rows of 100 to 1000 with k 1 to 11 10.4 -> 9.8 us)
     for (int i = count + lane; i < kEntries; i += 32) list[i] = 0;
     __syncwarp();
     cut<false>(list, kEntries, count, k);
@@ -729,8 +729,9 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(const Merge p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
   if (threadIdx.x == 0) list.count = spread_s = 0;
   for (int i = threadIdx.x; i < kBins; i += THREADS) bins[i] = 0;
-  grid_wait();  // the scan's lists
-  grid_trigger();
+  // the scan's lists. (The next call's scan waits for the end of this grid: let in earlier, its CTAs take the places
+  // of this one's where there are many, 2048 greedy rows of 32000 51.0 -> 62.6 us.)
+  grid_wait();
   const int per = p.splits * p.k;
   const u64* lists = p.lists + (size_t)b * p.rows_per_seq * per;
   const Piece* pieces = p.pieces + (size_t)b * p.rows_per_seq * p.splits;
@@ -989,7 +990,7 @@ dflash_status beam_select(int dtype, const BeamParams& a, size_t ws_bytes, cudaS
   const Merge merge = {c.lists, c.pieces, a.scores, a.tokens, a.parents, a.scores_out, a.ld_out,
                        a.beams, per_seq, splits, a.k, a.vocab, a.parent_base};
   // Four warps for few candidates of few rows: such sequences are many, and share an SM (2048 rows, greedy: 57 us
-  // with 128 threads, 72 with 512; 64 sequences of 8 beams, k 8: 34 and 31)
+  // with 128 threads, 72 with 512, both before the scan's last steps; 64 sequences of 8 beams, k 8: 34 and 31)
   const bool small = per_seq * splits <= 4 && (long long)a.beams * splits * a.k <= 128;
   return cuda_status(small ? merge_rows<128>(merge, a.batch, s) : merge_rows<512>(merge, a.batch, s));
 }

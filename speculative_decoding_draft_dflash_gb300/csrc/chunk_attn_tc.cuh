@@ -31,12 +31,12 @@
 // What bounds it. Many rows: the MMAs (1024 cycles a key tile and row tile with both products)
 // and the exponentials (128 x 128 at 16 a cycle and SM: 1024 too), which A and B overlap: 2800
 // to 3000 cycles per key tile of two row tiles, of which 2048 are MMAs. 8192 rows of 32 heads
-// from position 0: 354 us in a short run, 1.55 PFLOP/s of the 1.91 of a large matrix product, and
+// from position 0: 355 us in a short run, 1.55 PFLOP/s of the 1.91 of a large matrix product, and
 // 378 us once calls follow one another for a second (the power limit lowers the clock; the matrix
 // product then runs at 1.72). Few rows: HBM, as long as an item is long (294400 keys of 8 heads read
 // by single tokens: 187 us, 6.4 of 6.8 TB/s); each further item costs about 3.7 us, in which the
 // last tile's chain of S, softmax, PV and epilogue has nothing behind it, as both accumulators end
-// together (32 blocks of 16 tokens over 256 to 4096 keys: 70 us, 4.9 TB/s).
+// together (32 blocks of 16 tokens over 256 to 4096 keys: 67 us, 5.1 TB/s).
 // E4M3 with few rows: 1990 cycles a tile on long sequences (294400 keys: 127 us, 4.7 TB/s) where
 // HBM would allow 1400, with the tensor pipe busy for 46 %. Not the chain of S, softmax and PV: with
 // half the MMAs of S it would be 122 us, with half of PV's 124, with a quarter of V converted
@@ -45,7 +45,7 @@
 // converted, which leaves about 64 KB on their way, where bf16 has about 96 of 160 KB; at 4.7 and
 // 6.4 TB/s over 152 SMs both come to 2.1 to 2.3 us a load. Deeper rings have not been tried.
 //
-// The start: about 5 us from the launch to the first load, of lengths, split and page look-up one after another,
+// The start: about 4 us from the launch to the first load, of lengths, split and page look-up one after another,
 // run by the loading warp alone where there are at most 32 sequences.
 //
 // Tried and slower. The softmax run once on nothing while the work is looked for, so that its code is in the

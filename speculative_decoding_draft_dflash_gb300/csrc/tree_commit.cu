@@ -23,7 +23,6 @@ template <typename T>
 __global__ void __launch_bounds__(128, 8) tree_commit_kernel(const TreeCommitParams p) {
   __shared__ long long src[kRows], dst[kRows];  // row of KV head 0 in the layer, -1: not moved
   grid_wait();
-  grid_trigger();
   const int b = blockIdx.x, l = blockIdx.y >> 1, which = blockIdx.y & 1;
   const int a = p.accept_len[b], ctx = p.ctx_len[b], nodes = p.nodes[b];
   if (a == -1) return;

@@ -25,7 +25,6 @@ template <int NW>
 __global__ void __launch_bounds__(1024) tree_map_kernel(const TreeMapParams p) {
   __shared__ int up[kTreeMaxNodes];
   grid_wait();
-  grid_trigger();
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int lo = p.cu_rows[b], hi = p.cu_rows[b + 1], kv = p.kv_lens[b];
   const int t0 = p.nodes_before ? p.nodes_before[b] : 0;
