@@ -10,7 +10,7 @@
 // costs its depth in shared-memory latencies, and a chain of thousands of rows stays linear.
 //
 // Bound by latency: 58 to 220 KB of masks are a few hundredths of a microsecond at the copy rate. 32 trees of
-// 64 nodes 3.0 us in a replayed graph, 16 new rows behind 200 to 900 nodes of 64 sequences 2.6 (5.3 and 4.7
+// 64 nodes 2.9 us in a replayed graph, 16 new rows behind 200 to 900 nodes of 64 sequences 2.5 (5.0 and 4.7
 // call by call, which is the host's time): the launch, then three dependent loads (lengths, parents, the
 // masks taken over) and the walk.
 #include "tree.cuh"
