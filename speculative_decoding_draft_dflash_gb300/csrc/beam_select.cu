@@ -34,7 +34,7 @@
 // What bounds it. 256 rows of 131072 bf16 logits, 16 kept: 25.9 us in a replayed graph, where HBM would allow
 // 9.9: the scan about 20 (12 instructions a logit; the issue slots are half used, as one SM has two rows and
 // the next one), the merge the rest. 256 rows of 50001 f32 logits 22.5 (7.5), 1024 greedy rows of 131072 55.4
-// (39.5), 2048 of 32000 51.0 (19.3). One row of 32000 10.0, 128 rows of 100 to 1000 9.8: launches and two short
+// (39.5), 2048 of 32000 51.0 (19.3). One row of 32000 10.0, 128 rows of 100 to 1000 9.6: launches and two short
 // chains of barriers and code that is not in the cache yet.
 #include <float.h>
 
@@ -923,7 +923,9 @@ Cut cut_of(int rows, int beams, int vocab, int k) {
 template <typename T, int J>
 cudaError_t scan_rows(const Scan& p, cudaStream_t s) {
   static SmemLimit limit;
-  cudaError_t e = limit.raise(beam_scan_kernel<T, J>, (int)sizeof(ScanSmem<J>));
+  // all of the memory as shared, as the merge has it: an SM empties before that split changes, and the merge's CTAs,
+  // which are let in early, would wait for that (256 rows of 100 to 1000: 10.3 us, and 16.4 with different splits)
+  cudaError_t e = limit.raise(beam_scan_kernel<T, J>, (int)sizeof(ScanSmem<J>), false, true);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_BEAM_SCAN, s);
   const int slots = kCtas * chunk_sms();
@@ -934,7 +936,7 @@ cudaError_t scan_rows(const Scan& p, cudaStream_t s) {
 template <int THREADS>
 cudaError_t merge_rows(const Merge& p, int batch, cudaStream_t s) {
   static SmemLimit limit;
-  const cudaError_t e = limit.raise(beam_merge_kernel<THREADS>, (int)sizeof(float) * kMostRough);
+  const cudaError_t e = limit.raise(beam_merge_kernel<THREADS>, (int)sizeof(float) * kMostRough, false, true);
   if (e != cudaSuccess) return e;
   LaunchScope ls_(DFLASH_KERNEL_BEAM_MERGE, s);
   return launch_overlapped(beam_merge_kernel<THREADS>, dim3(batch), THREADS, sizeof(float) * (size_t)p.beams * p.splits * p.k,

@@ -57,10 +57,11 @@ struct Carver {
 // test lowered it with dflash_test_wait_limit; dflash_api.cu).
 unsigned long long wait_limit_ns();
 
-// Raises a kernel's dynamic shared-memory limit once per device (and allows clusters of more than eight CTAs).
+// Raises a kernel's dynamic shared-memory limit once per device (and allows clusters of more than eight CTAs; all_shared:
+// has all of an SM's memory split off as shared, so that it can join another such kernel's CTAs there).
 struct SmemLimit {
   unsigned char done[128] = {};
-  template <typename F> cudaError_t raise(F* kernel, int bytes, bool wide_clusters = false) {
+  template <typename F> cudaError_t raise(F* kernel, int bytes, bool wide_clusters = false, bool all_shared = false) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -68,6 +69,8 @@ struct SmemLimit {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && wide_clusters)
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && all_shared)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess && dev >= 0 && dev < 128) __atomic_store_n(&done[dev], 1, __ATOMIC_RELEASE);
     return e;
   }
