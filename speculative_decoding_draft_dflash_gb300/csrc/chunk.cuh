@@ -243,8 +243,8 @@ constexpr size_t kLocateBytes = sizeof(Seq<TREE>) + sizeof(long long);  // per s
 // The KV head and the item of a sequence that hold cost unit `rest` of it; per_head: of one of its heads. By a
 // whole warp.
 template <bool TOKENS, bool TREE>
-__device__ __noinline__ void locate_item(const Split<TOKENS, TREE>& p, const Seq<TREE>& s, long long rest, long long per_head,
-                                            Start<TREE>* st) {
+__device__ __noinline__ void locate_item(const Split<TOKENS, TREE>& p, const Seq<TREE>& s, long long rest,
+                                         long long per_head, Start<TREE>* st) {
   const int lane = threadIdx.x & 31;
   int kvh = 0;
   while (rest >= per_head) {  // (n_kv steps at most)
