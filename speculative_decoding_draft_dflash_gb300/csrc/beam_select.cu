@@ -727,7 +727,10 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(const Merge p) {
   __shared__ int bins[kBins], bin_s;
   __shared__ float top_s[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
-  if (threadIdx.x == 0) list.count = spread_s = 0;
+  if (threadIdx.x == 0) {
+    list.count = spread_s = 0;
+    bin_s = kBins - 1;  // (no threshold)
+  }
   for (int i = threadIdx.x; i < kBins; i += THREADS) bins[i] = 0;
   // the scan's lists. (The next call's scan waits for the end of this grid: let in earlier, its CTAs take the places
   // of this one's where there are many, 2048 greedy rows of 32000 51.0 -> 62.6 us.)
@@ -822,7 +825,7 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(const Merge p) {
         const int u = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += u;
       }
-      const int l = __ffs(__ballot_sync(0xffffffffu, upto >= p.k)) - 1;  // (there are k candidates)
+      const int l = __ffs(__ballot_sync(0xffffffffu, upto >= p.k)) - 1;  // (none, were there fewer than k candidates)
       if (lane == l) {
         int have = upto - mine, i = 0;
         while (i < kBins / 32 - 1 && have + n[i] < p.k) have += n[i++];
@@ -889,6 +892,13 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(const Merge p) {
     p.tokens[at] = (int)(place - (uint32_t)beam * (uint32_t)p.vocab);
     if (p.parents) p.parents[at] = p.parent_base + beam;
     if (p.scores_out) p.scores_out[at] = (float)score_of(score);
+  }
+  // The lists hold k candidates of a sequence; were there fewer, what the buffers held would still be no token
+  for (int r = n + threadIdx.x; r < p.k; r += THREADS) {
+    const size_t at = (size_t)b * p.ld_out + r;
+    p.tokens[at] = 0;
+    if (p.parents) p.parents[at] = p.parent_base;
+    if (p.scores_out) p.scores_out[at] = -INFINITY;
   }
 }
 
