@@ -16,7 +16,8 @@
 // maximum and number, for itself; the elements of noted runs are looked at one by one at the end, against the
 // bound of all tiles, of a few runs of a warp. A lane whose notes are full has the bound looked at again, and
 // where that does not help (rows of equal or of ascending logits) the warp keeps the k runs of the largest
-// maxima: each of the others has k elements before all of its own. (Elements taken as they came, or a list of a
+// maxima, of equal ones the first: each of the others has k elements before all of its own. From then on a run
+// is noted only above the least of these, which themselves stay candidates. (Elements taken as they came, or a list of a
 // warp's, cost more than the sums: what a warp does beside them waits for votes, shuffles and instructions
 // that are not in the cache.)
 //
@@ -280,10 +281,11 @@ __device__ __noinline__ u64 cut(u64* e, int slots, int n, int k) {
 }
 
 // A warp's notes, one lane's below one another: drops those below the bound and, if a lane is still full,
-// all but the k best, which it spreads over the lanes. Returns a bound for what comes later and the
-// lane's notes.
+// all but the k best, which it spreads over the lanes. Returns a bound that these reach, the least that a later
+// run has to have, which is above it (of equal maxima the first runs are kept, and later ones have k elements
+// before all of theirs), and the lane's notes.
 struct Cleared {
-  float bound;
+  float bound, later;
   int of_lane;
 };
 __device__ __noinline__ Cleared clear_notes(u64* notes, int n, int k, float bound) {
@@ -295,16 +297,17 @@ __device__ __noinline__ Cleared clear_notes(u64* notes, int n, int k, float boun
     const u64 note = notes[32 * i + lane];
     if ((uint32_t)(note >> 32) >= reach) notes[32 * kept++ + lane] = note;
   }
-  if (!__any_sync(0xffffffffu, kept == kSlots)) return {bound, kept};
+  if (!__any_sync(0xffffffffu, kept == kSlots)) return {bound, bound, kept};
 #pragma unroll 1
   for (int i = kept; i < kSlots; ++i) notes[32 * i + lane] = 0;
   const int all = __reduce_add_sync(0xffffffffu, kept);
   __syncwarp();
-  float later = bound;
   const int left = min(all, k);
   const u64 least = cut<true>(notes, 32 * kSlots, all, left);  // (spread over the lanes, even if all of them stay)
-  if (all > k) later = fmaxf(bound, float_of((uint32_t)(least >> 32) + 1));
-  return {later, left > lane ? (left - lane + 31) / 32 : 0};
+  const int of_lane = left > lane ? (left - lane + 31) / 32 : 0;
+  if (all <= k) return {bound, bound, of_lane};
+  const uint32_t reached = (uint32_t)(least >> 32);
+  return {fmaxf(bound, float_of(reached)), fmaxf(bound, float_of(reached + 1)), of_lane};
 }
 
 // Enters the elements of a warp's noted runs (L each, numbered from element `begin` on) that reach the
@@ -506,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 3) beam_scan_kernel(const Scan p) {
     typename Vec<T>::Most best = Vec<T>::kNone;  // this lane's largest so far
     float ref = -INFINITY, far = 0.f;            // far: beyond it the reference has to move
     float bound = 0.f;                           // what is below it is no candidate
+    float noting = 0.f;                          // what a run has to reach to be noted: the bound, or above it
     float sum = 0.f, low = 0.f;                  // sum + low
     auto publish = [&]() {
       const float v = warp < voters ? nth_lane(Vec<T>::value(best), q) : -INFINITY;
@@ -549,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 3) beam_scan_kernel(const Scan p) {
         const float v = warp_max(most);
         if (lane == 0) wmax[warp] = v;
         __syncthreads();
-        bound = nth_of(wbound, voters, nth);
+        noting = bound = nth_of(wbound, voters, nth);
         ref = wmax[0];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) ref = fmaxf(ref, wmax[w]);
@@ -559,16 +563,18 @@ __global__ void __launch_bounds__(kThreads, 3) beam_scan_kernel(const Scan p) {
         publish();
         __syncwarp();
         bound = fmaxf(bound, nth_of(wbound, voters, nth));
+        noting = fmaxf(noting, bound);
         due = 2 * due + 2;
       }
       ++seen;
-      if (most >= bound && run > 0) notes[32 * noted++ + lane] = entry_of(most, (base - begin) / L + threadIdx.x);
+      if (most >= noting && run > 0) notes[32 * noted++ + lane] = entry_of(most, (base - begin) / L + threadIdx.x);
       if (__any_sync(0xffffffffu, noted == kSlots || most > far || most == INFINITY)) {
         if (__any_sync(0xffffffffu, noted == kSlots)) {
           publish();
           __syncwarp();
           const Cleared c = clear_notes(notes, noted, p.k, fmaxf(bound, nth_of(wbound, voters, nth)));
           bound = c.bound;
+          noting = fmaxf(noting, c.later);
           noted = c.of_lane;
         }
         // ---- the reference

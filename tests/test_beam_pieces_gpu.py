@@ -11,6 +11,9 @@ from test_chunk_gpu import DEV, D  # noqa: F401  (D is the fixture)
 pytestmark = pytest.mark.gpu
 
 INF = float("inf")
+TILE = {"f32": 4096, "bf16": 8192}  # elements of a tile
+# (a row in one piece of 16, 8 and 13 tiles)
+ROWS = [("bf16", 256, 131072), ("f32", 256, 32000), ("f32", 256, 50001)]
 
 
 def expect(logits, scores, k):
@@ -26,11 +29,28 @@ def expect(logits, scores, k):
 
 
 def check(D, logits, scores, k, base=0):
-    """Every place is written (the buffers held -9), with what float64 gives."""
+    """Every place is written (the buffers held -9), with what float64 gives. Beams with rows of their own may change
+    places where their scores are nearer than the errors of their two log-sums: each is within 2 10^-6, so that
+    the order of the scores is sure from 4 10^-6 on ("high in one lane": rows that differ in noise, 10^-13 of their
+    sums). The tokens of one beam keep their order."""
+    batch, beams, vocab = logits.shape
     got = select(D, logits, scores, k, base)
     tok, par, want = expect(logits, scores, k)
-    assert torch.equal(got[0].long(), tok)
-    assert torch.equal(got[1].long(), par + base)
+    t, i = got[0].long(), got[1].long() - base
+    if beams > 1 and logits.stride(1) != 0 and not (torch.equal(t, tok) and torch.equal(i, par)):
+        assert ((t >= 0) & (t < vocab) & (i >= 0) & (i < beams)).all()
+        whole = expect(logits, scores, beams * k)            # (k of a beam are among them, or minus infinity)
+        for b in (~((t == tok) & (i == par)).all(1)).nonzero().flatten().tolist():
+            ranked = list(zip(whole[1][b].tolist(), whole[0][b].tolist()))
+            score = dict(zip(ranked, whole[2][b]))
+            mine = list(zip(i[b].tolist(), t[b].tolist()))
+            for j, (place, v) in enumerate(zip(mine, want[b])):
+                assert place == ranked[j] or (place[0] != ranked[j][0] and abs(score[place] - v) <= 4e-6), (b, j)
+            for beam in range(beams):
+                own = [p for p in mine if p[0] == beam]
+                assert own == [p for p in ranked if p[0] == beam][:len(own)], (b, beam)
+    else:
+        assert torch.equal(t, tok) and torch.equal(i, par)
     out, fin = np64(got[2]), np.isfinite(want)
     assert (np.isneginf(out) == ~fin).all()
     assert (np.abs(out[fin] - want[fin]) <= T.beam_bound(want[fin])).all()
@@ -56,3 +76,75 @@ def test_one_token_allowed_a_beam_keeps_every_beam(D, dtype, batch, beams, vocab
     assert (np.abs(np64(out[:, :beams]) - v[:, :beams]) <= T.beam_bound(v[:, :beams])).all()
     assert (out[:, beams:] == -INF).all()
     assert ((tok >= 0) & (tok < vocab)).all() and ((par >= 3) & (par < 3 + beams)).all()
+
+
+def high_in_one_lane(x, tile):
+    """Falling logits in the same lane's run of every tile, so that this lane alone has notes to spare; the last
+    of them have bare mantissas."""
+    x[..., 5::tile] = 39.0 - torch.arange(len(range(5, x.shape[-1], tile)), dtype=torch.float32)
+    x[..., 70] = 15.0
+
+
+KINDS = {
+    "equal": lambda x, tile: x.fill_(-2.5),
+    "zeros": lambda x, tile: x.zero_(),
+    "three values": lambda x, tile: x.copy_((x > 1.0).float() - (x < -1.0).float()),
+    "clipped": lambda x, tile: x.clamp_(-3.0, 3.0),                            # (1.5 standard deviations)
+    "clipped at 2": lambda x, tile: x.clamp_(-4.0, 4.0),
+    "one top value": lambda x, tile: x[..., ::11].fill_(20.0),                 # 3000 to 12000 elements
+    "top behind": lambda x, tile: x[..., x.shape[-1] // 2:].fill_(11.0),
+    "rounded": lambda x, tile: x.round_(),
+    "high in one lane": high_in_one_lane,
+    "ascending in steps": lambda x, tile: x.copy_((torch.arange(x.shape[-1]) // 700).float() * 0.125),
+}
+
+
+@pytest.mark.parametrize("dtype,batch,vocab", ROWS)
+@pytest.mark.parametrize("kind", KINDS)
+def test_rows_with_more_notes_than_a_lane_holds(D, dtype, batch, vocab, kind):
+    g = torch.Generator().manual_seed(21)
+    x = torch.randn((4, 1, vocab), generator=g) * 2
+    KINDS[kind](x, TILE[dtype])
+    x = x.to(DEV, TORCH[dtype]).repeat(batch // 4, 1, 1)
+    for k in (1, 8, 16, 128):
+        check(D, x, None, k)
+    s = torch.linspace(-1, 0, batch, device=DEV).view(-1, 4)                    # as four beams of a sequence
+    s[:, 2] = s[:, 1]
+    check(D, x.view(-1, 4, vocab), s.contiguous(), 8, base=1)
+
+
+@pytest.mark.parametrize("dtype,batch,vocab", ROWS)
+@pytest.mark.parametrize("n", [1, 5, 40])
+@pytest.mark.parametrize("lowest", [False, True])
+def test_rows_masked_to_a_few_tokens(D, dtype, batch, vocab, n, lowest):
+    """Fewer allowed tokens than asked for: the lowest of the others follow."""
+    x, s = allowed(dtype, batch, 1, vocab, n, torch.finfo(TORCH[dtype]).min if lowest else -INF)
+    for k in (1, 8, 128):
+        check(D, x, s, k)
+    check(D, x.view(-1, 8, vocab), s.view(-1, 8), 16)
+
+
+def test_one_token_allowed_a_beam(D):
+    for dtype, batch, beams, vocab, k in [("bf16", 32, 8, 131072, 16), ("f32", 64, 4, 50001, 8)]:
+        x, s = allowed(dtype, batch, beams, vocab, 1, -INF)
+        check(D, x, s, k)
+
+
+@pytest.mark.parametrize("dtype,vocab", [("bf16", 131072), ("bf16", 65601), ("f32", 50001)])
+def test_a_row_for_all_beams_of_many_sequences(D, dtype, vocab):
+    """A level of as many trees, masked and clipped."""
+    for kind in ("clipped", "high in one lane", "zeros"):
+        x = torch.randn((4, 1, vocab), generator=torch.Generator().manual_seed(5)) * 2
+        KINDS[kind](x, TILE[dtype])
+        x = x.to(DEV, TORCH[dtype]).repeat(64, 1, 1)
+        s = -4 * torch.rand((256, 3), generator=torch.Generator().manual_seed(6)).to(DEV)
+        check(D, x.expand(256, 3, vocab), s, 20)
+    x, _ = allowed(dtype, 256, 1, vocab, 5, -INF)
+    check(D, x.expand(256, 3, vocab), s, 20)
+
+
+def test_the_same_bits_again_where_notes_fill_up(D):
+    x = (torch.randn((256, 1, 131072), generator=torch.Generator().manual_seed(8)) * 2).clamp(-3, 3).to(DEV, torch.bfloat16)
+    want = select(D, x, None, 16)
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(select(D, x, None, 16), want))
