@@ -645,7 +645,8 @@ __global__ void __launch_bounds__(kThreads, 3) beam_scan_kernel(const Scan p) {
       if (mine != top && mine != -INFINITY) {
         const float2 w = exp_pair(fmaxf(mine - top, -80.f));
         const float q = v.x * w.x;
-        v = mine - top < -80.f ? make_float2(0.f, 0.f) : make_float2(q, fmaf(v.x, w.x, -q) + (v.x * w.y + v.y * w.x));
+        // (0 times the sum, so that NaN stays the mark of its row)
+        v = mine - top < -80.f ? make_float2(0.f * v.x, 0.f) : make_float2(q, fmaf(v.x, w.x, -q) + (v.x * w.y + v.y * w.x));
       }
       v = sum_lanes(v);
       if (lane == 0) p.pieces[piece] = {(double)v.x + (double)v.y, top, 0};

@@ -148,3 +148,15 @@ def test_the_same_bits_again_where_notes_fill_up(D):
     want = select(D, x, None, 16)
     for _ in range(20):
         assert all(torch.equal(a, b) for a, b in zip(select(D, x, None, 16), want))
+
+
+@pytest.mark.parametrize("dtype,batch,vocab", ROWS + [("bf16", 6, 131072), ("f32", 3, 50001)])
+@pytest.mark.parametrize("nan,high,value", [(5, 31000, 200.0), (5, 31000, 90.0), (31990, 70, 300.0), (20000, 31000, 81.0)])
+def test_rows_with_nan_next_to_a_much_larger_logit(D, dtype, batch, vocab, nan, high, value):
+    """The row has no probability, however far above the NaN's neighbours another logit lies. In the larger
+    calls a row is one piece, in the others several."""
+    x = (torch.randn((batch, 1, vocab), generator=torch.Generator().manual_seed(9)) * 2).to(DEV, TORCH[dtype])
+    x[::2, :, nan] = float("nan")
+    x[:, :, high] = value
+    for k in (1, 8):
+        check(D, x, None, k)
