@@ -566,7 +566,8 @@ dflash_status dflash_tree_attn(const dflash_dims* dims, const dflash_kv_cache* c
  *   next_anchor[b]  posterior at the path's last node
  * A sequence without rows, or refused (kv_lens[b] <= 0): a = -1, no path, anchor -1; the same for rows that
  * are not a valid range (DFLASH_DEV_ROWS).
- *   parents, tokens, posterior  device int32 [rows]; ctx_len int32 [batch], may be ctx_next
+ *   parents, tokens, posterior  device int32 [rows]; ctx_len int32 [batch], may be ctx_next (not where
+ *         dflash_tree_commit follows, which needs ctx_len as it was before)
  *   path  device int32 [batch][max_path]; next_cu_rows [batch + 1]; the others [batch]
  * Reads chunk->cu_rows and kv_lens. Unsupported: more than 8192 sequences.
  */
@@ -583,9 +584,11 @@ dflash_status dflash_tree_accept(const dflash_chunk* chunk, const int32_t* paren
  * accept_len -1 leaves a sequence as it is. A path that does not ascend within 0 .. nodes[b]-1, or
  * has a >= max_path, or nodes that reach beyond the capacity: DFLASH_DEV_TREE, the sequence is left as it
  * is. A page id outside the pool sets DFLASH_DEV_PAGE and the rows in it are not moved.
- *   ctx_len, accept_len  device int32 [batch]; path device int32 [batch][max_path]
- * Reads tree->nodes only. Host errors as for the other calls of the cache; unsupported: more than 4096
- * sequences or 32767 layers.
+ *   ctx_len, accept_len  device int32 [batch]; path device int32 [batch][max_path]. ctx_len holds the committed
+ *         rows under the tree, as given to dflash_tree_accept: not its ctx_next, behind which there is another
+ *         row of the cache than the path's (no check can tell the two apart)
+ * Reads tree->nodes only. Host errors as for the other calls of the cache, and an input that overlaps the cache's
+ * lengths (they are written meanwhile); unsupported: more than 4096 sequences or 32767 layers.
  */
 dflash_status dflash_tree_commit(const dflash_dims* dims, const dflash_kv_cache* cache, const dflash_tree* tree,
                                  const int32_t* ctx_len, const int32_t* path, int max_path,

@@ -100,6 +100,14 @@ DFLASH_API dflash_status dflash_tree_commit(const dflash_dims* d, const dflash_k
   if (st != DFLASH_OK) return st;
   if (max_path <= 0 || !aligned4(ctx_len) || !aligned4(path) || !aligned4(accept_len)) return DFLASH_ERR_INVALID_ARG;
   if (c->n_layers > 32767) return DFLASH_ERR_UNSUPPORTED;  // (two grid rows a layer)
+  // the lengths are written while other CTAs read these
+  const size_t n = (size_t)c->batch;
+  auto in_lens = [&](const int32_t* a, size_t m) {
+    const uintptr_t lo = (uintptr_t)a, from = (uintptr_t)c->lens;
+    return lo < from + 4 * n * c->n_layers && from < lo + 4 * m;
+  };
+  if (in_lens(ctx_len, n) || in_lens(accept_len, n) || in_lens(tree->nodes, n) || in_lens(path, n * max_path))
+    return DFLASH_ERR_INVALID_ARG;
   TreeCommitParams p;
   memset(&p, 0, sizeof(p));
   p.status = status_word();

@@ -660,7 +660,8 @@ def dflash_tree_attn(dims, cache, layer, plan, tree, q, sliding_window, scaling,
 
 def dflash_tree_accept(plan, parents, tokens, posterior, ctx_len, accept_len, path, next_cu_rows,
                        ctx_next, next_anchor, stream=None):
-    """The accepted path of every sequence's tree; path is int32 [batch][max_path]."""
+    """The accepted path of every sequence's tree; path is int32 [batch][max_path]. ctx_next may be ctx_len, but not
+    where dflash_tree_commit follows, which needs ctx_len as it was before."""
     dev, rows, batch = plan.device, plan.rows, plan.batch
     _on_current("chunk plan", dev)
     shape = path.shape
@@ -677,7 +678,8 @@ _ACCEPT = ("parents", "tokens", "posterior", "ctx_len", "path", "accept_len", "n
 
 
 def dflash_tree_commit(dims, cache, tree, ctx_len, path, accept_len, stream=None):
-    """Moves the accepted paths' rows behind the committed ones, in every layer, and sets lengths."""
+    """Moves the accepted paths' rows behind the committed ones, in every layer, and sets lengths. ctx_len as given
+    to dflash_tree_accept (not its ctx_next), in an array that is not part of the cache's lengths."""
     desc, dev = _desc(dims, cache), tree.device
     _on_current("tree", dev)
     if tree.batch != desc.batch:

@@ -100,6 +100,16 @@ def test_commit_refuses(D):
     assert _commit(D, cache=_cache(D, n_layers=32768)) == UNSUPPORTED
 
 
+def test_commit_refuses_inputs_that_are_the_lengths(D):
+    """2 layers of 4 sequences from 1024 on: 32 bytes, which the call writes while it reads the others."""
+    cache = _cache(D, lens=1024, block_table=4096)
+    for at in (1024, 1040, 1052, 1012):
+        for name in ("ctx_len", "accept_len", "path"):
+            assert _commit(D, cache=cache, **{name: at}) == INVALID, (name, at)
+        assert _commit(D, cache=cache, tree=_tree(D, nodes=at)) == INVALID, at
+    assert _commit(D, cache=cache, path=1024 - 4 * 4 * 8 + 4) == INVALID     # (its last element)
+
+
 def _select(D, dtype=1, **kw):
     a = dict(logits=4096, ld_seq=1000, ld_beam=100, scores=64, batch=2, beams=4, vocab=100, k=8, base=0, tokens=128,
              parents=192, out=256, ld_out=8, ws=65536, wsb=1 << 30)
