@@ -454,10 +454,11 @@ __device__ __noinline__ void repair(const Params<TREE>& p, const Item<TREE>& it,
     } else {
       row = ((long long)it.w.b * p.split.n_kv + it.w.kvh) * p.split.capacity + k;
     }
+    [[maybe_unused]] uint4 m;  // TREE: keys that the row sees
+    if constexpr (TREE) m = chunk::tree_bits(p.tree, it.w.b, pos - it.w.ctx, it.w.ctx, k, p.split.window);
 #pragma unroll 1
     for (int e = 0; e < TK; ++e) {
       if constexpr (TREE) {
-        const uint4 m = chunk::tree_bits(p.tree, it.w.b, pos - it.w.ctx, it.w.ctx, k, p.split.window);
         if (((e < 32 ? m.x : e < 64 ? m.y : e < 96 ? m.z : m.w) >> (e & 31) & 1) == 0) continue;
       } else {
         if (k + e > pos || (p.split.window > 0 && pos - (k + e) >= p.split.window)) continue;

@@ -951,3 +951,40 @@ def test_attn_any_number_of_sequences(D, kv, batch):
     for b in refused:
         assert (out[int(s.cu[b]):int(s.cu[b + 1])] == 0).all()
     assert D.dflash_status_get() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_attn_hidden_keys_of_a_window(D, kv):
+    """A value that is not finite behind chains of 128 nodes: with a window too, only the rows that see it are not
+    finite, and the masks are not looked up key by key (a window takes keys away; it took 2.6 times as long)."""
+    n, ctx, B, bad = 128, 1000, 8, 100
+    s = TreeStep(D, kv, (32, 8, 128), [ctx] * B, [0] * B, [n] * B, seed=3, max_nodes=n)
+    s.parents = i32([i - 1 for _ in range(B) for i in range(n)])
+    s.map(), s.tree_map()
+    q = torch.empty((s.M, s.n_h * s.d), dtype=s.q.dtype, device=DEV)
+    s.append(q)
+    clean, out, took = {}, torch.empty_like(q), {}
+    for window in (0, 20):
+        clean[window] = torch.empty_like(q)
+        s.tree_attn(q, clean[window], window)
+    for b in range(B):
+        K, V = (s.cache.rows(w, 0, b, 0, ctx + n, codes=True).clone() for w in "kv")
+        if kv == "fp8":
+            K, V = (x.to(torch.float8_e4m3fn).view(torch.uint8) for x in (K, V))
+        V[:, ctx + bad] = 0x7F if kv == "fp8" else float("nan")
+        s.cache.set_rows(0, b, K, V)
+    for window in (0, 20):
+        times = []
+        for _ in range(9):
+            at = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            at[0].record()
+            s.tree_attn(q, out, window)
+            at[1].record()
+            torch.cuda.synchronize()
+            times.append(at[0].elapsed_time(at[1]))
+        took[window] = sorted(times)[4]
+        o, c = out.view(B, n, -1), clean[window].view(B, n, -1)
+        sees = torch.tensor([t >= bad and (not window or t - bad < window) for t in range(n)], device=DEV)
+        assert o[:, sees].isnan().all() and torch.equal(o[:, ~sees], c[:, ~sees])
+    assert D.dflash_status_get() == 0
+    assert took[20] < 1.5 * took[0], took
