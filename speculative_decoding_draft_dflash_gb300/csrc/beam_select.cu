@@ -925,7 +925,9 @@ Cut cut_of(int rows, int beams, int vocab, int k) {
   const int slots = kCtas * chunk_sms(), units = (vocab + UNIT - 1) / UNIT, fit = kMostRough / 2 / (beams * k);
   Cut best = {1, units * UNIT};
   double least = 1e300;
-  for (int s = 1; s <= units && (s == 1 || s <= fit) && (long long)rows * (s - 1) < 8LL * slots; ++s) {
+  // Every s that makes other pieces: the first of those that cut a row into pieces of `per` units (2 sqrt(units) of
+  // them at most, as an s takes 10 ns of each call's host time; all s of 2^24 logits: 20 us)
+  for (int s = 1; (s == 1 || s <= fit) && (long long)rows * (s - 1) < 8LL * slots;) {
     const int per = (units + s - 1) / s, n = (units + per - 1) / per;
     const long long turns = ((long long)rows * n + slots - 1) / slots;
     const double cost = (double)turns * (per + 27) + (double)beams * n * k / 128.;
@@ -933,6 +935,8 @@ Cut cut_of(int rows, int beams, int vocab, int k) {
       least = cost;
       best = {n, per * UNIT};
     }
+    if (per == 1) break;
+    s = (units + per - 2) / (per - 1);
   }
   return best;
 }

@@ -159,3 +159,49 @@ def test_binding_refuses_host_and_mismatched_tensors(D):
     for bad in (t.float(), t[:1], t[:, :2], t.t().contiguous().t(), t[0]):
         with pytest.raises(ValueError, match="tokens"):
             D._k_rows(bad, "tokens", i32, 2, 3, -1)
+
+
+def _beam_bytes(batch, beams, vocab, k, sms):
+    """The selection's workspace, with every number of pieces of a row tried: the least of turns of CTAs x (units of a
+    piece + 27) + candidates / 128, of equal ones the fewest pieces."""
+    slots, units, fit = 3 * sms, -(-vocab // 2048), 8192 // (beams * k)
+
+    def pieces(rows):
+        cost = {}
+        for s in range(1, units + 1):
+            if (s > 1 and s > fit) or rows * (s - 1) >= 8 * slots:
+                break
+            per = -(-units // s)
+            n = -(-units // per)
+            cost.setdefault(-(-rows * n // slots) * (per + 27) + beams * n * k / 128, n)
+        return rows * cost[min(cost)]
+
+    most = max(pieces(batch * beams), pieces(batch))
+    return sum(-(-most * size // 256) * 256 for size in (8 * k, 16))
+
+
+def test_select_cuts_rows_at_the_least_cost_in_little_host_time(D):
+    """Few rows of a long vocabulary may have thousands of pieces: not every number of them is tried in a call (it took
+    13 times as long for a row of 2^24 as for one of 131072)."""
+    import random
+    import time
+
+    r = random.Random(3)
+    sizes = [(1, 1, 1, 1), (1, 1, 2 ** 24, 1), (3, 128, 5 * 10 ** 6, 128), (1, 1, 2 ** 28, 1), (1, 1, 2 ** 28 - 2047, 2)]
+    for _ in range(300):
+        beams = r.choice((1, 1, 2, 5, 8, 33))
+        vocab = int(2 ** r.uniform(0, 23))
+        sizes.append((int(2 ** r.uniform(0, 9)), beams, vocab, min(r.choice((1, 2, 8, 50, 128)), beams * vocab)))
+    for size in sizes:
+        got = D.dflash_beam_workspace_bytes(*size)
+        assert got in (_beam_bytes(*size, 148), _beam_bytes(*size, 152)), size   # (148: no device to ask)
+
+    def best(*size):
+        took = []
+        for _ in range(200):
+            t = time.perf_counter()
+            D.dflash_beam_workspace_bytes(*size)
+            took.append(time.perf_counter() - t)
+        return min(took)
+
+    assert best(1, 1, 2 ** 24, 1) < 6 * best(1, 1, 131072, 1)
