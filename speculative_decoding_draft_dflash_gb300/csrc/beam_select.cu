@@ -674,18 +674,25 @@ __device__ __forceinline__ double score_of(u64 k) {
   return __longlong_as_double((long long)(k ^ ((k >> 63) ? 1ull << 63 : ~0ull)));
 }
 
-// A sequence's ranked candidates: the score's order, then the lowest place.
+// A sequence's ranked candidates: the score's order, then the beam, the logit's order and the token. (With the logit,
+// as 64 bits do not tell all scores of a beam apart: logits of 10^-20, or next to a score of 10^30. The candidates of
+// one piece would be its largest logits then, and those of several the first pieces'.)
 struct Ranked {
   u64 score[kMergeCap];
-  uint32_t place[kMergeCap];  // beam * vocab + token
+  u64 place[kMergeCap];  // lowest first: beam, logit, largest first, token
   int count;
 };
+// A place: the token in `bits` bits, 32 of the logit above them. (Beams x vocabulary is below 2^31, so that a beam has
+// 32 - bits.)
+__device__ __forceinline__ u64 place_of(uint32_t beam, uint32_t order, uint32_t token, int bits) {
+  return ((u64)beam << 32 | (0xffffffffu - order)) << bits | token;
+}
 
 constexpr int kMostRough = 16384;  // candidates of a sequence (kBeamMax beams of as many)
 constexpr int kBins = 256, kFirstBin = 117 << 3;  // distances from 2^-10 to 2^22
 
 // Entry i's place among n by `parts` neighbouring lanes (a power of two), all of which get it.
-__device__ __forceinline__ int rank_of(const Ranked& l, int n, u64 score, uint32_t place, int parts) {
+__device__ __forceinline__ int rank_of(const Ranked& l, int n, u64 score, u64 place, int parts) {
   int rank = 0;
 #pragma unroll 4
   for (int j = threadIdx.x & (parts - 1); j < n; j += parts)
@@ -699,7 +706,7 @@ template <int THREADS>
 __device__ __noinline__ void cut_ranked(Ranked& l, int k) {
   const int n = min(l.count, kMergeCap);
   u64 mine[kMergeCap / THREADS];
-  uint32_t at[kMergeCap / THREADS];
+  u64 at[kMergeCap / THREADS];
   int rank[kMergeCap / THREADS];
 #pragma unroll
   for (int t = 0; t < kMergeCap / THREADS; ++t) {
@@ -846,25 +853,25 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(const Merge p) {
   const float slack = (2.f * __int_as_float(spread_s) + fabsf(bound) + fabsf(top)) * 9.6e-7f;
   if (bound != -INFINITY) bound -= slack;
   // ---- exact scores of what reaches it
-  u64 least = 0;
-  uint32_t least_place = 0xffffffffu;
+  const int bits = 32 - __clz(p.vocab - 1);  // of a token
+  u64 least = 0, least_place = ~0ull;
   for (int base = 0; base < total; base += THREADS) {
     const int c = base + threadIdx.x;
     bool todo = c < total && rough[c] >= bound;
-    u64 key = 0;
-    uint32_t place = 0;
+    u64 key = 0, place = 0;
     if (todo) {
       const int beam = beam_of(c), i = c - beam * per, r = p.rows_per_seq == 1 ? 0 : beam;
       const float s = beam_s[beam].x;
       double score = -INFINITY;
-      uint32_t token = i;
+      uint32_t token = i, order = 0;
       if (!isnan(s)) {
         const u64 e = lists[r == beam ? c : i];
         token = token_of(e);
+        order = (uint32_t)(e >> 32);
         score = (double)s + (((double)logit_of(e) - shift[r]) - lse[r]);
       }
       key = order_of(score);
-      place = (uint32_t)beam * (uint32_t)p.vocab + token;
+      place = place_of(beam, order, token, bits);
     }
     bool more;
     do {
@@ -891,13 +898,12 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(const Merge p) {
   while (2 * parts * n <= THREADS && parts < 8) parts *= 2;
   for (int i = threadIdx.x / parts; i < (n + 31) / 32 * 32; i += THREADS / parts) {
     const u64 score = i < n ? list.score[i] : 0;
-    const uint32_t place = i < n ? list.place[i] : 0;
+    const u64 place = i < n ? list.place[i] : 0;
     const int r = rank_of(list, n, score, place, parts);
     if (i >= n || r >= p.k || (threadIdx.x & (parts - 1)) != 0) continue;
-    const int beam = (int)(place / (uint32_t)p.vocab);
     const size_t at = (size_t)b * p.ld_out + r;
-    p.tokens[at] = (int)(place - (uint32_t)beam * (uint32_t)p.vocab);
-    if (p.parents) p.parents[at] = p.parent_base + beam;
+    p.tokens[at] = (int)(place & ((1ull << bits) - 1));
+    if (p.parents) p.parents[at] = p.parent_base + (int)(place >> (32 + bits));
     if (p.scores_out) p.scores_out[at] = (float)score_of(score);
   }
   // The lists hold k candidates of a sequence; were there fewer, what the buffers held would still be no token

@@ -160,3 +160,27 @@ def test_rows_with_nan_next_to_a_much_larger_logit(D, dtype, batch, vocab, nan, 
     x[:, :, high] = value
     for k in (1, 8):
         check(D, x, None, k)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("batch,vocab", [(1, 131072), (2, 50001), (40, 20000), (256, 65601), (3, 700)])
+def test_scores_that_64_bits_do_not_tell_apart(D, dtype, batch, vocab):
+    """Tiny logits, and logits next to a far larger score or logit: a beam's tokens still come in the order of their
+    logits, equal ones lowest first, in however many pieces its row is."""
+    g = torch.Generator().manual_seed(12)
+    noise = torch.randn((batch, 1, vocab), generator=g)
+    tiny, far = (noise * 1e-20).to(DEV, TORCH[dtype]), noise.to(DEV, TORCH[dtype])
+    spiked = far.clone()
+    spiked[..., vocab // 3] = 3e38
+    s = torch.full((batch, 1), -1e30, device=DEV)
+    for x, scores in ((tiny, None), (far, s), (spiked, None), (tiny, s)):
+        rank = torch.sort(x[:, 0].double(), dim=1, descending=True, stable=True)[1]
+        for k in (1, 8, 100):
+            tok, par, _ = select(D, x, scores, k, base=2)
+            assert torch.equal(tok.long(), rank[:, :k]) and (par == 2).all()
+    # two beams alike: the first one's tokens, in order, before the second one's
+    two = tiny.expand(batch, 2, vocab)
+    for x in (two, two.contiguous()):
+        tok, par, _ = select(D, x, torch.cat((s, s), 1), 60)
+        assert (par == 0).all() and torch.equal(tok.long(), torch.sort(tiny[:, 0].double(), dim=1, descending=True,
+                                                                        stable=True)[1][:, :60])
